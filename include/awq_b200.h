@@ -266,6 +266,83 @@ awq_status_t awq_linear_w4a16_batch(const awq_linear_desc_t *descs, int n, int64
                                     int group_size, void *stream);
 
 /*
+ * awq_gated_w4a16 — the gated feed-forward's first half on a packed layer: with
+ * (g | u) = (x / s16) * dequant(W)^T, W the joint gate and up matrix [2F, in]
+ * (gate rows first; the two share s_X and are searched and packed jointly),
+ *     h[m, f] = act(g[m, f]) * u[m, f].
+ * act: AWQ_ACT_SILU g * sigmoid(g), AWQ_ACT_GELU g * Phi(g), AWQ_ACT_GELU_TANH its
+ * tanh form.  x : [M, in] bf16 device; h : [M, F] bf16 device, written.
+ * Storage arguments as awq_linear_w4a16 with out = 2F; any F >= 1, M <= 2^20,
+ * in <= 49152.  g and u are held in fp32 and rounded nowhere before h.
+ * Precision of the operands: x / s16 is rounded to fp16 after a power-of-two
+ * scale per token, (code - z) * scale once to fp16 after one per layer.
+ * h must not overlap any input.  Asynchronous.
+ */
+typedef enum { AWQ_ACT_SILU = 0, AWQ_ACT_GELU = 1, AWQ_ACT_GELU_TANH = 2 } awq_act_t;
+
+awq_status_t awq_gated_w4a16(const uint16_t *x, int64_t M, int64_t in, int64_t F,
+                             const uint32_t *qweight, const uint16_t *scales,
+                             const uint32_t *zeros, const uint16_t *s16, int group_size,
+                             int act, uint16_t *h, void *stream);
+
+/*
+ * awq_gated_w4a16_grad — the gradient of awq_gated_w4a16 with respect to x, the
+ * packed weights frozen.  g and u are computed again from x, then
+ *     dg = dh * u * act'(g),  du = dh * act(g),  dx = ([dg | du] * dequant(W)) / s16.
+ * dh : [M, F] bf16 device;  dx : [M, in] bf16 device, written.  Other arguments as
+ * awq_gated_w4a16.  dg and du are rounded to fp16 after a power-of-two scale per
+ * token.  A token's gradient depends on that token's rows alone.
+ * dx must not overlap any input.  Asynchronous.
+ */
+awq_status_t awq_gated_w4a16_grad(const uint16_t *dh, const uint16_t *x, int64_t M, int64_t in,
+                                  int64_t F, const uint32_t *qweight, const uint16_t *scales,
+                                  const uint32_t *zeros, const uint16_t *s16, int group_size,
+                                  int act, uint16_t *dx, void *stream);
+
+/*
+ * awq_linear_w4a16_grad — the gradient of awq_linear_w4a16 with respect to x, the
+ * packed weights frozen (adapters, soft prompts and norms below a packed layer):
+ *     dx[m, i] = ( sum_o dy[m, o] * (code[o, i] - z[o, i/gs]) * scales[o, i/gs] ) / s16[i].
+ * dy : [M, out] bf16 device;  dx : [M, in] bf16 device, written.  s16 == NULL: x was
+ * used as is (the gradient of the pre-divided input).  Storage arguments as
+ * awq_linear_w4a16; any out >= 1, M <= 2^20.  dy is held as fp16 after a
+ * power-of-two scale per token (exact down to 2^-29 of the token's largest),
+ * the weights as in awq_gated_w4a16.  dx must not overlap any input.  Asynchronous.
+ */
+awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, int64_t out,
+                                   const uint32_t *qweight, const uint16_t *scales,
+                                   const uint32_t *zeros, const uint16_t *s16, int group_size,
+                                   uint16_t *dx, void *stream);
+
+/*
+ * awq_cross_entropy — softmax cross entropy of a dense output head, which the
+ * method leaves in 16 bits: per token, with logits l = x[m] * W^T never written,
+ *     lse[m]  = log sum_v exp(l[v]),   loss[m] = lse[m] - l[labels[m]].
+ * A label outside [0, V) (e.g. -100) marks a token that is not scored: loss[m] = 0.
+ * x : [M, in] bf16, W : [V, in] bf16, labels : [M] int64, loss and lse : [M] fp32
+ * written; all device.  in % 64 == 0, in <= 49152, any V in [1, 2^24], M <= 2^20.
+ * Products are exact, sums fp32.  Asynchronous.
+ */
+awq_status_t awq_cross_entropy(const uint16_t *x, int64_t M, int64_t in, const uint16_t *W,
+                               int64_t V, const int64_t *labels, float *loss, float *lse,
+                               void *stream);
+
+/*
+ * awq_cross_entropy_grad — its gradient: with p = exp(x[m] * W^T - lse[m]),
+ *     d[m, v] = (p[v] - [v == labels[m]]) * dloss[m]   (0 for a token not scored),
+ *     dx = d * W,   dW = d^T * x.
+ * lse : [M] fp32 from awq_cross_entropy on the same x and W;  dloss : [M] fp32, the
+ * gradient of each token's loss (1 / scored tokens for a mean).  dx : [M, in] bf16,
+ * written;  dW : [V, in] bf16, written, or NULL when the head is frozen.  d is computed
+ * in pieces of the vocabulary and rounded to bf16; the pieces of dx meet in fp32.
+ * Rows of x that are not scored add nothing to dW whatever they hold.  dx and dW must not
+ * overlap any input or each other.  Asynchronous.
+ */
+awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, const uint16_t *W,
+                                    int64_t V, const int64_t *labels, const float *lse,
+                                    const float *dloss, uint16_t *dx, uint16_t *dW, void *stream);
+
+/*
  * awq_fold_scale — fold the division by s into the operator that produces
  * this layer's input ([AWQ-blog] Method: X / s is merged into the preceding
  * operator, so the W4A16 layer runs with s16 == NULL):
@@ -319,7 +396,8 @@ awq_status_t awq_act_stats_noalloc(const void *X, int x_dtype, int64_t N, int64_
  * call of the calling host thread (summed over the two search phases), waiting
  * for the end event if needed.  Returns a negative value if nothing was timed.
  *   kind: 0 = activation statistics (both kernels), 1 = fused search kernel,
- *         2 = pack kernel, 3 = W4A16 apply kernel.
+ *         2 = pack kernel, 3 = W4A16 apply kernel, 4 = the tensor-core products of the
+ *         gated, gradient and cross-entropy calls.
  */
 void awq_set_kernel_timing(int enable);
 double awq_last_kernel_ms(int kind);

@@ -12,6 +12,11 @@ names:
     awq_pack_int4(W, sX, alpha, clip, ...)   -> packed INT4 codes, fp16 scales, zeros, s
     awq_pack_quant(W, sX, alpha, ...)        -> the same at w_bit 3 or 4, per-group clip ratios
     awq_linear_w4a16(x, packed...)           -> y = (x / s) @ dequant(W)^T (s16=None: x pre-divided)
+    awq_gated_w4a16(x, packed..., act)       -> act(g) * u, (g | u) = (x / s) @ dequant(W)^T
+    awq_gated_w4a16_grad(dh, x, packed...)   -> its gradient with respect to x
+    awq_linear_w4a16_grad(dy, packed...)     -> gradient of awq_linear_w4a16 with respect to x
+    awq_cross_entropy(x, W, labels)          -> per-token loss and log-sum-exp of x @ W^T
+    awq_cross_entropy_grad(x, W, labels, ..) -> its gradients with respect to x and W
     awq_fold_scale(P, s16)                   -> P / s per row (1/s folded into the previous op)
     awq_wait_selftest(limit, arrive)         -> status of one bounded in-kernel wait
 
@@ -73,6 +78,16 @@ def _load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.awq_linear_w4a16_batch.argtypes = [P, I, L, I, P]
     lib.awq_group_clip.restype = I
     lib.awq_group_clip.argtypes = [P, I, L, L, P, I, L, P, D, I, I, I, P, I, P, P, P]
+    lib.awq_gated_w4a16.restype = I
+    lib.awq_gated_w4a16.argtypes = [P, L, L, L, P, P, P, P, I, I, P, P]
+    lib.awq_gated_w4a16_grad.restype = I
+    lib.awq_gated_w4a16_grad.argtypes = [P, P, L, L, L, P, P, P, P, I, I, P, P]
+    lib.awq_linear_w4a16_grad.restype = I
+    lib.awq_linear_w4a16_grad.argtypes = [P, L, L, L, P, P, P, P, I, P, P]
+    lib.awq_cross_entropy.restype = I
+    lib.awq_cross_entropy.argtypes = [P, L, L, P, L, P, P, P, P]
+    lib.awq_cross_entropy_grad.restype = I
+    lib.awq_cross_entropy_grad.argtypes = [P, L, L, P, L, P, P, P, P, P, P]
     lib.awq_fold_scale.restype = I
     lib.awq_fold_scale.argtypes = [P, I, L, L, P, P, P]
     lib.awq_wait_selftest.restype = I
@@ -91,11 +106,12 @@ EXPORTS = ("awq_version", "awq_status_string", "awq_last_error", "awq_act_stats"
            "awq_pack_quant",
            "awq_linear_w4a16", "awq_linear_w4a16_batch", "awq_fold_scale", "awq_wait_selftest",
            "awq_set_kernel_timing",
-           "awq_last_kernel_ms", "awq_act_stats_noalloc")
+           "awq_last_kernel_ms", "awq_act_stats_noalloc", "awq_gated_w4a16", "awq_gated_w4a16_grad",
+           "awq_linear_w4a16_grad", "awq_cross_entropy", "awq_cross_entropy_grad")
 
 MAX_POINTS = 4096
 
-KT_STATS, KT_SEARCH, KT_PACK, KT_APPLY = 0, 1, 2, 3
+KT_STATS, KT_SEARCH, KT_PACK, KT_APPLY, KT_DENSE = 0, 1, 2, 3, 4
 
 
 def set_kernel_timing(enable: bool) -> None:
@@ -429,3 +445,162 @@ def awq_linear_w4a16_batch(layers, group_size: int = 128, outs=None):
            lib.awq_linear_w4a16_batch(ctypes.cast(descs, ctypes.c_void_p), len(layers), M,
                                       group_size, _stream(layers[0][0])))
     return ys
+
+
+ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _act_code(act) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def _rows(t: torch.Tensor, name: str, like: torch.Tensor, M: int, cols: int):
+    """An [M, cols] bf16 operand on `like`'s device."""
+    if t.dim() != 2 or t.dtype != torch.bfloat16 or tuple(t.shape) != (M, cols):
+        raise ValueError(f"{name} must be a bfloat16 tensor of shape [{M}, {cols}]")
+    _dev(t, name)
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, the other inputs on {like.device}")
+    return t
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _apart(out: torch.Tensor, name: str, *inputs):
+    """A result must not share memory with an input (the kernels read while they write)."""
+    a, b = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for t in inputs:
+        if t is not None and t.data_ptr() < b and a < t.data_ptr() + t.numel() * t.element_size():
+            raise ValueError(f"{name} overlaps an input")
+
+
+def awq_gated_w4a16(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                    zeros: torch.Tensor | None, s16: torch.Tensor | None, group_size: int = 128,
+                    act: str = "silu", out: torch.Tensor | None = None):
+    """h [M, F] bf16 = act(g) * u with (g | u) = (x / s16) @ dequant(W)^T for bf16 x [M, in] and
+    the packed joint gate and up matrix W [2F, in] (gate rows first).  act: 'silu', 'gelu' or
+    'gelu_tanh'.  s16=None when x has already been divided by s."""
+    out_f = _w4a16_operands(x, qweight, scales, zeros, s16, group_size)
+    if out_f % 2:
+        raise ValueError(f"qweight has {out_f} rows; gate and up need an even number")
+    M, inp = x.shape
+    a = _act_code(act)
+    if out is None:
+        out = torch.empty((M, out_f // 2), dtype=torch.bfloat16, device=x.device)
+    else:
+        _out(out, "out", x, torch.bfloat16, M * (out_f // 2))
+        _apart(out, "out", x, qweight, scales, zeros, s16)
+    with torch.cuda.device(x.device):
+        st = lib.awq_gated_w4a16(x.data_ptr(), M, inp, out_f // 2, qweight.data_ptr(), scales.data_ptr(),
+                                 _ptr(zeros), _ptr(s16), group_size, a, out.data_ptr(), _stream(x))
+    _check("awq_gated_w4a16", st)
+    return out
+
+
+def awq_gated_w4a16_grad(dh: torch.Tensor, x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                         zeros: torch.Tensor | None, s16: torch.Tensor | None, group_size: int = 128,
+                         act: str = "silu", out: torch.Tensor | None = None):
+    """dx [M, in] bf16, the gradient of awq_gated_w4a16 with respect to x, for bf16 dh [M, F]; the
+    packed weights are frozen, and g and u are computed again from x."""
+    out_f = _w4a16_operands(x, qweight, scales, zeros, s16, group_size)
+    if out_f % 2:
+        raise ValueError(f"qweight has {out_f} rows; gate and up need an even number")
+    M, inp = x.shape
+    _rows(dh, "dh", x, M, out_f // 2)
+    a = _act_code(act)
+    if out is None:
+        out = torch.empty((M, inp), dtype=torch.bfloat16, device=x.device)
+    else:
+        _out(out, "out", x, torch.bfloat16, M * inp)
+        _apart(out, "out", dh, x, qweight, scales, zeros, s16)
+    with torch.cuda.device(x.device):
+        st = lib.awq_gated_w4a16_grad(dh.data_ptr(), x.data_ptr(), M, inp, out_f // 2, qweight.data_ptr(),
+                                      scales.data_ptr(), _ptr(zeros), _ptr(s16), group_size, a,
+                                      out.data_ptr(), _stream(x))
+    _check("awq_gated_w4a16_grad", st)
+    return out
+
+
+def awq_linear_w4a16_grad(dy: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                          zeros: torch.Tensor | None, s16: torch.Tensor | None, group_size: int = 128,
+                          out: torch.Tensor | None = None):
+    """dx [M, in] bf16 = (dy @ dequant(W)) / s16 for bf16 dy [M, out]: the gradient of
+    awq_linear_w4a16 with respect to x, the packed weights frozen."""
+    if dy.dim() != 2 or qweight.dim() != 2:
+        raise ValueError("dy and qweight must be 2-D")
+    M, inp = dy.shape[0], qweight.shape[1] * 8
+    if out is None:
+        out = torch.empty((M, inp), dtype=torch.bfloat16, device=dy.device)
+    else:
+        _out(out, "out", dy, torch.bfloat16, M * inp)
+        _apart(out, "out", dy, qweight, scales, zeros, s16)
+    # the layer's operands against the [M, in] side, then dy against its output side
+    out_f = _w4a16_operands(out.view(M, inp), qweight, scales, zeros, s16, group_size)
+    _rows(dy, "dy", out, M, out_f)
+    with torch.cuda.device(dy.device):
+        st = lib.awq_linear_w4a16_grad(dy.data_ptr(), M, inp, out_f, qweight.data_ptr(), scales.data_ptr(),
+                                       _ptr(zeros), _ptr(s16), group_size, out.data_ptr(), _stream(dy))
+    _check("awq_linear_w4a16_grad", st)
+    return out
+
+
+def _ce_operands(x, W, labels):
+    """x [M, in] bf16, W [V, in] bf16, labels [M] int64 on one device.  Returns (M, in, V)."""
+    if x.dim() != 2 or x.dtype != torch.bfloat16 or W.dim() != 2 or W.dtype != torch.bfloat16:
+        raise ValueError("x and W must be 2-D bfloat16 tensors")
+    M, inp = x.shape
+    if W.shape[1] != inp:
+        raise ValueError("x and W disagree on the input width")
+    if labels.dtype != torch.int64 or tuple(labels.shape) != (M,):
+        raise ValueError(f"labels must be int64 with {M} elements (one per token)")
+    for t, n in ((x, "x"), (W, "W"), (labels, "labels")):
+        _dev(t, n)
+        if t.device != x.device:
+            raise ValueError(f"{n} is on {t.device}, x on {x.device}")
+    return M, inp, W.shape[0]
+
+
+def awq_cross_entropy(x: torch.Tensor, W: torch.Tensor, labels: torch.Tensor):
+    """(loss [M], lse [M]) fp32: the softmax cross entropy of each token's logits x[m] @ W^T for
+    bf16 x [M, in] and a bf16 head W [V, in], the logits never written.  A label outside [0, V)
+    (e.g. -100) marks a token that is not scored: its loss is 0."""
+    M, inp, V = _ce_operands(x, W, labels)
+    loss = torch.empty(M, dtype=torch.float32, device=x.device)
+    lse = torch.empty(M, dtype=torch.float32, device=x.device)
+    with torch.cuda.device(x.device):
+        st = lib.awq_cross_entropy(x.data_ptr(), M, inp, W.data_ptr(), V, labels.data_ptr(),
+                                   loss.data_ptr(), lse.data_ptr(), _stream(x))
+    _check("awq_cross_entropy", st)
+    return loss, lse
+
+
+def awq_cross_entropy_grad(x: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, lse: torch.Tensor,
+                           dloss: torch.Tensor, want_dw: bool = True, dx: torch.Tensor | None = None,
+                           dW: torch.Tensor | None = None):
+    """(dx [M, in], dW [V, in]) bf16 for lse [M] of awq_cross_entropy on the same x and W and
+    dloss [M] fp32, the gradient of each token's loss; dW is None with want_dw=False (a frozen head).
+    Tokens that are not scored have no gradient and add nothing to dW."""
+    M, inp, V = _ce_operands(x, W, labels)
+    for t, n in ((lse, "lse"), (dloss, "dloss")):
+        _out(t, n, x, torch.float32, M)
+    if dW is not None and not want_dw:
+        raise ValueError("dW given with want_dw=False")
+    if dx is None:
+        dx = torch.empty((M, inp), dtype=torch.bfloat16, device=x.device)
+    else:
+        _out(dx, "dx", x, torch.bfloat16, M * inp)
+        _apart(dx, "dx", x, W, labels, lse, dloss, dW)
+    if want_dw and dW is None:
+        dW = torch.empty((V, inp), dtype=torch.bfloat16, device=x.device)
+    elif want_dw:
+        _out(dW, "dW", x, torch.bfloat16, V * inp)
+        _apart(dW, "dW", x, W, labels, lse, dloss)
+    with torch.cuda.device(x.device):
+        st = lib.awq_cross_entropy_grad(x.data_ptr(), M, inp, W.data_ptr(), V, labels.data_ptr(), lse.data_ptr(),
+                                        dloss.data_ptr(), dx.data_ptr(), _ptr(dW), _stream(x))
+    _check("awq_cross_entropy_grad", st)
+    return dx, dW

@@ -109,14 +109,15 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
     return fn;
 }
 
-// A 2-D tiled tensor map over a row-major [dim1, dim0] array.
+// A 2-D tiled tensor map over a row-major [dim1, dim0] array, its rows `ld` elements apart
+// (0: dim0).
 awq_status_t make_map_2d(CUtensorMap *map, CUtensorMapDataType dt, size_t elem, const void *ptr,
                          uint64_t dim0, uint64_t dim1, uint32_t box0, uint32_t box1,
-                         CUtensorMapSwizzle swz) {
+                         CUtensorMapSwizzle swz, uint64_t ld = 0) {
     auto enc = get_encode();
     if (!enc) return fail(AWQ_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(dim0), static_cast<cuuint64_t>(dim1)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(dim0 * elem)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>((ld ? ld : dim0) * elem)};
     cuuint32_t box[2] = {box0, box1};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = enc(map, dt, 2, const_cast<void *>(ptr), dims, strides, box, estr,
@@ -165,7 +166,7 @@ awq_status_t make_search_maps(awq::SearchMaps *m, const uint16_t *x16, int64_t N
 bool valid_dtype(int d) { return d == AWQ_F32 || d == AWQ_BF16; }
 
 // Optional CUDA-event timing of the main kernels (see awq_set_kernel_timing).
-constexpr int KT_KINDS = 4;
+constexpr int KT_KINDS = 5;
 thread_local bool t_timing = false;
 constexpr int KT_MAX = 64;          // launches one entry point may bracket
 struct KTimer {
@@ -772,6 +773,321 @@ awq_status_t awq_linear_w4a16(const uint16_t *x, int64_t M, int64_t in, int64_t 
     AWQ_CUDA(awq::launch_w4a16_tc(x, M, in, out, scales, zeros, s16, group_size, y, plan, wsp, maps,
                                   st));
     kt_end(3, st);
+    return AWQ_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// The checks that every call on a packed layer shares (W is [out][in] in awq_pack_int4's layout).
+awq_status_t check_packed(int64_t M, int64_t in, int64_t out, const uint32_t *qweight, const uint16_t *scales,
+                          const uint32_t *zeros, const uint16_t *s16, int group_size) {
+    if (!qweight || !scales) return fail(AWQ_ERR_ARG, "NULL pointer");
+    if (M < 1 || in < 1 || out < 1) return fail(AWQ_ERR_ARG, "bad shape");
+    if (group_size != 32 && group_size != 64 && group_size != 128)
+        return fail(AWQ_ERR_UNSUPPORTED, "group_size %d not in {32, 64, 128}", group_size);
+    if (in % 64 != 0) return fail(AWQ_ERR_UNSUPPORTED, "in=%lld is not a multiple of 64", (long long)in);
+    if (in % group_size != 0)
+        return fail(AWQ_ERR_UNSUPPORTED, "in=%lld is not a multiple of group_size %d", (long long)in, group_size);
+    if (in > 49152) return fail(AWQ_ERR_UNSUPPORTED, "in=%lld above 49152", (long long)in);
+    if (out > (1 << 24)) return fail(AWQ_ERR_UNSUPPORTED, "out=%lld above 2^24", (long long)out);
+    if (M > (1 << 20)) return fail(AWQ_ERR_UNSUPPORTED, "M=%lld above 2^20", (long long)M);
+    if (!aligned16(qweight) || (reinterpret_cast<uintptr_t>(scales) & 1u) ||
+        (zeros && (reinterpret_cast<uintptr_t>(zeros) & 3u)) || (s16 && !aligned16(s16)))
+        return fail(AWQ_ERR_ALIGN, "misaligned pointer");
+    return AWQ_OK;
+}
+
+bool valid_act(int act) { return act == AWQ_ACT_SILU || act == AWQ_ACT_GELU || act == AWQ_ACT_GELU_TANH; }
+
+int64_t round64(int64_t v) { return (v + 63) / 64 * 64; }
+int ceil_div(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// Operand maps of a dense product: `rows` x `k` K-major, 64 k x box_rows; or MN-major [k][mn], 64 x 64.
+awq_status_t map_kmajor(CUtensorMap *m, bool bf16, const void *p, int64_t k, int64_t rows, int64_t ld, int box_rows) {
+    return make_map_2d(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p, k, rows,
+                       awq::SLAB_K, static_cast<uint32_t>(box_rows), CU_TENSOR_MAP_SWIZZLE_128B, ld);
+}
+awq_status_t map_mnmajor(CUtensorMap *m, bool bf16, const void *p, int64_t mn, int64_t k, int64_t ld) {
+    return make_map_2d(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p, mn, k, 64,
+                       awq::SLAB_K, CU_TENSOR_MAP_SWIZZLE_128B, ld);
+}
+
+}  // namespace
+
+extern "C" {
+
+static awq_status_t gated_dense(const uint16_t *dh, const uint16_t *x, int64_t M, int64_t in, int64_t F,
+                                const uint32_t *qweight, const uint16_t *scales, const uint32_t *zeros,
+                                const uint16_t *s16, int group_size, int act, uint16_t *out, int sms,
+                                cudaStream_t st) {
+    const int64_t O = 2 * F, Fp = round64(F);
+    Workspace ws(st);
+    size_t bytes = Workspace::up(2 * M * in) + Workspace::up(4 * M) + Workspace::up(4) + Workspace::up(2 * O * in);
+    if (dh) bytes += Workspace::up(4 * M) + Workspace::up(2 * M * 2 * Fp);
+    if (awq_status_t s = ws.reserve(bytes)) return s;
+    uint16_t *xs = ws.take<uint16_t>(M * in);
+    float *sx = ws.take<float>(M);
+    unsigned *dmax = ws.take<unsigned>(1);
+    uint16_t *w16 = ws.take<uint16_t>(O * in);
+    int *grow = dh ? ws.take<int>(M) : nullptr;
+    uint16_t *d16 = dh ? ws.take<uint16_t>(M * 2 * Fp) : nullptr;
+    AWQ_CUDA(awq::launch_rows16(x, s16, M, in, in, dh, F, scales, O * (in / group_size), xs, sx, grow, dmax, st));
+    AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, O, in, group_size, dmax, w16, sms, st));
+    awq::GemmArgs a{};
+    a.M = M;
+    a.bn = awq::gemm_tile_cols(M, 2 * (dh ? Fp : F), sms);
+    a.mt = ceil_div(M, 256);
+    a.nt = ceil_div(dh ? Fp : F, a.bn / 2);
+    a.nk[0] = static_cast<int>(in / 64);
+    a.sx = sx;
+    a.dmax = dmax;
+    a.grow = grow;
+    a.inner = static_cast<int>(in);
+    a.act = act;
+    a.F = F;
+    a.Fp = Fp;
+    a.dh = dh;
+    a.out = out;
+    a.d16 = d16;
+    a.ldd = 2 * Fp;
+    awq::GemmMaps maps;
+    if (awq_status_t s = map_kmajor(&maps.a, false, xs, in, M, in, 128)) return s;
+    if (awq_status_t s = map_kmajor(&maps.b, false, w16, in, O, in, a.bn / 2)) return s;
+    kt_reset(4);
+    kt_begin(4, st);
+    AWQ_CUDA(awq::launch_gemm16(dh ? awq::EPI_GATED_BWD : awq::EPI_GATED, false, false, maps, a, sms, st));
+    kt_end(4, st);
+    if (!dh) return AWQ_OK;
+    // dx = ([dg | du] W) / s: K runs over the gate rows of W, then its up rows
+    awq::GemmArgs b{};
+    b.M = M;
+    b.N = in;
+    b.bn = awq::gemm_tile_cols(M, in, sms);
+    b.mt = ceil_div(M, 256);
+    b.nt = ceil_div(in, b.bn);
+    b.nk[0] = b.nk[1] = static_cast<int>(Fp / 64);
+    b.a_seg = static_cast<int>(Fp);
+    b.b_seg = static_cast<int>(F);
+    b.grow = grow;
+    b.dmax = dmax;
+    b.inner = static_cast<int>(in);
+    b.s16 = s16;
+    b.out = out;
+    if (awq_status_t s = map_kmajor(&maps.a, false, d16, 2 * Fp, M, 2 * Fp, 128)) return s;
+    if (awq_status_t s = map_mnmajor(&maps.b, false, w16, in, O, in)) return s;
+    kt_begin(4, st);
+    AWQ_CUDA(awq::launch_gemm16(awq::EPI_OUT, false, false, maps, b, sms, st));
+    kt_end(4, st);
+    return AWQ_OK;
+}
+
+awq_status_t awq_gated_w4a16(const uint16_t *x, int64_t M, int64_t in, int64_t F, const uint32_t *qweight,
+                             const uint16_t *scales, const uint32_t *zeros, const uint16_t *s16, int group_size,
+                             int act, uint16_t *h, void *stream) {
+    awq::NvtxRange nvtx_range("awq_gated_w4a16");
+    g_last_error.clear();
+    if (!x || !h) return fail(AWQ_ERR_ARG, "NULL pointer");
+    if (!valid_act(act)) return fail(AWQ_ERR_ARG, "bad act %d", act);
+    if (F < 1 || F > (1 << 23)) return fail(AWQ_ERR_ARG, "bad F=%lld", (long long)F);
+    if (awq_status_t s = check_packed(M, in, 2 * F, qweight, scales, zeros, s16, group_size)) return s;
+    if (!aligned16(x) || !aligned16(h)) return fail(AWQ_ERR_ALIGN, "misaligned pointer");
+    int sms;
+    if (awq_status_t s = device_info(&sms)) return s;
+    return gated_dense(nullptr, x, M, in, F, qweight, scales, zeros, s16, group_size, act, h, sms,
+                       static_cast<cudaStream_t>(stream));
+}
+
+awq_status_t awq_gated_w4a16_grad(const uint16_t *dh, const uint16_t *x, int64_t M, int64_t in, int64_t F,
+                                  const uint32_t *qweight, const uint16_t *scales, const uint32_t *zeros,
+                                  const uint16_t *s16, int group_size, int act, uint16_t *dx, void *stream) {
+    awq::NvtxRange nvtx_range("awq_gated_w4a16_grad");
+    g_last_error.clear();
+    if (!dh || !x || !dx) return fail(AWQ_ERR_ARG, "NULL pointer");
+    if (!valid_act(act)) return fail(AWQ_ERR_ARG, "bad act %d", act);
+    if (F < 1 || F > (1 << 23)) return fail(AWQ_ERR_ARG, "bad F=%lld", (long long)F);
+    if (awq_status_t s = check_packed(M, in, 2 * F, qweight, scales, zeros, s16, group_size)) return s;
+    if (!aligned16(dh) || !aligned16(x) || !aligned16(dx)) return fail(AWQ_ERR_ALIGN, "misaligned pointer");
+    int sms;
+    if (awq_status_t s = device_info(&sms)) return s;
+    return gated_dense(dh, x, M, in, F, qweight, scales, zeros, s16, group_size, act, dx, sms,
+                       static_cast<cudaStream_t>(stream));
+}
+
+awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, int64_t out, const uint32_t *qweight,
+                                   const uint16_t *scales, const uint32_t *zeros, const uint16_t *s16,
+                                   int group_size, uint16_t *dx, void *stream) {
+    awq::NvtxRange nvtx_range("awq_linear_w4a16_grad");
+    g_last_error.clear();
+    if (!dy || !dx) return fail(AWQ_ERR_ARG, "NULL pointer");
+    if (awq_status_t s = check_packed(M, in, out, qweight, scales, zeros, s16, group_size)) return s;
+    if (!aligned16(dy) || !aligned16(dx)) return fail(AWQ_ERR_ALIGN, "misaligned pointer");
+    int sms;
+    if (awq_status_t s = device_info(&sms)) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int64_t ld = round64(out);
+    Workspace ws(st);
+    if (awq_status_t s = ws.reserve(Workspace::up(2 * M * ld) + Workspace::up(4 * M) + Workspace::up(4) +
+                                    Workspace::up(2 * out * in)))
+        return s;
+    uint16_t *d16 = ws.take<uint16_t>(M * ld);
+    float *sx = ws.take<float>(M);
+    unsigned *dmax = ws.take<unsigned>(1);
+    uint16_t *w16 = ws.take<uint16_t>(out * in);
+    AWQ_CUDA(awq::launch_rows16(dy, nullptr, M, out, ld, nullptr, 0, scales, out * (in / group_size), d16, sx, nullptr,
+                                dmax, st));
+    AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, out, in, group_size, dmax, w16, sms, st));
+    awq::GemmArgs b{};
+    b.M = M;
+    b.N = in;
+    b.bn = awq::gemm_tile_cols(M, in, sms);
+    b.mt = ceil_div(M, 256);
+    b.nt = ceil_div(in, b.bn);
+    b.nk[0] = ceil_div(out, 64);
+    b.sx = sx;
+    b.dmax = dmax;
+    b.s16 = s16;
+    b.out = dx;
+    awq::GemmMaps maps;
+    if (awq_status_t s = map_kmajor(&maps.a, false, d16, out, M, ld, 128)) return s;
+    if (awq_status_t s = map_mnmajor(&maps.b, false, w16, in, out, in)) return s;
+    kt_reset(4);
+    kt_begin(4, st);
+    AWQ_CUDA(awq::launch_gemm16(awq::EPI_OUT, false, false, maps, b, sms, st));
+    kt_end(4, st);
+    return AWQ_OK;
+}
+
+static awq_status_t check_ce(const uint16_t *x, int64_t M, int64_t in, const uint16_t *W, int64_t V,
+                             const int64_t *labels) {
+    if (!x || !W || !labels) return fail(AWQ_ERR_ARG, "NULL pointer");
+    if (M < 1 || in < 1 || V < 1) return fail(AWQ_ERR_ARG, "bad shape");
+    if (in % 64 != 0) return fail(AWQ_ERR_UNSUPPORTED, "in=%lld is not a multiple of 64", (long long)in);
+    if (in > 49152 || V > (1 << 24) || M > (1 << 20)) return fail(AWQ_ERR_UNSUPPORTED, "sizes above in 49152, V 2^24, M 2^20");
+    if (!aligned16(x) || !aligned16(W) || (reinterpret_cast<uintptr_t>(labels) & 7u))
+        return fail(AWQ_ERR_ALIGN, "misaligned pointer");
+    return AWQ_OK;
+}
+
+awq_status_t awq_cross_entropy(const uint16_t *x, int64_t M, int64_t in, const uint16_t *W, int64_t V,
+                               const int64_t *labels, float *loss, float *lse, void *stream) {
+    awq::NvtxRange nvtx_range("awq_cross_entropy");
+    g_last_error.clear();
+    if (!loss || !lse) return fail(AWQ_ERR_ARG, "NULL pointer");
+    if (awq_status_t s = check_ce(x, M, in, W, V, labels)) return s;
+    if ((reinterpret_cast<uintptr_t>(loss) & 3u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return fail(AWQ_ERR_ALIGN, "misaligned pointer");
+    int sms;
+    if (awq_status_t s = device_info(&sms)) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    awq::GemmArgs a{};
+    a.M = M;
+    a.N = a.V = V;
+    a.bn = awq::gemm_tile_cols(M, V, sms);
+    a.mt = ceil_div(M, 256);
+    a.nt = ceil_div(V, a.bn);
+    a.nk[0] = static_cast<int>(in / 64);
+    Workspace ws(st);
+    if (awq_status_t s = ws.reserve(Workspace::up(4 * M) + Workspace::up(sizeof(float2) * M * a.nt))) return s;
+    a.tgt = ws.take<float>(M);
+    a.part = ws.take<float2>(M * a.nt);
+    a.labels = labels;
+    awq::GemmMaps maps;
+    if (awq_status_t s = map_kmajor(&maps.a, true, x, in, M, in, 128)) return s;
+    if (awq_status_t s = map_kmajor(&maps.b, true, W, in, V, in, a.bn / 2)) return s;
+    kt_reset(4);
+    kt_begin(4, st);
+    AWQ_CUDA(awq::launch_gemm16(awq::EPI_CE, true, false, maps, a, sms, st));
+    kt_end(4, st);
+    AWQ_CUDA(awq::launch_ce_final(a.part, a.nt, M, labels, V, a.tgt, loss, lse, st));
+    return AWQ_OK;
+}
+
+awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, const uint16_t *W, int64_t V,
+                                    const int64_t *labels, const float *lse, const float *dloss, uint16_t *dx,
+                                    uint16_t *dW, void *stream) {
+    awq::NvtxRange nvtx_range("awq_cross_entropy_grad");
+    g_last_error.clear();
+    if (!lse || !dloss || !dx) return fail(AWQ_ERR_ARG, "NULL pointer");
+    if (awq_status_t s = check_ce(x, M, in, W, V, labels)) return s;
+    if ((reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(dloss) & 3u) || !aligned16(dx) ||
+        (dW && !aligned16(dW)))
+        return fail(AWQ_ERR_ALIGN, "misaligned pointer");
+    int sms;
+    if (awq_status_t s = device_info(&sms)) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // Pieces of the vocabulary: the 16-bit gradients of one piece take about 64 MB, so that the
+    // products that read them find them in L2; at least 4096 entries.
+    int64_t vc = (int64_t(64) << 20) / (2 * M);
+    vc = vc < 4096 ? 4096 : vc;
+    const int64_t pieces = (V + vc - 1) / vc;
+    vc = ((V + pieces - 1) / pieces + 255) / 256 * 256;
+    const int64_t ldd = vc < round64(V) ? vc : round64(V);
+    Workspace ws(st);
+    size_t bytes = Workspace::up(2 * M * ldd);
+    if (pieces > 1) bytes += Workspace::up(4 * M * in);
+    if (dW) bytes += Workspace::up(2 * M * in);
+    if (awq_status_t s = ws.reserve(bytes)) return s;
+    uint16_t *d16 = ws.take<uint16_t>(M * ldd);
+    float *acc = pieces > 1 ? ws.take<float>(M * in) : nullptr;
+    uint16_t *xz = nullptr;
+    if (dW) {
+        xz = ws.take<uint16_t>(M * in);
+        AWQ_CUDA(awq::launch_scored_rows(x, labels, V, M, in, xz, sms, st));
+    }
+    kt_reset(4);
+    kt_begin(4, st);
+    for (int64_t v0 = 0; v0 < V; v0 += vc) {
+        const int64_t n = V - v0 < vc ? V - v0 : vc;
+        const uint16_t *Wp = W + v0 * in;
+        awq::GemmMaps maps;
+        awq::GemmArgs a{};
+        a.M = M;
+        a.N = n;
+        a.V = V;
+        a.v0 = v0;
+        a.bn = awq::gemm_tile_cols(M, n, sms);
+        a.mt = ceil_div(M, 256);
+        a.nt = ceil_div(n, a.bn);
+        a.nk[0] = static_cast<int>(in / 64);
+        a.labels = labels;
+        a.lse = lse;
+        a.dloss = dloss;
+        a.d16 = d16;
+        a.ldd = ldd;
+        if (awq_status_t s = map_kmajor(&maps.a, true, x, in, M, in, 128)) return s;
+        if (awq_status_t s = map_kmajor(&maps.b, true, Wp, in, n, in, a.bn / 2)) return s;
+        AWQ_CUDA(awq::launch_gemm16(awq::EPI_CE_BWD, true, false, maps, a, sms, st));
+        awq::GemmArgs b{};
+        b.M = M;
+        b.N = in;
+        b.bn = awq::gemm_tile_cols(M, in, sms);
+        b.mt = ceil_div(M, 256);
+        b.nt = ceil_div(in, b.bn);
+        b.nk[0] = ceil_div(n, 64);
+        b.out = dx;
+        b.acc = acc;
+        b.first = v0 == 0;
+        b.last = v0 + vc >= V;
+        if (awq_status_t s = map_kmajor(&maps.a, true, d16, n, M, ldd, 128)) return s;
+        if (awq_status_t s = map_mnmajor(&maps.b, true, Wp, in, n, in)) return s;
+        AWQ_CUDA(awq::launch_gemm16(awq::EPI_OUT, true, false, maps, b, sms, st));
+        if (dW) {
+            awq::GemmArgs c{};
+            c.M = n;
+            c.N = in;
+            c.bn = awq::gemm_tile_cols(n, in, sms);
+            c.mt = ceil_div(n, 256);
+            c.nt = ceil_div(in, c.bn);
+            c.nk[0] = ceil_div(M, 64);
+            c.out = dW + v0 * in;
+            if (awq_status_t s = map_mnmajor(&maps.a, true, d16, n, M, ldd)) return s;
+            if (awq_status_t s = map_mnmajor(&maps.b, true, xz, in, M, in)) return s;
+            AWQ_CUDA(awq::launch_gemm16(awq::EPI_OUT, true, true, maps, c, sms, st));
+        }
+    }
+    kt_end(4, st);
     return AWQ_OK;
 }
 

@@ -200,6 +200,57 @@ cudaError_t launch_group_clip(const void *W, bool w_bf16, int64_t O, int64_t I, 
 // timeout code to *err.
 cudaError_t launch_wait_selftest(long long limit, bool arrive, int *err, cudaStream_t st);
 
+// ---- dense 16-bit products on the tensor cores and the epilogues of the operators that train
+// through packed weights and score a vocabulary (k_dense.cu), with their operand preparation
+// (k_dequant.cu)
+enum { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
+enum { EPI_GATED = 0, EPI_GATED_BWD = 1, EPI_OUT = 2, EPI_CE = 3, EPI_CE_BWD = 4 };
+struct GemmMaps {
+    CUtensorMap a, b;           // K-major: box 64 k x 128 rows (b: bn / 2 rows); MN-major: box 64 x 64
+};
+struct GemmArgs {
+    int64_t M, N;               // rows and columns of D (EPI_GATED*: N unused)
+    int mt, nt;                 // tiles of 256 rows and of bn columns (EPI_GATED*: of bn / 2 gate columns)
+    int bn;                     // tile columns of the pair
+    int nk[2];                  // 64-deep K slabs of the two K segments
+    int a_seg, b_seg;           // first K coordinate of the second segment in A and in B
+    // scales
+    const float *sx;            // [M]: A's row m carries 1 / sx[m] (a power of two)
+    const unsigned *dmax;       // the layer's largest |Delta| (the weights carry 2^-kW)
+    const int *grow;            // [M]: exponent bound of the token's gradients (DGU_NONE: none)
+    const uint16_t *s16;        // [N] fp16: divides column n (EPI_OUT)
+    int inner;                  // in, of the gated product
+    int act;
+    int64_t F, Fp;              // gate columns; rounded up to 64
+    const uint16_t *dh;         // [M][F] bf16
+    // cross entropy
+    const int64_t *labels;      // [M]
+    int64_t V, v0;              // vocabulary; first entry of this piece
+    const float *lse, *dloss;   // [M]
+    float *tgt;                 // [M] the label's logit
+    float2 *part;               // [nt][M] (maximum, sum of exponentials)
+    // outputs
+    uint16_t *out;              // bf16
+    uint16_t *d16;              // [M][ldd] 16-bit gradients
+    int64_t ldd;
+    float *acc;                 // [M][N] fp32, pieces meet here (EPI_OUT), or null
+    bool first, last;           // first: acc is not read; last: the result goes to out
+};
+int gemm_tile_cols(int64_t M, int64_t N, int num_sms);
+cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, const GemmArgs &a, int num_sms,
+                          cudaStream_t st);
+cudaError_t launch_ce_final(const float2 *part, int nt, int64_t M, const int64_t *labels, int64_t V,
+                            const float *tgt, float *loss, float *lse, cudaStream_t st);
+// Token rows to fp16 with a power-of-two scale each (out [M][ld], sx [M]); dh [M][F] with grow [M]
+// optional; *dmax = the layer's largest |Delta| as fp16 bits.
+cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int64_t cols, int64_t ld,
+                          const uint16_t *dh, int64_t F, const uint16_t *scales, int64_t n_scales, uint16_t *out,
+                          float *sx, int *grow, unsigned *dmax, cudaStream_t st);
+cudaError_t launch_dequant(const uint32_t *q, const uint16_t *scales, const uint32_t *zeros, int64_t O, int64_t I,
+                           int gs, const unsigned *dmax, uint16_t *out, int num_sms, cudaStream_t st);
+cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t V, int64_t M, int64_t I,
+                               uint16_t *out, int num_sms, cudaStream_t st);
+
 // ---- fold of 1/s into the previous operator: out[r][c] = P[r][c] / s16[r]
 // (one IEEE fp32 division, then bf16 rounding when bf16).
 cudaError_t launch_fold_scale(const void *P, bool bf16, int64_t R, int64_t C, const uint16_t *s16,

@@ -1,0 +1,539 @@
+// Dense 16-bit products on the tensor cores, D[m, n] = sum_k A[m, k] B[n, k] with fp32
+// accumulation, and the epilogues of the operators that train through packed weights and
+// score a vocabulary:
+//
+//   EPI_GATED      A = x / s (fp16), B = dequantised gate rows | up rows:
+//                  h = act(g) * u, both projections, the activation and the product in one pass;
+//   EPI_GATED_BWD  the same product, then dg = dh * u * act'(g) and du = dh * act(g) as fp16,
+//                  each token scaled by a power of two (the operand of the product with W);
+//   EPI_OUT        D * row scale / s[n], optionally added to an fp32 buffer: the input gradients
+//                  (B read along its rows: K is W's row) and the head's weight gradient;
+//   EPI_CE         logits = x W^T of one vocabulary tile: each row's maximum and sum of
+//                  exponentials over the tile, and the label's logit; the logits stay on chip;
+//   EPI_CE_BWD     (exp(logit - lse) - [n = label]) * dloss as bf16, one piece of the vocabulary.
+//
+// CTA pairs (clusters of two, one CTA per SM, persistent over output tiles): a tile is 256 rows
+// x bn columns (bn <= 256, a multiple of 32) on tcgen05.mma.cta_group::2, M = 256, N = bn,
+// K = 16.  Each CTA stages its own 128 rows of A and half of B's columns, 64 deep, by TMA into a
+// six-stage ring of 32 KB; the accumulator has two 256-column halves of TMEM, so the epilogue of a
+// tile overlaps the main loop of the next.  Warps: 0 TMA, 1 MMA, 4-7 epilogue (lane = row).
+// A K-major operand lies as [rows][64 k] in 128-byte swizzled rows; an operand read along its
+// rows (MN-major) as blocks of [64 k][64 n], 8 KB each, in the same swizzle.
+//
+// Tiles are walked in bands of eight row tiles, the row tile fastest, so the pairs that run at
+// one time share a few column tiles of B and one band of A in L2.
+//
+// Every wait is bounded, as in the other kernels: a CTA that gives up raises its abort flag,
+// waits (bounded) for its MMAs and leaves without writing its remaining tiles.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "awq_internal.h"
+#include "awq_ptx.cuh"
+#include "w4a16_act.cuh"
+
+namespace awq {
+
+namespace {
+
+constexpr int GM_STAGES = 6;
+constexpr int GM_A_BYTES = 128 * SLAB_K * 2;          // 16 KB: this CTA's rows of A
+constexpr int GM_B_BYTES = 128 * SLAB_K * 2;          // 16 KB: this CTA's columns of B
+constexpr int GM_STAGE = GM_A_BYTES + GM_B_BYTES;
+constexpr int GM_THREADS = 256;
+constexpr int GM_EPI_WARP0 = 4;
+constexpr int GM_BAND = 8;                            // row tiles walked together
+constexpr uint32_t GM_TMEM = 512;
+constexpr int GM_BARS = 2 * GM_STAGES + 4 + 1;
+constexpr int GM_SMEM = 1024 + GM_STAGES * GM_STAGE + GM_BARS * 8 + 16;
+static_assert(GM_SMEM <= 232448, "shared memory plan");
+
+// Shared-memory descriptor of an MN-major operand in the 128-byte swizzle: blocks of 64
+// elements along MN (8192 bytes apart: 64 k rows of 128 bytes), 8 k rows per 1024-byte atom.
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(8192 >> 4) << 16;              // leading byte offset: next 64 along MN
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;              // stride byte offset: next 8 along K
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+struct Tile {
+    int m, n;
+};
+__device__ __forceinline__ Tile decode_tile(int t, int mt, int nt) {
+    const int band = t / (GM_BAND * nt);
+    const int r = t - band * (GM_BAND * nt);
+    const int h = mt - band * GM_BAND < GM_BAND ? mt - band * GM_BAND : GM_BAND;
+    Tile o;
+    o.n = r / h;
+    o.m = band * GM_BAND + (r - o.n * h);
+    return o;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float bf16f(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+
+// 16 consecutive values to bf16 at p[0..16): 16-byte stores when the row allows (`vec`),
+// else one by one below `n` values.
+__device__ __forceinline__ void store_bf16_16(uint16_t *p, const float (&v)[16], bool vec, int64_t n) {
+    if (vec && n >= 16) {
+        uint4 *q = reinterpret_cast<uint4 *>(p);
+        q[0] = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+        q[1] = make_uint4(bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]), bf16x2(v[14], v[15]));
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+        if (k < n) p[k] = __bfloat16_as_ushort(__float2bfloat16_rn(v[k]));
+}
+
+// ---- epilogues of one thread's row (its TMEM lane at `acc`), tile columns [0, bn).  The TMEM
+// loads are warp-wide: rows beyond M skip only the work between them, and every loop ends in a
+// warp barrier.
+
+__device__ __forceinline__ void epi_gated(const GemmArgs &a, uint32_t acc, int64_t row, int64_t f0) {
+    const int half = a.bn / 2;
+    const float sc = row < a.M ? __ldg(a.sx + row) : 0.0f;
+    const float sw = dq_scale(a.dmax);
+    const bool vec = a.F % 8 == 0;
+#pragma unroll 1
+    for (int c = 0; c < half; c += 16) {
+        uint32_t g[16], u[16];
+        tmem_ld16_wait(acc + c, g);
+        tmem_ld16_wait(acc + half + c, u);
+        float h[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            // the two power-of-two factors one after the other: each is a normal float
+            const float gv = (__uint_as_float(g[k]) * sc) * sw, uv = (__uint_as_float(u[k]) * sc) * sw;
+            h[k] = act_value(gv, a.act) * uv;
+        }
+        if (row < a.M && f0 + c < a.F) store_bf16_16(a.out + row * a.F + f0 + c, h, vec, a.F - f0 - c);
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t f0) {
+    const int half = a.bn / 2;
+    const bool ok = row < a.M;
+    const float sc = ok ? __ldg(a.sx + row) : 0.0f;
+    const float sw = dq_scale(a.dmax);
+    // 2^-e of this token's gradients
+    const float sd = ok ? ldexpf(1.0f, -dgu_exp(__ldg(a.grow + row), a.inner, a.dmax)) : 0.0f;
+    const uint16_t *dh = a.dh + (ok ? row : 0) * a.F;
+#pragma unroll 1
+    for (int c = 0; c < half; c += 16) {
+        uint32_t g[16], u[16];
+        tmem_ld16_wait(acc + c, g);
+        tmem_ld16_wait(acc + half + c, u);
+        if (ok && f0 + c < a.Fp) {
+        uint32_t pg[8], pu[8];
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+            float dg[2], du[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int64_t f = f0 + c + k + j;
+                const float gv = (__uint_as_float(g[k + j]) * sc) * sw, uv = (__uint_as_float(u[k + j]) * sc) * sw;
+                float da;
+                const float av = act_both(gv, a.act, da);
+                const float d = f < a.F ? bf16f(__ldg(dh + f)) * sd : 0.0f;
+                // columns of the padding are exact zeros whatever the tile holds there
+                dg[j] = f < a.F ? (d * uv) * da : 0.0f;
+                du[j] = f < a.F ? d * av : 0.0f;
+            }
+            const __half2 hg = __floats2half2_rn(dg[0], dg[1]), hu = __floats2half2_rn(du[0], du[1]);
+            pg[k / 2] = *reinterpret_cast<const uint32_t *>(&hg);
+            pu[k / 2] = *reinterpret_cast<const uint32_t *>(&hu);
+        }
+        uint4 *qg = reinterpret_cast<uint4 *>(a.d16 + row * a.ldd + f0 + c);
+        uint4 *qu = reinterpret_cast<uint4 *>(a.d16 + row * a.ldd + a.Fp + f0 + c);
+        qg[0] = make_uint4(pg[0], pg[1], pg[2], pg[3]);
+        qg[1] = make_uint4(pg[4], pg[5], pg[6], pg[7]);
+        qu[0] = make_uint4(pu[0], pu[1], pu[2], pu[3]);
+        qu[1] = make_uint4(pu[4], pu[5], pu[6], pu[7]);
+        }
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0) {
+    const bool ok = row < a.M;
+    float sc = 1.0f, sw = 1.0f;
+    if (a.grow) {                                      // gated gradient: 2^e of the token
+        sc = ok ? ldexpf(1.0f, dgu_exp(__ldg(a.grow + row), a.inner, a.dmax)) : 0.0f;
+        sw = dq_scale(a.dmax);
+    } else if (a.sx) {
+        sc = ok ? __ldg(a.sx + row) : 0.0f;
+        sw = dq_scale(a.dmax);
+    }
+#pragma unroll 1
+    for (int c = 0; c < a.bn; c += 16) {
+        uint32_t r[16];
+        tmem_ld16_wait(acc + c, r);
+        if (ok && n0 + c < a.N) {                     // N is a multiple of 64: a 16-column chunk is in or out
+        float v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = (__uint_as_float(r[k]) * sc) * sw;
+        if (a.s16) {
+            const uint4 *sp = reinterpret_cast<const uint4 *>(a.s16 + n0 + c);
+            const uint4 s0 = __ldg(sp), s1 = __ldg(sp + 1);
+            const uint32_t sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const __half2 h = *reinterpret_cast<const __half2 *>(&sv[k]);
+                v[2 * k] = v[2 * k] / __low2float(h);
+                v[2 * k + 1] = v[2 * k + 1] / __high2float(h);
+            }
+        }
+        if (a.acc) {
+            float4 *q = reinterpret_cast<float4 *>(a.acc + row * a.N + n0 + c);
+            if (!a.first) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 p = q[k];
+                    v[4 * k] += p.x; v[4 * k + 1] += p.y; v[4 * k + 2] += p.z; v[4 * k + 3] += p.w;
+                }
+            }
+            if (!a.last) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) q[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            }
+        }
+        if (!a.acc || a.last) store_bf16_16(a.out + row * a.N + n0 + c, v, true, 16);
+        }
+        __syncwarp();
+    }
+}
+
+constexpr float LOG2E = 1.4426950408889634f;
+
+__device__ __forceinline__ void epi_ce(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int ntile) {
+    const bool ok = row < a.M;
+    const int64_t lab = ok ? __ldg(a.labels + row) : -1;
+    float mx = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < a.bn; c += 16) {
+        uint32_t r[16];
+        tmem_ld16_wait(acc + c, r);
+        if (ok && n0 + c < a.N) {
+        float v[16], cm = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            v[k] = n0 + c + k < a.N ? __uint_as_float(r[k]) : -INFINITY;
+            cm = fmaxf(cm, v[k]);
+        }
+        const int64_t j = lab - n0 - c;
+        if (j >= 0 && j < 16 && lab < a.N) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                if (j == k) a.tgt[row] = v[k];
+        }
+        const float nm = fmaxf(mx, cm);
+        // a tile of nothing but -inf (or NaN) keeps a finite reference
+        const float ref = nm == -INFINITY ? 0.0f : nm;
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) s += exp2f((v[k] - ref) * LOG2E);
+        sum = sum * exp2f((mx - ref) * LOG2E) + s;
+        mx = nm;
+        }
+        __syncwarp();
+    }
+    if (ok) a.part[static_cast<int64_t>(ntile) * a.M + row] = make_float2(mx, sum);
+}
+
+__device__ __forceinline__ void epi_ce_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0) {
+    const bool ok = row < a.M;
+    const int64_t lab = ok ? __ldg(a.labels + row) : -1;
+    const bool scored = lab >= 0 && lab < a.V;
+    const float lse = ok ? __ldg(a.lse + row) : 0.0f;
+    const float w = ok ? __ldg(a.dloss + row) : 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < a.bn; c += 16) {
+        uint32_t r[16];
+        tmem_ld16_wait(acc + c, r);
+        if (ok && n0 + c < a.N) {
+        float v[16];
+        const int64_t j = lab - a.v0 - n0 - c;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            float p = exp2f((__uint_as_float(r[k]) - lse) * LOG2E);
+            if (j == k) p -= 1.0f;
+            v[k] = scored ? p * w : 0.0f;
+        }
+        // the row stride is a multiple of 64: the store may run into the row's own padding
+        store_bf16_16(a.d16 + row * a.ldd + n0 + c, v, true, 16);
+        }
+        __syncwarp();
+    }
+}
+
+template <int EPI, bool BF16, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(GM_THREADS, 1)
+    gemm16_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(ring + GM_STAGES * GM_STAGE);
+    uint64_t *empty = full + GM_STAGES;
+    uint64_t *acc_full = empty + GM_STAGES;            // [2]: accumulator halves
+    uint64_t *acc_empty = acc_full + 2;                // [2]
+    uint64_t *drain = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int tiles = a.mt * a.nt;
+    const int nk = a.nk[0] + a.nk[1];                  // 64-deep slabs of both K segments
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < GM_STAGES; ++s) {
+            mbar_init(&full[s], 1);                    // the leader's expect_tx; bytes of both CTAs
+            mbar_init(&empty[s], 1);                   // the leader's multicast commit
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&acc_full[h], 1);
+            mbar_init(&acc_empty[h], 2 * 4);           // epilogue warps of both CTAs
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, GM_TMEM);
+        tmem_relinquish_pair();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&maps.a);
+        tma_prefetch_desc(&maps.b);
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int bh = a.bn / 2;                           // B columns of this CTA
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            const int nb = B_MN ? (bh + 63) / 64 : 1;  // blocks of 64 columns when B is MN-major
+            const uint32_t bytes = GM_A_BYTES + (B_MN ? nb * 8192 : bh * 128);
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                const Tile tl = decode_tile(t, a.mt, a.nt);
+                const int m0 = tl.m * 256 + static_cast<int>(rank) * 128;
+                const int n0 = EPI == EPI_GATED || EPI == EPI_GATED_BWD
+                                   ? tl.n * bh + static_cast<int>(rank) * static_cast<int>(a.F)   // gate | up rows
+                                   : tl.n * a.bn + static_cast<int>(rank) * bh;
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const uint32_t st = it % GM_STAGES;
+                    if (!mbar_wait(&empty[st], ((it / GM_STAGES) & 1u) ^ 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * bytes);
+                    const uint32_t bar = cluster_addr(&full[st], 0);
+                    uint8_t *sa = ring + st * GM_STAGE, *sb = sa + GM_A_BYTES;
+                    const bool seg = kb >= a.nk[0];
+                    const int ks = (seg ? kb - a.nk[0] : kb) * SLAB_K;
+                    const int ka = ks + (seg ? a.a_seg : 0), kk = ks + (seg ? a.b_seg : 0);
+                    if constexpr (A_MN) {
+                        tma_load_2d_pair(sa, &maps.a, bar, m0, ka);
+                        tma_load_2d_pair(sa + 8192, &maps.a, bar, m0 + 64, ka);
+                    } else {
+                        tma_load_2d_pair(sa, &maps.a, bar, ka, m0);
+                    }
+                    if constexpr (B_MN) {
+                        for (int j = 0; j < nb; ++j) tma_load_2d_pair(sb + j * 8192, &maps.b, bar, n0 + 64 * j, kk);
+                    } else {
+                        tma_load_2d_pair(sb, &maps.b, bar, kk, n0);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = idesc_f16_f32(256, a.bn, BF16) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+            const uint32_t ring0 = smem_u32(ring);
+            uint32_t it = 0, ti = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs, ++ti) {
+                const uint32_t h = ti & 1u;
+                if (!mbar_wait(&acc_empty[h], ((ti >> 1) & 1u) ^ 1u, abort_flag)) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + h * 256;
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const uint32_t st = it % GM_STAGES;
+                    if (!mbar_wait(&full[st], (it / GM_STAGES) & 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = ring0 + st * GM_STAGE, sb = sa + GM_A_BYTES;
+#pragma unroll
+                    for (int k = 0; k < SLAB_K / 16; ++k)
+                        umma_f16_pair(d, A_MN ? sdesc_mnmajor_sw128(sa + k * 2048) : sdesc_kmajor_sw128(sa + k * 32),
+                                      B_MN ? sdesc_mnmajor_sw128(sb + k * 2048) : sdesc_kmajor_sw128(sb + k * 32),
+                                      idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                    umma_commit_pair(&empty[st], 0x3);
+                }
+                if (ok) umma_commit_pair(&acc_full[h], 0x3);
+            }
+            umma_commit_pair(drain, 0x3);
+        }
+        __syncwarp();
+    } else if (warp >= GM_EPI_WARP0) {
+        const int quad = warp & 3;
+        uint32_t ti = 0;
+        for (int t = pair; t < tiles; t += pairs, ++ti) {
+            const Tile tl = decode_tile(t, a.mt, a.nt);
+            const uint32_t h = ti & 1u;
+            const bool ok = mbar_wait_sleep(&acc_full[h], (ti >> 1) & 1u, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const uint32_t acc = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + h * 256;
+            const int64_t row = static_cast<int64_t>(tl.m) * 256 + rank * 128 + quad * 32 + lane;
+            if constexpr (EPI == EPI_GATED) epi_gated(a, acc, row, static_cast<int64_t>(tl.n) * bh);
+            if constexpr (EPI == EPI_GATED_BWD) epi_gated_bwd(a, acc, row, static_cast<int64_t>(tl.n) * bh);
+            if constexpr (EPI == EPI_OUT) epi_out(a, acc, row, static_cast<int64_t>(tl.n) * a.bn);
+            if constexpr (EPI == EPI_CE) epi_ce(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, tl.n);
+            if constexpr (EPI == EPI_CE_BWD) epi_ce_bwd(a, acc, row, static_cast<int64_t>(tl.n) * a.bn);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[h], 0));
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    // Every pair MMA has finished (the leader's last commit reaches both CTAs) before TMEM is
+    // freed, and neither CTA leaves while the other may still signal its barriers or read its
+    // shared memory.
+    if (warp == 1 && lane == 0) mbar_wait_drain(drain, 0);
+    __syncwarp();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, GM_TMEM);
+    }
+}
+
+template <int EPI, bool BF16, bool A_MN, bool B_MN>
+cudaError_t launch_t(const GemmMaps &maps, const GemmArgs &a, int num_sms, cudaStream_t st) {
+    auto *kernel = gemm16_kernel<EPI, BF16, A_MN, B_MN>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(GM_THREADS);
+    cfg.dynamicSmemBytes = GM_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // Persistent: as many pairs as can be resident at once (one CTA per SM).
+    static int max_pairs[64] = {};
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int pairs = dev >= 0 && dev < 64 ? max_pairs[dev] : 0;
+    if (pairs == 0) {
+        cfg.gridDim = dim3(static_cast<unsigned>(2 * (num_sms / 2)));
+        e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
+        if (e != cudaSuccess) return e;
+        if (pairs < 1) return cudaErrorInvalidConfiguration;
+        if (dev >= 0 && dev < 64) max_pairs[dev] = pairs;
+    }
+    const int tiles = a.mt * a.nt;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
+    return cudaLaunchKernelEx(&cfg, kernel, maps, a);
+}
+
+}  // namespace
+
+// Tile columns: of the multiples of 32 up to 256 the one with the fewest waves x width.
+int gemm_tile_cols(int64_t M, int64_t N, int num_sms) {
+    const int64_t mt = (M + 255) / 256, pairs = num_sms / 2;
+    int best = 256;
+    int64_t cost = INT64_MAX;
+    for (int bn = 256; bn >= 64; bn -= 32) {
+        const int64_t tiles = mt * ((N + bn - 1) / bn);
+        const int64_t c = (tiles + pairs - 1) / pairs * bn;
+        if (c < cost) {
+            cost = c;
+            best = bn;
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, const GemmArgs &a, int num_sms,
+                          cudaStream_t st) {
+    switch (epi) {
+        case EPI_GATED: return launch_t<EPI_GATED, false, false, false>(maps, a, num_sms, st);
+        case EPI_GATED_BWD: return launch_t<EPI_GATED_BWD, false, false, false>(maps, a, num_sms, st);
+        case EPI_CE: return launch_t<EPI_CE, true, false, false>(maps, a, num_sms, st);
+        case EPI_CE_BWD: return launch_t<EPI_CE_BWD, true, false, false>(maps, a, num_sms, st);
+        default:
+            if (a_mn) return launch_t<EPI_OUT, true, true, true>(maps, a, num_sms, st);
+            return bf16 ? launch_t<EPI_OUT, true, false, true>(maps, a, num_sms, st)
+                        : launch_t<EPI_OUT, false, false, true>(maps, a, num_sms, st);
+    }
+}
+
+// ------------------------------------------------------------------ cross entropy, last step
+namespace {
+
+// One warp per token: the tiles' (maximum, sum) pairs to the log of the sum of exponentials, in
+// the order of the tiles for each lane and by a fixed tree across lanes.
+__global__ void __launch_bounds__(256) ce_final_kernel(const float2 *__restrict__ part, int nt, int64_t M,
+                                                       const int64_t *__restrict__ labels, int64_t V,
+                                                       const float *__restrict__ tgt, float *__restrict__ loss,
+                                                       float *__restrict__ lse) {
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (m >= M) return;
+    float mx = -INFINITY, sum = 0.0f;
+    for (int t = lane; t < nt; t += 32) {
+        const float2 p = __ldg(part + static_cast<int64_t>(t) * M + m);
+        const float nm = fmaxf(mx, p.x), ref = nm == -INFINITY ? 0.0f : nm;
+        sum = sum * exp2f((mx - ref) * LOG2E) + p.y * exp2f((p.x - ref) * LOG2E);
+        mx = nm;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, mx, off), os = __shfl_xor_sync(0xffffffffu, sum, off);
+        const float nm = fmaxf(mx, om), ref = nm == -INFINITY ? 0.0f : nm;
+        sum = sum * exp2f((mx - ref) * LOG2E) + os * exp2f((om - ref) * LOG2E);
+        mx = nm;
+    }
+    if (lane == 0) {
+        const float l = mx + logf(sum);
+        const int64_t lab = __ldg(labels + m);
+        lse[m] = l;
+        loss[m] = lab >= 0 && lab < V ? l - __ldg(tgt + m) : 0.0f;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_ce_final(const float2 *part, int nt, int64_t M, const int64_t *labels, int64_t V,
+                            const float *tgt, float *loss, float *lse, cudaStream_t st) {
+    ce_final_kernel<<<static_cast<unsigned>((M + 7) / 8), 256, 0, st>>>(part, nt, M, labels, V, tgt, loss, lse);
+    return cudaGetLastError();
+}
+
+}  // namespace awq
