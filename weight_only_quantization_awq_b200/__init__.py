@@ -478,15 +478,20 @@ def _apart(out: torch.Tensor, name: str, *inputs):
             raise ValueError(f"{name} overlaps an input")
 
 
+def _gated_operands(x, qweight, scales, zeros, s16, group_size: int):
+    """The operands of a joint gate and up matrix: an even number of rows.  Returns 2F."""
+    if qweight.dim() == 2 and qweight.shape[0] % 2:
+        raise ValueError(f"qweight has {qweight.shape[0]} rows; gate and up need an even number")
+    return _w4a16_operands(x, qweight, scales, zeros, s16, group_size)
+
+
 def awq_gated_w4a16(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
                     zeros: torch.Tensor | None, s16: torch.Tensor | None, group_size: int = 128,
                     act: str = "silu", out: torch.Tensor | None = None):
     """h [M, F] bf16 = act(g) * u with (g | u) = (x / s16) @ dequant(W)^T for bf16 x [M, in] and
     the packed joint gate and up matrix W [2F, in] (gate rows first).  act: 'silu', 'gelu' or
     'gelu_tanh'.  s16=None when x has already been divided by s."""
-    out_f = _w4a16_operands(x, qweight, scales, zeros, s16, group_size)
-    if out_f % 2:
-        raise ValueError(f"qweight has {out_f} rows; gate and up need an even number")
+    out_f = _gated_operands(x, qweight, scales, zeros, s16, group_size)
     M, inp = x.shape
     a = _act_code(act)
     if out is None:
@@ -506,9 +511,7 @@ def awq_gated_w4a16_grad(dh: torch.Tensor, x: torch.Tensor, qweight: torch.Tenso
                          act: str = "silu", out: torch.Tensor | None = None):
     """dx [M, in] bf16, the gradient of awq_gated_w4a16 with respect to x, for bf16 dh [M, F]; the
     packed weights are frozen, and g and u are computed again from x."""
-    out_f = _w4a16_operands(x, qweight, scales, zeros, s16, group_size)
-    if out_f % 2:
-        raise ValueError(f"qweight has {out_f} rows; gate and up need an even number")
+    out_f = _gated_operands(x, qweight, scales, zeros, s16, group_size)
     M, inp = x.shape
     _rows(dh, "dh", x, M, out_f // 2)
     a = _act_code(act)
