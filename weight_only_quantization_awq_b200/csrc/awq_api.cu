@@ -834,7 +834,7 @@ static awq_status_t gated_dense(const uint16_t *dh, const uint16_t *x, int64_t M
     int *grow = dh ? ws.take<int>(M) : nullptr;
     uint16_t *d16 = dh ? ws.take<uint16_t>(M * 2 * Fp) : nullptr;
     AWQ_CUDA(awq::launch_rows16(x, s16, M, in, in, dh, F, scales, O * (in / group_size), xs, sx, grow, dmax, st));
-    AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, O, in, group_size, dmax, w16, sms, st));
+    AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, O, in, group_size, dmax, w16, st));
     awq::GemmArgs a{};
     a.M = M;
     a.bn = awq::gemm_tile_cols(M, 2 * (dh ? Fp : F), sms);
@@ -937,7 +937,7 @@ awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, in
     uint16_t *w16 = ws.take<uint16_t>(out * in);
     AWQ_CUDA(awq::launch_rows16(dy, nullptr, M, out, ld, nullptr, 0, scales, out * (in / group_size), d16, sx, nullptr,
                                 dmax, st));
-    AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, out, in, group_size, dmax, w16, sms, st));
+    AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, out, in, group_size, dmax, w16, st));
     awq::GemmArgs b{};
     b.M = M;
     b.N = in;

@@ -247,7 +247,7 @@ cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int
                           const uint16_t *dh, int64_t F, const uint16_t *scales, int64_t n_scales, uint16_t *out,
                           float *sx, int *grow, unsigned *dmax, cudaStream_t st);
 cudaError_t launch_dequant(const uint32_t *q, const uint16_t *scales, const uint32_t *zeros, int64_t O, int64_t I,
-                           int gs, const unsigned *dmax, uint16_t *out, int num_sms, cudaStream_t st);
+                           int gs, const unsigned *dmax, uint16_t *out, cudaStream_t st);
 cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t V, int64_t M, int64_t I,
                                uint16_t *out, int num_sms, cudaStream_t st);
 

@@ -99,6 +99,25 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t *bar, uint32_t parity,
     return mbar_wait(bar, parity, abort_flag, limit);
 }
 
+// The same wait by a whole converged warp, with one outcome for all its lanes.  The loops that
+// issue tcgen05.mma and TMA copies run warp-wide with it, one elected lane issuing: their
+// counters and descriptors then stay in uniform registers, where the instructions want them.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                               long long limit = AWQ_WAIT_CYCLES) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit));
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Same, ignoring the abort flag (used only to drain in-flight copies on exit).
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t *bar, uint32_t parity,
                                                 long long limit = AWQ_WAIT_CYCLES) {

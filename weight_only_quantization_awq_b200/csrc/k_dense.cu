@@ -15,13 +15,18 @@
 // CTA pairs (clusters of two, one CTA per SM, persistent over output tiles): a tile is 256 rows
 // x bn columns (bn <= 256, a multiple of 32) on tcgen05.mma.cta_group::2, M = 256, N = bn,
 // K = 16.  Each CTA stages its own 128 rows of A and half of B's columns, 64 deep, by TMA into a
-// six-stage ring of 32 KB; the accumulator has two 256-column halves of TMEM, so the epilogue of a
+// 192 KB ring (six stages at bn = 256); the accumulator has two 256-column halves of TMEM, so the epilogue of a
 // tile overlaps the main loop of the next.  Warps: 0 TMA, 1 MMA, 4-7 epilogue (lane = row).
 // A K-major operand lies as [rows][64 k] in 128-byte swizzled rows; an operand read along its
 // rows (MN-major) as blocks of [64 k][64 n], 8 KB each, in the same swizzle.
 //
 // Tiles are walked in bands of eight row tiles, the row tile fastest, so the pairs that run at
 // one time share a few column tiles of B and one band of A in L2.
+//
+// The TMA and MMA warps run their loops warp-wide, one elected lane issuing, so that ring counters
+// and descriptors live in uniform registers.  With one lane running the loop alone, a slab took
+// at least 570 cycles whatever its width, and a 2048 x 32000 x 4096 product 359 us; so it is 326 us
+// (1645 TFLOP/s, 99% of the measured 1652).
 //
 // Every wait is bounded, as in the other kernels: a CTA that gives up raises its abort flag,
 // waits (bounded) for its MMAs and leaves without writing its remaining tiles.
@@ -36,16 +41,15 @@ namespace awq {
 
 namespace {
 
-constexpr int GM_STAGES = 6;
+constexpr int GM_MAX_STAGES = 12;
 constexpr int GM_A_BYTES = 128 * SLAB_K * 2;          // 16 KB: this CTA's rows of A
-constexpr int GM_B_BYTES = 128 * SLAB_K * 2;          // 16 KB: this CTA's columns of B
-constexpr int GM_STAGE = GM_A_BYTES + GM_B_BYTES;
+constexpr int GM_RING = 192 * 1024;                   // operand ring
 constexpr int GM_THREADS = 256;
 constexpr int GM_EPI_WARP0 = 4;
 constexpr int GM_BAND = 8;                            // row tiles walked together
 constexpr uint32_t GM_TMEM = 512;
-constexpr int GM_BARS = 2 * GM_STAGES + 4 + 1;
-constexpr int GM_SMEM = 1024 + GM_STAGES * GM_STAGE + GM_BARS * 8 + 16;
+constexpr int GM_BARS = 2 * GM_MAX_STAGES + 4 + 1;
+constexpr int GM_SMEM = 1024 + GM_RING + GM_BARS * 8 + 16;
 static_assert(GM_SMEM <= 232448, "shared memory plan");
 
 // Shared-memory descriptor of an MN-major operand in the 128-byte swizzle: blocks of 64
@@ -281,9 +285,9 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(ring + GM_STAGES * GM_STAGE);
-    uint64_t *empty = full + GM_STAGES;
-    uint64_t *acc_full = empty + GM_STAGES;            // [2]: accumulator halves
+    uint64_t *full = reinterpret_cast<uint64_t *>(ring + GM_RING);
+    uint64_t *empty = full + GM_MAX_STAGES;
+    uint64_t *acc_full = empty + GM_MAX_STAGES;            // [2]: accumulator halves
     uint64_t *acc_empty = acc_full + 2;                // [2]
     uint64_t *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
@@ -294,9 +298,13 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int tiles = a.mt * a.nt;
     const int nk = a.nk[0] + a.nk[1];                  // 64-deep slabs of both K segments
+    const int bh = a.bn / 2;                           // B columns of this CTA
+    const int nb = (bh + 63) / 64;                     // blocks of 64 columns when B is MN-major
+    const uint32_t stage = GM_A_BYTES + (B_MN ? nb * 8192 : (bh * 128 + 1023) / 1024 * 1024);
+    const int fit = static_cast<int>(GM_RING / stage), stages = fit < GM_MAX_STAGES ? fit : GM_MAX_STAGES;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < GM_STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(&full[s], 1);                    // the leader's expect_tx; bytes of both CTAs
             mbar_init(&empty[s], 1);                   // the leader's multicast commit
         }
@@ -320,32 +328,27 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int bh = a.bn / 2;                           // B columns of this CTA
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            const int nb = B_MN ? (bh + 63) / 64 : 1;  // blocks of 64 columns when B is MN-major
-            const uint32_t bytes = GM_A_BYTES + (B_MN ? nb * 8192 : bh * 128);
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                const Tile tl = decode_tile(t, a.mt, a.nt);
-                const int m0 = tl.m * 256 + static_cast<int>(rank) * 128;
-                const int n0 = EPI == EPI_GATED || EPI == EPI_GATED_BWD
-                                   ? tl.n * bh + static_cast<int>(rank) * static_cast<int>(a.F)   // gate | up rows
-                                   : tl.n * a.bn + static_cast<int>(rank) * bh;
-                for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const uint32_t st = it % GM_STAGES;
-                    if (!mbar_wait(&empty[st], ((it / GM_STAGES) & 1u) ^ 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
+        uint32_t st = 0, ph = 1;
+        bool ok = true;
+        const uint32_t bytes = GM_A_BYTES + (B_MN ? nb * 8192 : bh * 128);
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            const Tile tl = decode_tile(t, a.mt, a.nt);
+            const int m0 = tl.m * 256 + static_cast<int>(rank) * 128;
+            const int n0 = EPI == EPI_GATED || EPI == EPI_GATED_BWD
+                               ? tl.n * bh + static_cast<int>(rank) * static_cast<int>(a.F)   // gate | up rows
+                               : tl.n * a.bn + static_cast<int>(rank) * bh;
+            for (int kb = 0; kb < nk; ++kb) {
+                ok = mbar_wait_warp(&empty[st], ph, abort_flag);
+                if (!ok) break;
+                const uint32_t bar = cluster_addr(&full[st], 0);
+                uint8_t *sa = ring + st * stage, *sb = sa + GM_A_BYTES;
+                const bool seg = kb >= a.nk[0];
+                const int ks = (seg ? kb - a.nk[0] : kb) * SLAB_K;
+                const int ka = ks + (seg ? a.a_seg : 0), kk = ks + (seg ? a.b_seg : 0);
+                if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * bytes);
-                    const uint32_t bar = cluster_addr(&full[st], 0);
-                    uint8_t *sa = ring + st * GM_STAGE, *sb = sa + GM_A_BYTES;
-                    const bool seg = kb >= a.nk[0];
-                    const int ks = (seg ? kb - a.nk[0] : kb) * SLAB_K;
-                    const int ka = ks + (seg ? a.a_seg : 0), kk = ks + (seg ? a.b_seg : 0);
                     if constexpr (A_MN) {
                         tma_load_2d_pair(sa, &maps.a, bar, m0, ka);
                         tma_load_2d_pair(sa + 8192, &maps.a, bar, m0 + 64, ka);
@@ -353,45 +356,55 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
                         tma_load_2d_pair(sa, &maps.a, bar, ka, m0);
                     }
                     if constexpr (B_MN) {
-                        for (int j = 0; j < nb; ++j) tma_load_2d_pair(sb + j * 8192, &maps.b, bar, n0 + 64 * j, kk);
+                        tma_load_2d_pair(sb, &maps.b, bar, n0, kk);
+                        if (nb > 1) tma_load_2d_pair(sb + 8192, &maps.b, bar, n0 + 64, kk);
                     } else {
                         tma_load_2d_pair(sb, &maps.b, bar, kk, n0);
                     }
                 }
+                __syncwarp();
+                if (++st == static_cast<uint32_t>(stages)) {
+                    st = 0;
+                    ph ^= 1u;
+                }
             }
         }
-        __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             const uint32_t idesc = idesc_f16_f32(256, a.bn, BF16) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
             const uint32_t ring0 = smem_u32(ring);
-            uint32_t it = 0, ti = 0;
+            uint32_t st = 0, ph = 0, ti = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs, ++ti) {
                 const uint32_t h = ti & 1u;
-                if (!mbar_wait(&acc_empty[h], ((ti >> 1) & 1u) ^ 1u, abort_flag)) break;
+                ok = mbar_wait_warp(&acc_empty[h], ((ti >> 1) & 1u) ^ 1u, abort_flag);
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + h * 256;
-                for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const uint32_t st = it % GM_STAGES;
-                    if (!mbar_wait(&full[st], (it / GM_STAGES) & 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
+                for (int kb = 0; kb < nk; ++kb) {
+                    ok = mbar_wait_warp(&full[st], ph, abort_flag);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sa = ring0 + st * GM_STAGE, sb = sa + GM_A_BYTES;
+                    const uint32_t sa = ring0 + st * stage, sb = sa + GM_A_BYTES;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < SLAB_K / 16; ++k)
-                        umma_f16_pair(d, A_MN ? sdesc_mnmajor_sw128(sa + k * 2048) : sdesc_kmajor_sw128(sa + k * 32),
-                                      B_MN ? sdesc_mnmajor_sw128(sb + k * 2048) : sdesc_kmajor_sw128(sb + k * 32),
-                                      idesc, (kb > 0 || k > 0) ? 1u : 0u);
-                    umma_commit_pair(&empty[st], 0x3);
+                        for (int k = 0; k < SLAB_K / 16; ++k)
+                            umma_f16_pair(d, A_MN ? sdesc_mnmajor_sw128(sa + k * 2048) : sdesc_kmajor_sw128(sa + k * 32),
+                                          B_MN ? sdesc_mnmajor_sw128(sb + k * 2048) : sdesc_kmajor_sw128(sb + k * 32),
+                                          idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                        umma_commit_pair(&empty[st], 0x3);
+                        if (kb == nk - 1) umma_commit_pair(&acc_full[h], 0x3);
+                    }
+                    __syncwarp();
+                    if (++st == static_cast<uint32_t>(stages)) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
-                if (ok) umma_commit_pair(&acc_full[h], 0x3);
             }
-            umma_commit_pair(drain, 0x3);
+            if (elect_one()) umma_commit_pair(drain, 0x3);
+            __syncwarp();
         }
-        __syncwarp();
     } else if (warp >= GM_EPI_WARP0) {
         const int quad = warp & 3;
         uint32_t ti = 0;
@@ -464,14 +477,18 @@ cudaError_t launch_t(const GemmMaps &maps, const GemmArgs &a, int num_sms, cudaS
 
 }  // namespace
 
-// Tile columns: of the multiples of 32 up to 256 the one with the fewest waves x width.
+// Tile columns: of the multiples of 32 up to 256 the one with the least waves x time of a 64-deep
+// slab.  Measured slab times (cycles at 1.9 GHz, 2048 tokens, K-major and MN-major B alike): 64
+// columns 410-450, 128 460-490, 192 530-560, 224 610, 256 690-720: a handshake and the A tile cost
+// about 350 cycles beside one cycle a column, until the MMAs themselves take over at 224.
 int gemm_tile_cols(int64_t M, int64_t N, int num_sms) {
     const int64_t mt = (M + 255) / 256, pairs = num_sms / 2;
     int best = 256;
     int64_t cost = INT64_MAX;
     for (int bn = 256; bn >= 64; bn -= 32) {
         const int64_t tiles = mt * ((N + bn - 1) / bn);
-        const int64_t c = (tiles + pairs - 1) / pairs * bn;
+        const int slab = bn <= 192 ? 350 + bn : 272 * bn / 100;
+        const int64_t c = (tiles + pairs - 1) / pairs * slab;
         if (c < cost) {
             cost = c;
             best = bn;

@@ -14,11 +14,21 @@ namespace {
 // not depend on the order of its terms.
 __device__ __forceinline__ void scales_max(const uint16_t *__restrict__ scales, int64_t n, int64_t first,
                                            int64_t step, unsigned *dmax) {
+    // 16 bytes at a time from the first 16-byte boundary on; the ragged ends one by one
     unsigned mb = 0u;
-    for (int64_t i = first; i < n; i += step) {
-        const unsigned b = __ldg(scales + i) & 0x7FFFu;
-        mb = b > mb ? b : mb;
+    const int64_t head = ((16 - (reinterpret_cast<uintptr_t>(scales) & 15)) & 15) / 2;
+    const int64_t h = head < n ? head : n, vecs = (n - h) / 8;
+    const uint4 *v = reinterpret_cast<const uint4 *>(scales + h);
+    for (int64_t i = first; i < vecs; i += step) {
+        const uint4 q = __ldg(v + i);
+        // two 15-bit magnitudes to a word: the maximum of each half on its own
+        const unsigned m = __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu),
+                                    __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
+        mb = max(mb, max(m >> 16, m & 0xFFFFu));
     }
+    const int64_t rest = h + n - (h + vecs * 8);
+    for (int64_t i = first; i < rest; i += step)
+        mb = max(mb, static_cast<unsigned>(__ldg(scales + (i < h ? i : vecs * 8 + i))) & 0x7FFFu);
     mb = __reduce_max_sync(0xffffffffu, mb);
     if ((threadIdx.x & 31) == 0) atomicMax(dmax, mb);
 }
@@ -44,8 +54,9 @@ __device__ __forceinline__ void row_chunk(const uint16_t *__restrict__ r, const 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const __half2 h = *reinterpret_cast<const __half2 *>(&w[e]);
-            v[2 * e] = v[2 * e] / __low2float(h);
-            v[2 * e + 1] = v[2 * e + 1] / __high2float(h);
+            // (2 ulp: far below the fp16 rounding that follows)
+            v[2 * e] = __fdividef(v[2 * e], __low2float(h));
+            v[2 * e + 1] = __fdividef(v[2 * e + 1], __high2float(h));
         }
     }
 }
@@ -135,7 +146,9 @@ __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict_
 }
 
 // W16[o][i] = fp16((code - z) * Delta * 2^-kW): one rounding, the difference and the power of two
-// are exact.  One packed word (8 columns, one 16-byte store) per thread and step.
+// are exact.  A thread takes DQ_WORDS packed words (8 columns, one 16-byte store each), a block's
+// width apart, so every load and store of a warp is contiguous; their loads are in flight together.
+constexpr int DQ_WORDS = 4;
 __global__ void __launch_bounds__(256) dequant_kernel(const uint32_t *__restrict__ q,
                                                       const uint16_t *__restrict__ scales,
                                                       const uint32_t *__restrict__ zeros, int64_t words, int wpr,
@@ -143,23 +156,42 @@ __global__ void __launch_bounds__(256) dequant_kernel(const uint32_t *__restrict
                                                       uint16_t *__restrict__ out) {
     const float sw = ldexpf(1.0f, -dq_exp(dmax));
     const int nzw = (nG + 7) / 8;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < words; i += step) {
-        const int64_t o = i / wpr;
-        const int w = static_cast<int>(i - o * wpr);
-        const int g = w >> (lg - 3);
-        const uint32_t v = __ldg(q + i);
-        const float d = __half2float(__ushort_as_half(__ldg(scales + o * nG + g))) * sw;
-        const int z = zeros ? (__ldg(zeros + o * nzw + (g >> 3)) >> (4 * (g & 7))) & 15 : 8;
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * (256 * DQ_WORDS);
+    const int64_t o0 = base / wpr;                    // one 64-bit division a block
+    const int w0 = static_cast<int>(base - o0 * wpr);
+    uint32_t v[DQ_WORDS], zw[DQ_WORDS];
+    uint16_t sv[DQ_WORDS];
+    int gz[DQ_WORDS];
+#pragma unroll
+    for (int u = 0; u < DQ_WORDS; ++u) {
+        const int off = u * 256 + threadIdx.x;
+        if (base + off < words) {
+            const int w = w0 + off, dr = w / wpr, g = (w - dr * wpr) >> (lg - 3);
+            const int64_t o = o0 + dr;
+            v[u] = __ldcs(q + base + off);            // read once
+            sv[u] = __ldg(scales + o * nG + g);
+            zw[u] = zeros ? __ldg(zeros + o * nzw + (g >> 3)) : 0x88888888u;
+            gz[u] = 4 * (g & 7);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < DQ_WORDS; ++u) {
+        const int off = u * 256 + threadIdx.x;
+        if (base + off >= words) break;
+        const float d = __half2float(__ushort_as_half(sv[u])) * sw;
+        // nibbles (2e, 2e + 1) beside each other: 1024 + code as fp16 bits, minus (1024 + z) exactly
+        const uint32_t z = (0x6400u | ((zw[u] >> gz[u]) & 15u)) * 0x00010001u;
         uint32_t h[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float a = static_cast<float>(static_cast<int>((v >> (8 * e)) & 15u) - z) * d;
-            const float b = static_cast<float>(static_cast<int>((v >> (8 * e + 4)) & 15u) - z) * d;
-            const __half2 hv = __floats2half2_rn(a, b);
+            const uint32_t b = v[u] >> (8 * e);
+            const uint32_t c = (b & 15u) | ((b << 12) & 0x000F0000u) | 0x64006400u;
+            const __half2 cz = __hsub2(*reinterpret_cast<const __half2 *>(&c), *reinterpret_cast<const __half2 *>(&z));
+            const float2 f = __half22float2(cz);
+            const __half2 hv = __floats2half2_rn(f.x * d, f.y * d);
             h[e] = *reinterpret_cast<const uint32_t *>(&hv);
         }
-        *reinterpret_cast<uint4 *>(out + i * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(out + (base + off) * 8) = make_uint4(h[0], h[1], h[2], h[3]);
     }
 }
 
@@ -190,17 +222,17 @@ cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int
                           float *sx, int *grow, unsigned *dmax, cudaStream_t st) {
     cudaError_t e = cudaMemsetAsync(dmax, 0, sizeof(unsigned), st);
     if (e != cudaSuccess) return e;
-    const int64_t extra = (n_scales + 2047) / 2048 < 148 ? (n_scales + 2047) / 2048 : 148;
+    const int64_t extra = (n_scales + 8191) / 8192 < 148 ? (n_scales + 8191) / 8192 : 148;
     rows16_kernel<<<static_cast<unsigned>(M + extra), 256, 0, st>>>(x, s16, M, cols, ld, dh, F, scales, n_scales, out,
                                                                      sx, grow, dmax);
     return cudaGetLastError();
 }
 
 cudaError_t launch_dequant(const uint32_t *q, const uint16_t *scales, const uint32_t *zeros, int64_t O, int64_t I,
-                           int gs, const unsigned *dmax, uint16_t *out, int num_sms, cudaStream_t st) {
+                           int gs, const unsigned *dmax, uint16_t *out, cudaStream_t st) {
     const int64_t words = O * (I / 8);
-    const int64_t blocks = (words + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
-    dequant_kernel<<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, st>>>(
+    const int64_t blocks = (words + 256 * DQ_WORDS - 1) / (256 * DQ_WORDS);
+    dequant_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
         q, scales, zeros, words, static_cast<int>(I / 8), gs == 32 ? 5 : (gs == 64 ? 6 : 7), static_cast<int>(I / gs),
         dmax, out);
     return cudaGetLastError();
