@@ -478,11 +478,42 @@ def _apart(out: torch.Tensor, name: str, *inputs):
             raise ValueError(f"{name} overlaps an input")
 
 
+def _fits(x, cols, qweight, scales, zeros, s16, group_size: int, dev: int) -> bool:
+    """Whether a packed layer's operands are what _w4a16_operands asks for, in one expression: a
+    decode-sized call spends less time in its kernel than in checks that name each fault."""
+    if group_size <= 0 or qweight.dim() != 2:
+        return False
+    out_f, words = qweight.shape
+    inp = words * 8
+    nG = inp // group_size
+    return (x.dim() == 2 and x.dtype == torch.bfloat16 and x.shape[1] == (cols or inp) and inp % group_size == 0
+            and x.get_device() == dev and x.is_contiguous()
+            and qweight.element_size() == 4 and qweight.get_device() == dev and qweight.is_contiguous()
+            and scales.element_size() == 2 and scales.numel() == out_f * nG and scales.get_device() == dev
+            and scales.is_contiguous()
+            and (zeros is None or (zeros.element_size() == 4 and zeros.numel() == out_f * ((nG + 7) // 8)
+                                   and zeros.get_device() == dev and zeros.is_contiguous()))
+            and (s16 is None or (s16.element_size() == 2 and s16.numel() == inp and s16.get_device() == dev
+                                 and s16.is_contiguous())))
+
+
+def _launch(name: str, fn, dev: int, *args) -> None:
+    """Call `fn` on the current stream of device `dev`, with `dev` the current device."""
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    _check(name, st)
+
+
 def _gated_operands(x, qweight, scales, zeros, s16, group_size: int):
-    """The operands of a joint gate and up matrix: an even number of rows.  Returns 2F."""
+    """The operands of a joint gate and up matrix: an even number of rows.  Returns F."""
     if qweight.dim() == 2 and qweight.shape[0] % 2:
         raise ValueError(f"qweight has {qweight.shape[0]} rows; gate and up need an even number")
-    return _w4a16_operands(x, qweight, scales, zeros, s16, group_size)
+    if not (x.is_cuda and _fits(x, 0, qweight, scales, zeros, s16, group_size, x.get_device())):
+        _w4a16_operands(x, qweight, scales, zeros, s16, group_size)
+    return qweight.shape[0] // 2
 
 
 def awq_gated_w4a16(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
@@ -491,18 +522,16 @@ def awq_gated_w4a16(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor
     """h [M, F] bf16 = act(g) * u with (g | u) = (x / s16) @ dequant(W)^T for bf16 x [M, in] and
     the packed joint gate and up matrix W [2F, in] (gate rows first).  act: 'silu', 'gelu' or
     'gelu_tanh'.  s16=None when x has already been divided by s."""
-    out_f = _gated_operands(x, qweight, scales, zeros, s16, group_size)
+    F = _gated_operands(x, qweight, scales, zeros, s16, group_size)
     M, inp = x.shape
     a = _act_code(act)
     if out is None:
-        out = torch.empty((M, out_f // 2), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((M, F))
     else:
-        _out(out, "out", x, torch.bfloat16, M * (out_f // 2))
+        _out(out, "out", x, torch.bfloat16, M * F)
         _apart(out, "out", x, qweight, scales, zeros, s16)
-    with torch.cuda.device(x.device):
-        st = lib.awq_gated_w4a16(x.data_ptr(), M, inp, out_f // 2, qweight.data_ptr(), scales.data_ptr(),
-                                 _ptr(zeros), _ptr(s16), group_size, a, out.data_ptr(), _stream(x))
-    _check("awq_gated_w4a16", st)
+    _launch("awq_gated_w4a16", lib.awq_gated_w4a16, x.get_device(), x.data_ptr(), M, inp, F, qweight.data_ptr(),
+            scales.data_ptr(), _ptr(zeros), _ptr(s16), group_size, a, out.data_ptr())
     return out
 
 
@@ -511,20 +540,17 @@ def awq_gated_w4a16_grad(dh: torch.Tensor, x: torch.Tensor, qweight: torch.Tenso
                          act: str = "silu", out: torch.Tensor | None = None):
     """dx [M, in] bf16, the gradient of awq_gated_w4a16 with respect to x, for bf16 dh [M, F]; the
     packed weights are frozen, and g and u are computed again from x."""
-    out_f = _gated_operands(x, qweight, scales, zeros, s16, group_size)
+    F = _gated_operands(x, qweight, scales, zeros, s16, group_size)
     M, inp = x.shape
-    _rows(dh, "dh", x, M, out_f // 2)
+    _rows(dh, "dh", x, M, F)
     a = _act_code(act)
     if out is None:
-        out = torch.empty((M, inp), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((M, inp))
     else:
         _out(out, "out", x, torch.bfloat16, M * inp)
         _apart(out, "out", dh, x, qweight, scales, zeros, s16)
-    with torch.cuda.device(x.device):
-        st = lib.awq_gated_w4a16_grad(dh.data_ptr(), x.data_ptr(), M, inp, out_f // 2, qweight.data_ptr(),
-                                      scales.data_ptr(), _ptr(zeros), _ptr(s16), group_size, a,
-                                      out.data_ptr(), _stream(x))
-    _check("awq_gated_w4a16_grad", st)
+    _launch("awq_gated_w4a16_grad", lib.awq_gated_w4a16_grad, x.get_device(), dh.data_ptr(), x.data_ptr(), M, inp, F,
+            qweight.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(s16), group_size, a, out.data_ptr())
     return out
 
 
@@ -535,19 +561,18 @@ def awq_linear_w4a16_grad(dy: torch.Tensor, qweight: torch.Tensor, scales: torch
     awq_linear_w4a16 with respect to x, the packed weights frozen."""
     if dy.dim() != 2 or qweight.dim() != 2:
         raise ValueError("dy and qweight must be 2-D")
-    M, inp = dy.shape[0], qweight.shape[1] * 8
+    M, inp, out_f = dy.shape[0], qweight.shape[1] * 8, qweight.shape[0]
     if out is None:
         out = torch.empty((M, inp), dtype=torch.bfloat16, device=dy.device)
     else:
         _out(out, "out", dy, torch.bfloat16, M * inp)
         _apart(out, "out", dy, qweight, scales, zeros, s16)
-    # the layer's operands against the [M, in] side, then dy against its output side
-    out_f = _w4a16_operands(out.view(M, inp), qweight, scales, zeros, s16, group_size)
-    _rows(dy, "dy", out, M, out_f)
-    with torch.cuda.device(dy.device):
-        st = lib.awq_linear_w4a16_grad(dy.data_ptr(), M, inp, out_f, qweight.data_ptr(), scales.data_ptr(),
-                                       _ptr(zeros), _ptr(s16), group_size, out.data_ptr(), _stream(dy))
-    _check("awq_linear_w4a16_grad", st)
+    if not (dy.is_cuda and _fits(dy, out_f, qweight, scales, zeros, s16, group_size, dy.get_device())):
+        # the layer's operands against the [M, in] side, then dy against its output side
+        _w4a16_operands(out.view(M, inp), qweight, scales, zeros, s16, group_size)
+        _rows(dy, "dy", out, M, out_f)
+    _launch("awq_linear_w4a16_grad", lib.awq_linear_w4a16_grad, dy.get_device(), dy.data_ptr(), M, inp, out_f,
+            qweight.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(s16), group_size, out.data_ptr())
     return out
 
 
@@ -574,10 +599,8 @@ def awq_cross_entropy(x: torch.Tensor, W: torch.Tensor, labels: torch.Tensor):
     M, inp, V = _ce_operands(x, W, labels)
     loss = torch.empty(M, dtype=torch.float32, device=x.device)
     lse = torch.empty(M, dtype=torch.float32, device=x.device)
-    with torch.cuda.device(x.device):
-        st = lib.awq_cross_entropy(x.data_ptr(), M, inp, W.data_ptr(), V, labels.data_ptr(),
-                                   loss.data_ptr(), lse.data_ptr(), _stream(x))
-    _check("awq_cross_entropy", st)
+    _launch("awq_cross_entropy", lib.awq_cross_entropy, x.get_device(), x.data_ptr(), M, inp, W.data_ptr(), V,
+            labels.data_ptr(), loss.data_ptr(), lse.data_ptr())
     return loss, lse
 
 
@@ -602,8 +625,6 @@ def awq_cross_entropy_grad(x: torch.Tensor, W: torch.Tensor, labels: torch.Tenso
     elif want_dw:
         _out(dW, "dW", x, torch.bfloat16, V * inp)
         _apart(dW, "dW", x, W, labels, lse, dloss)
-    with torch.cuda.device(x.device):
-        st = lib.awq_cross_entropy_grad(x.data_ptr(), M, inp, W.data_ptr(), V, labels.data_ptr(), lse.data_ptr(),
-                                        dloss.data_ptr(), dx.data_ptr(), _ptr(dW), _stream(x))
-    _check("awq_cross_entropy_grad", st)
+    _launch("awq_cross_entropy_grad", lib.awq_cross_entropy_grad, x.get_device(), x.data_ptr(), M, inp, W.data_ptr(), V,
+            labels.data_ptr(), lse.data_ptr(), dloss.data_ptr(), dx.data_ptr(), _ptr(dW))
     return dx, dW

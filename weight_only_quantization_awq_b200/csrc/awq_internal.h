@@ -251,6 +251,14 @@ cudaError_t launch_dequant(const uint32_t *q, const uint16_t *scales, const uint
 cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t V, int64_t M, int64_t I,
                                uint16_t *out, int num_sms, cudaStream_t st);
 
+// ---- gated feed-forward for decode-sized M (k_gated_dec.cu); supported: the staged activations
+// and two tiles' scales fit one SM's shared memory
+constexpr int64_t GATED_DEC_MAX_M = 16;
+bool gated_dec_supported(int64_t M, int64_t I, int gs);
+cudaError_t launch_gated_dec(const uint16_t *x, int64_t M, int64_t I, int64_t F, const uint32_t *q,
+                             const uint16_t *scales, const uint32_t *zeros, const uint16_t *s16, int gs, int act,
+                             uint16_t *h, int num_sms, cudaStream_t st);
+
 // ---- fold of 1/s into the previous operator: out[r][c] = P[r][c] / s16[r]
 // (one IEEE fp32 division, then bf16 rounding when bf16).
 cudaError_t launch_fold_scale(const void *P, bool bf16, int64_t R, int64_t C, const uint16_t *s16,
