@@ -833,7 +833,8 @@ static awq_status_t gated_dense(const uint16_t *dh, const uint16_t *x, int64_t M
     uint16_t *w16 = ws.take<uint16_t>(O * in);
     int *grow = dh ? ws.take<int>(M) : nullptr;
     uint16_t *d16 = dh ? ws.take<uint16_t>(M * 2 * Fp) : nullptr;
-    AWQ_CUDA(awq::launch_rows16(x, s16, M, in, in, dh, F, scales, O * (in / group_size), xs, sx, grow, dmax, st));
+    AWQ_CUDA(awq::launch_rows16(x, s16, M, in, in, dh, F, scales, O * (in / group_size), false, xs, sx, grow,
+                                dmax, 1, st));
     AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, O, in, group_size, dmax, w16, st));
     awq::GemmArgs a{};
     a.M = M;
@@ -883,6 +884,65 @@ static awq_status_t gated_dense(const uint16_t *dh, const uint16_t *x, int64_t M
     return AWQ_OK;
 }
 
+// The gated product (dh null) or its gradient for up to a few hundred tokens: the weights are
+// dequantised on the way into the tensor cores.
+static awq_status_t gated_skinny(const uint16_t *dh, const uint16_t *x, int64_t M, int64_t in, int64_t F,
+                                 const uint32_t *qweight, const uint16_t *scales, const uint32_t *zeros,
+                                 const uint16_t *s16, int group_size, int act, uint16_t *out, int sms,
+                                 cudaStream_t st) {
+    const int64_t O = 2 * F, ldd = round64(O);
+    const awq::SkinnyPlan fp = awq::skinny_plan(M, (F + 63) / 64, in, sms);
+    const awq::SkinnyPlan gp = awq::skinny_plan(M, (in + 127) / 128, O, sms);
+    const int64_t parts = dh && gp.part_vecs > fp.part_vecs ? gp.part_vecs : fp.part_vecs;
+    const int64_t words = 1 + fp.counters + (dh ? gp.counters : 0);
+    Workspace ws(st);
+    size_t bytes = Workspace::up(2 * M * in) + Workspace::up(4 * M) + Workspace::up(4 * words) + Workspace::up(16 * parts);
+    if (dh) bytes += Workspace::up(4 * M) + Workspace::up(2 * M * ldd);
+    if (awq_status_t s = ws.reserve(bytes)) return s;
+    uint16_t *xs = ws.take<uint16_t>(M * in);
+    float *sx = ws.take<float>(M);
+    unsigned *dmax = ws.take<unsigned>(words);
+    float4 *part = ws.take<float4>(parts);
+    int *grow = dh ? ws.take<int>(M) : nullptr;
+    uint16_t *d16 = dh ? ws.take<uint16_t>(M * ldd) : nullptr;
+    AWQ_CUDA(awq::launch_rows16(x, s16, M, in, in, dh, F, scales, O * (in / group_size), true, xs, sx, grow, dmax,
+                                words, st));
+    awq::SkinnyArgs a{};
+    a.q = qweight;
+    a.scales = scales;
+    a.zeros = zeros;
+    a.O = O;
+    a.I = in;
+    a.F = F;
+    a.M = M;
+    a.lg = group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
+    a.sx = sx;
+    a.dmax = dmax;
+    a.grow = grow;
+    a.inner = static_cast<int>(in);
+    a.act = act;
+    a.dh = dh;
+    a.out = out;
+    a.d16 = d16;
+    a.ldd = ldd;
+    a.part = part;
+    a.counter = dmax + 1;
+    CUtensorMap map;
+    if (awq_status_t s = map_kmajor(&map, false, xs, in, M, in, fp.n)) return s;
+    kt_reset(4);
+    kt_begin(4, st);
+    AWQ_CUDA(awq::launch_skinny(false, dh ? awq::EPI_GATED_BWD : awq::EPI_GATED, map, a, fp, st));
+    kt_end(4, st);
+    if (!dh) return AWQ_OK;
+    a.s16 = s16;
+    a.counter = dmax + 1 + fp.counters;
+    if (awq_status_t s = map_kmajor(&map, false, d16, O, M, ldd, gp.n)) return s;
+    kt_begin(4, st);
+    AWQ_CUDA(awq::launch_skinny(true, awq::EPI_OUT, map, a, gp, st));
+    kt_end(4, st);
+    return AWQ_OK;
+}
+
 awq_status_t awq_gated_w4a16(const uint16_t *x, int64_t M, int64_t in, int64_t F, const uint32_t *qweight,
                              const uint16_t *scales, const uint32_t *zeros, const uint16_t *s16, int group_size,
                              int act, uint16_t *h, void *stream) {
@@ -903,6 +963,9 @@ awq_status_t awq_gated_w4a16(const uint16_t *x, int64_t M, int64_t in, int64_t F
         kt_end(4, st);
         return AWQ_OK;
     }
+    if (awq::skinny_supported(M, 2 * F, in))
+        return gated_skinny(nullptr, x, M, in, F, qweight, scales, zeros, s16, group_size, act, h, sms,
+                            static_cast<cudaStream_t>(stream));
     return gated_dense(nullptr, x, M, in, F, qweight, scales, zeros, s16, group_size, act, h, sms,
                        static_cast<cudaStream_t>(stream));
 }
@@ -919,6 +982,9 @@ awq_status_t awq_gated_w4a16_grad(const uint16_t *dh, const uint16_t *x, int64_t
     if (!aligned16(dh) || !aligned16(x) || !aligned16(dx)) return fail(AWQ_ERR_ALIGN, "misaligned pointer");
     int sms;
     if (awq_status_t s = device_info(&sms)) return s;
+    if (awq::skinny_supported(M, 2 * F, in))
+        return gated_skinny(dh, x, M, in, F, qweight, scales, zeros, s16, group_size, act, dx, sms,
+                            static_cast<cudaStream_t>(stream));
     return gated_dense(dh, x, M, in, F, qweight, scales, zeros, s16, group_size, act, dx, sms,
                        static_cast<cudaStream_t>(stream));
 }
@@ -935,6 +1001,39 @@ awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, in
     if (awq_status_t s = device_info(&sms)) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t ld = round64(out);
+    if (awq::skinny_supported(M, out, in)) {
+        const awq::SkinnyPlan p = awq::skinny_plan(M, (in + 127) / 128, out, sms);
+        Workspace ws(st);
+        if (awq_status_t s = ws.reserve(Workspace::up(2 * M * ld) + Workspace::up(4 * M) +
+                                        Workspace::up(4 * (1 + p.counters)) + Workspace::up(16 * p.part_vecs)))
+            return s;
+        uint16_t *d16 = ws.take<uint16_t>(M * ld);
+        awq::SkinnyArgs a{};
+        float *sx = ws.take<float>(M);
+        unsigned *dmax = ws.take<unsigned>(1 + p.counters);
+        a.part = ws.take<float4>(p.part_vecs);
+        AWQ_CUDA(awq::launch_rows16(dy, nullptr, M, out, ld, nullptr, 0, scales, out * (in / group_size), false, d16, sx,
+                                    nullptr, dmax, 1 + p.counters, st));
+        a.q = qweight;
+        a.scales = scales;
+        a.zeros = zeros;
+        a.O = out;
+        a.I = in;
+        a.M = M;
+        a.lg = group_size == 32 ? 5 : group_size == 64 ? 6 : 7;
+        a.sx = sx;
+        a.dmax = dmax;
+        a.s16 = s16;
+        a.out = dx;
+        a.counter = dmax + 1;
+        CUtensorMap map;
+        if (awq_status_t s = map_kmajor(&map, false, d16, out, M, ld, p.n)) return s;
+        kt_reset(4);
+        kt_begin(4, st);
+        AWQ_CUDA(awq::launch_skinny(true, awq::EPI_OUT, map, a, p, st));
+        kt_end(4, st);
+        return AWQ_OK;
+    }
     Workspace ws(st);
     if (awq_status_t s = ws.reserve(Workspace::up(2 * M * ld) + Workspace::up(4 * M) + Workspace::up(4) +
                                     Workspace::up(2 * out * in)))
@@ -943,8 +1042,8 @@ awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, in
     float *sx = ws.take<float>(M);
     unsigned *dmax = ws.take<unsigned>(1);
     uint16_t *w16 = ws.take<uint16_t>(out * in);
-    AWQ_CUDA(awq::launch_rows16(dy, nullptr, M, out, ld, nullptr, 0, scales, out * (in / group_size), d16, sx, nullptr,
-                                dmax, st));
+    AWQ_CUDA(awq::launch_rows16(dy, nullptr, M, out, ld, nullptr, 0, scales, out * (in / group_size), false, d16, sx,
+                                nullptr, dmax, 1, st));
     AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, out, in, group_size, dmax, w16, st));
     awq::GemmArgs b{};
     b.M = M;

@@ -242,14 +242,51 @@ cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, c
 cudaError_t launch_ce_final(const float2 *part, int nt, int64_t M, const int64_t *labels, int64_t V,
                             const float *tgt, float *loss, float *lse, cudaStream_t st);
 // Token rows to fp16 with a power-of-two scale each (out [M][ld], sx [M]); dh [M][F] with grow [M]
-// optional; *dmax = the layer's largest |Delta| as fp16 bits.
+// optional; *dmax = the layer's largest |Delta| as fp16 bits.  permute: the columns of each 8 in the
+// order (0,4,1,5,2,6,3,7).  `zeroed` words from dmax on start at zero (dmax itself, tile counters).
 cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int64_t cols, int64_t ld,
-                          const uint16_t *dh, int64_t F, const uint16_t *scales, int64_t n_scales, uint16_t *out,
-                          float *sx, int *grow, unsigned *dmax, cudaStream_t st);
+                          const uint16_t *dh, int64_t F, const uint16_t *scales, int64_t n_scales, bool permute,
+                          uint16_t *out, float *sx, int *grow, unsigned *dmax, int64_t zeroed, cudaStream_t st);
 cudaError_t launch_dequant(const uint32_t *q, const uint16_t *scales, const uint32_t *zeros, int64_t O, int64_t I,
                            int gs, const unsigned *dmax, uint16_t *out, cudaStream_t st);
 cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t V, int64_t M, int64_t I,
                                uint16_t *out, int num_sms, cudaStream_t st);
+
+// ---- products with a packed matrix for up to a few hundred tokens, dequantised on the way into
+// the tensor cores (k_skinny.cu): forward EPI_GATED / EPI_GATED_BWD (64 gate and 64 up rows per tile, K
+// = in), gradient EPI_OUT (128 columns per tile, K = out)
+struct SkinnyPlan {
+    int n, token_tiles;         // tokens per tile (a multiple of 16, <= 256), tiles of tokens
+    int tiles, ks, grid;        // tiles of W, 128-deep stages of K, CTAs
+    int64_t part_vecs, counters;     // workspace: fp32 partial sums, by four; tile counters (zeroed)
+};
+// above SKINNY_MAX_M tokens, or 4 GB of codes: dequantise once, dense products
+constexpr int64_t SKINNY_MAX_M = 512;
+inline bool skinny_supported(int64_t M, int64_t O, int64_t I) { return M <= SKINNY_MAX_M && O * I <= int64_t(1) << 32; }
+SkinnyPlan skinny_plan(int64_t M, int64_t tiles, int64_t k, int num_sms);
+struct SkinnyArgs {
+    const uint32_t *q;
+    const uint16_t *scales;
+    const uint32_t *zeros;
+    int64_t O, I, F, M;
+    int lg;                     // log2 of the group size
+    const float *sx;            // [M]: the token tile's row m carries 1 / sx[m]
+    const unsigned *dmax;       // the layer's largest |Delta| (the weights carry 2^-kW)
+    const int *grow;            // [M] exponent bound of the token's gradients, or null
+    const uint16_t *s16;        // [I]: divides column i (EPI_OUT)
+    int inner, act;
+    const uint16_t *dh;         // [M][F] bf16
+    uint16_t *out;              // bf16 result
+    uint16_t *d16;              // [M][ldd]: gate gradients, then up gradients, fp16
+    int64_t ldd;
+    float4 *part;
+    unsigned *counter;
+    // set by launch_skinny
+    int n, tiles, ks, units, acc_cols, stages;
+};
+// bmap: the tokens' fp16 rows [M][K] (forward: columns of each 8 in the order (0,4,1,5,2,6,3,7)), box 64 x n.
+cudaError_t launch_skinny(bool grad, int epi, const CUtensorMap &bmap, SkinnyArgs a, const SkinnyPlan &p,
+                          cudaStream_t st);
 
 // ---- gated feed-forward for decode-sized M (k_gated_dec.cu); supported: the staged activations
 // and two tiles' scales fit one SM's shared memory

@@ -372,7 +372,9 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
     } else if (warp == 1) {
         if (rank == 0) {
             const uint32_t idesc = idesc_f16_f32(256, a.bn, BF16) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
-            const uint32_t ring0 = smem_u32(ring);
+            const uint32_t ring0 = smem_u32(ring), lead = elect_one() ? 1u : 0u;
+            const uint64_t da0 = A_MN ? sdesc_mnmajor_sw128(ring0) : sdesc_kmajor_sw128(ring0);
+            const uint64_t db0 = B_MN ? sdesc_mnmajor_sw128(ring0 + GM_A_BYTES) : sdesc_kmajor_sw128(ring0 + GM_A_BYTES);
             uint32_t st = 0, ph = 0, ti = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs, ++ti) {
@@ -386,16 +388,13 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t sa = ring0 + st * stage, sb = sa + GM_A_BYTES;
-                    if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < SLAB_K / 16; ++k)
-                            umma_f16_pair(d, A_MN ? sdesc_mnmajor_sw128(sa + k * 2048) : sdesc_kmajor_sw128(sa + k * 32),
+                    for (int k = 0; k < SLAB_K / 16; ++k)
+                        umma_f16_pair_lead(lead, d, A_MN ? sdesc_mnmajor_sw128(sa + k * 2048) : sdesc_kmajor_sw128(sa + k * 32),
                                           B_MN ? sdesc_mnmajor_sw128(sb + k * 2048) : sdesc_kmajor_sw128(sb + k * 32),
-                                          idesc, (kb > 0 || k > 0) ? 1u : 0u);
-                        umma_commit_pair(&empty[st], 0x3);
-                        if (kb == nk - 1) umma_commit_pair(&acc_full[h], 0x3);
-                    }
-                    __syncwarp();
+                                           idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                    umma_commit_pair_lead(lead, &empty[st], 0x3);
+                    if (kb == nk - 1) umma_commit_pair_lead(lead, &acc_full[h], 0x3);
                     if (++st == static_cast<uint32_t>(stages)) {
                         st = 0;
                         ph ^= 1u;

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict_
                                                      int64_t M, int64_t cols, int64_t ld,
                                                      const uint16_t *__restrict__ dh, int64_t F,
                                                      const uint16_t *__restrict__ scales, int64_t n_scales,
-                                                     uint16_t *__restrict__ out, float *__restrict__ sx,
+                                                     bool permute, uint16_t *__restrict__ out, float *__restrict__ sx,
                                                      int *__restrict__ grow, unsigned *__restrict__ dmax) {
     if (blockIdx.x >= M) {
         const int64_t nb = gridDim.x - M;
@@ -118,10 +118,9 @@ __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict_
         uint32_t h[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            v[2 * e] *= sc;
-            v[2 * e + 1] *= sc;
-            sq = fmaf(v[2 * e], v[2 * e], fmaf(v[2 * e + 1], v[2 * e + 1], sq));
-            const __half2 hv = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+            const float lo = (permute ? v[e] : v[2 * e]) * sc, hi = (permute ? v[e + 4] : v[2 * e + 1]) * sc;
+            sq = fmaf(lo, lo, fmaf(hi, hi, sq));
+            const __half2 hv = __floats2half2_rn(lo, hi);
             h[e] = *reinterpret_cast<const uint32_t *>(&hv);
         }
         // ld is a multiple of 8: a last partial chunk stays inside its own row
@@ -218,12 +217,12 @@ cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t
 }
 
 cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int64_t cols, int64_t ld,
-                          const uint16_t *dh, int64_t F, const uint16_t *scales, int64_t n_scales, uint16_t *out,
-                          float *sx, int *grow, unsigned *dmax, cudaStream_t st) {
-    cudaError_t e = cudaMemsetAsync(dmax, 0, sizeof(unsigned), st);
+                          const uint16_t *dh, int64_t F, const uint16_t *scales, int64_t n_scales, bool permute,
+                          uint16_t *out, float *sx, int *grow, unsigned *dmax, int64_t zeroed, cudaStream_t st) {
+    cudaError_t e = cudaMemsetAsync(dmax, 0, sizeof(unsigned) * zeroed, st);
     if (e != cudaSuccess) return e;
     const int64_t extra = (n_scales + 8191) / 8192 < 148 ? (n_scales + 8191) / 8192 : 148;
-    rows16_kernel<<<static_cast<unsigned>(M + extra), 256, 0, st>>>(x, s16, M, cols, ld, dh, F, scales, n_scales, out,
+    rows16_kernel<<<static_cast<unsigned>(M + extra), 256, 0, st>>>(x, s16, M, cols, ld, dh, F, scales, n_scales, permute, out,
                                                                      sx, grow, dmax);
     return cudaGetLastError();
 }

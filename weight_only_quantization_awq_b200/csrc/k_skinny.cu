@@ -1,0 +1,517 @@
+// Products with a packed weight matrix for up to a few hundred tokens, the weights dequantised on
+// the way into the tensor cores (tcgen05), in both directions:
+//
+//   forward   D[o, m] = sum_i W[o, i] xs[m, i]     (the gated projections; A = W, K = in)
+//   gradient  D[i, m] = sum_o W[o, i] dy[m, o]     (A = W^T, K = out)
+//
+// with the tokens on the MMA's N side (N = tokens rounded to 16, at most 256), so that few tokens
+// cost few cycles, and 128 rows or columns of W on its M side.  Both directions share one stage:
+// 128 rows x 128 columns of W as fp16, two blocks of [128 rows][64 columns] in 128-byte swizzled
+// rows.  Read K-major, they are 128 rows of A and two 64-deep slabs of K; read MN-major, 128 columns
+// of A^T and eight 16-deep steps of K.  Nothing but the descriptors differs.
+//
+// Bound: the packed weights from HBM for few tokens, the shared-memory traffic of the stages (32 KB
+// written and read per 128 x 128 weights, about 260 cycles, and the tokens' tile) above.
+//
+// Roles: 16 warps dequantise, in two groups that take the stages in turn, so that one group computes
+// while the other stores (a thread: 64 columns of one row, two 16-byte loads of codes fetched SK_PF
+// of its stages ahead into registers; shift, LOP3, exact HSUB2 or HFMA2 to code - z, HMUL2 by
+// Delta 2^-kW, eight 16-byte stores); one warp fetches the token tiles by TMA, one
+// issues the MMAs, four write the results from TMEM, whose two accumulators let a tile's
+// epilogue run beside the next tile's products.
+//
+// Split: the (tile, 128-deep stage) sequence is cut into equal contiguous ranges, one per CTA,
+// one CTA per SM.  A tile that several CTAs share leaves fp32 partial sums in the workspace; the last CTA
+// to arrive (a counter) adds them in the order of the CTAs, so the result does not depend on which
+// one that is.  Nobody waits for another CTA.
+//
+// The nibble pairs (e, e + 4) of a word become neighbouring fp16 values, so the 8 columns of a word
+// lie in the order (0,4,1,5,2,6,3,7).  Forward, the tokens' columns are stored in the same order;
+// in the gradient it is the order of the accumulator's lanes, and the epilogue writes lane p to
+// column frag_perm8(p) of its word.
+//
+// Every wait is bounded: a CTA that gives up raises its abort flag, waits (bounded) for its copies and
+// MMAs in flight, frees its TMEM and leaves without writing its remaining tiles.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "awq_internal.h"
+#include "awq_ptx.cuh"
+#include "w4a16_act.cuh"
+#include "w4a16_frag.cuh"
+
+namespace awq {
+
+namespace {
+
+constexpr int SK_DQ_WARPS = 16;
+constexpr int SK_WARP_EPI = 16, SK_WARP_TMA = 20, SK_WARP_MMA = 21;   // 16-19: TMEM lane quadrants 0-3
+constexpr int SK_THREADS = 22 * 32;
+constexpr int SK_PF = 1;                              // units of packed codes in flight per thread (twice that per CTA)
+constexpr int SK_A_BYTES = 32768;                     // 128 x 128 fp16
+constexpr int SK_MAX_STAGES = 5;
+constexpr int SK_XBUF = 2 * 16 * 128 * 4;             // the epilogue's exchange of gate and up values
+constexpr int SK_TAIL = SK_XBUF + 2 * 256 * 4 + (4 * SK_MAX_STAGES + 5) * 8 + 32;
+
+__device__ __forceinline__ uint64_t sk_desc_mn(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(16384 >> 4) << 16;             // the next 64 columns
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;              // the next 8 rows of K
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+
+__device__ __forceinline__ uint32_t sk_sub(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t sk_fma(uint32_t a, uint32_t b, uint32_t c) {
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
+                              *reinterpret_cast<const __half2 *>(&c));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t sk_mul(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ float sk_bf16(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+
+// First unit of CTA c's range.
+__device__ __forceinline__ int sk_first(const SkinnyArgs &a, int c) {
+    return static_cast<int>(static_cast<int64_t>(a.units) * c / static_cast<int>(gridDim.x));
+}
+
+template <bool GRAD, int EPI>
+__global__ void __launch_bounds__(SK_THREADS, 1)
+    skinny_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constant__ SkinnyArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int b_bytes = a.n * 256;                    // a token tile: two slabs of [n][64]
+    const int stage = SK_A_BYTES + b_bytes, stages = a.stages;
+    float *xbuf = reinterpret_cast<float *>(ring + stages * stage);     // [2][16 tokens][128 lanes]
+    float *tsc = xbuf + 2 * 16 * 128, *tsd = tsc + 256;                 // per token: result scale, gradient scale
+    uint64_t *a_full = reinterpret_cast<uint64_t *>(tsd + 256);
+    uint64_t *b_full = a_full + SK_MAX_STAGES, *empty = b_full + SK_MAX_STAGES;
+    uint64_t *acc_full = empty + SK_MAX_STAGES, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *is_last = abort_flag + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int u0 = sk_first(a, blockIdx.x), u1 = sk_first(a, blockIdx.x + 1);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&a_full[s], SK_DQ_WARPS / 2);
+            mbar_init(&b_full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&acc_full[h], 1);
+            mbar_init(&acc_empty[h], 4);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        *is_last = 0;
+        fence_mbar_init();
+    }
+    if (warp == SK_WARP_MMA) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == SK_WARP_TMA && lane == 0) tma_prefetch_desc(&bmap);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // All 512 columns: the allocation starts at column 0, and a constant base keeps the MMAs'
+    // operands in uniform registers.
+    constexpr uint32_t tmem_base = 0;
+
+    if (warp < SK_DQ_WARPS) {
+        // ---- dequantise: group `grp` of eight warps takes every second unit; thread = row r of the
+        // stage, columns 32 h .. + 31 of both of its 64-column blocks
+        const int grp = warp >> 3, r = (threadIdx.x & 255) >> 1, hf = threadIdx.x & 1;
+        const int wpr = static_cast<int>(a.I / 8), nG = static_cast<int>(a.I >> a.lg), nzw = (nG + 7) / 8;
+        const float dscale = ldexpf(1.0f, -dq_exp(a.dmax));
+        // Raw loads of the units to come: nothing touches a value before its unit, so nothing waits
+        // for it earlier.  Addresses are 32-bit offsets from the three base pointers (the packed
+        // matrix is below 4 GB); a row or column past the end reads the first word instead and gets
+        // a scale of zero.
+        struct Raw {
+            uint4 q[2];                               // codes of the two blocks
+            uint16_t s[2];
+            uint32_t z[2];
+            int g;                                    // group of block 0's columns; bits 29, 30: block 0, 1 is real
+        } raw[SK_PF];
+        int pt = (u0 + grp) / a.ks % a.tiles, pk = (u0 + grp) % a.ks;   // tile and K stage of the next load
+        uint32_t qo = 0, so = 0, zo = 0;              // codes: words; scales: elements; zero words
+        int g = 0, rem0 = 0, rem1 = 0;                // group of block 0; K positions left from its first, and block 1's (<= 0: none)
+        const uint32_t qstep = GRAD ? 256u * static_cast<uint32_t>(wpr) : 32u;   // two stages of K
+        const uint32_t sstep = GRAD ? 256u * static_cast<uint32_t>(nG) : 256u >> a.lg;
+        const uint32_t zstep = GRAD ? 256u * static_cast<uint32_t>(nzw) : 0u;
+        const int gstep = GRAD ? 0 : 256 >> a.lg;
+        const int blk = a.lg == 7 ? 0 : 64 >> a.lg;   // groups from block 0's columns to block 1's
+        auto place = [&]() {
+            int o, col;
+            if (GRAD) {
+                o = pk * 128 + r;
+                col = pt * 128 + hf * 32;
+                rem0 = col < static_cast<int>(a.I) ? static_cast<int>(a.O) - o : 0;
+                rem1 = col + 64 < static_cast<int>(a.I) ? rem0 : -(1 << 30);
+            } else {                                  // 64 gate rows, then their up rows
+                const int f = pt * 64 + (r & 63);
+                o = (r >> 6) * static_cast<int>(a.F) + f;
+                col = pk * 128 + hf * 32;
+                rem0 = f < static_cast<int>(a.F) ? static_cast<int>(a.I) - col : 0;
+                rem1 = rem0 - 64;
+            }
+            g = col >> a.lg;
+            qo = static_cast<uint32_t>(o) * static_cast<uint32_t>(wpr) + (static_cast<uint32_t>(col) >> 3);
+            so = static_cast<uint32_t>(o) * static_cast<uint32_t>(nG) + static_cast<uint32_t>(g);
+            zo = static_cast<uint32_t>(o) * static_cast<uint32_t>(nzw);
+        };
+        auto fetch = [&](Raw &w) {
+            const bool r0 = rem0 > 0, r1 = rem1 > 0;
+            w.g = g | (r0 ? 1 << 29 : 0) | (r1 ? 1 << 30 : 0);
+            w.q[0] = __ldcs(reinterpret_cast<const uint4 *>(a.q + (r0 ? qo : 0u)));
+            w.q[1] = __ldcs(reinterpret_cast<const uint4 *>(a.q + (r1 ? qo + 8u : 0u)));
+            w.s[0] = __ldg(a.scales + (r0 ? so : 0u));
+            if (blk) w.s[1] = __ldg(a.scales + (r1 ? so + blk : 0u));
+            if (a.zeros) {
+                w.z[0] = __ldg(a.zeros + (r0 ? zo + (static_cast<uint32_t>(g) >> 3) : 0u));
+                if (blk) w.z[1] = __ldg(a.zeros + (r1 ? zo + (static_cast<uint32_t>(g + blk) >> 3) : 0u));
+            }
+            pk += 2;
+            if (pk < a.ks) {
+                qo += qstep;
+                so += sstep;
+                zo += zstep;
+                g += gstep;
+                rem0 -= 256;
+                rem1 -= 256;
+            } else {
+                while (pk >= a.ks) {                  // (K may be a single stage)
+                    pk -= a.ks;
+                    if (++pt == a.tiles) pt = 0;      // the next token tile
+                }
+                place();
+            }
+        };
+        place();
+#pragma unroll
+        for (int u = 0; u < SK_PF; ++u) fetch(raw[u]);
+        const uint32_t P = 0x64006400u;
+        const uint32_t row_off = static_cast<uint32_t>(r * 128);
+        const uint32_t sx0 = static_cast<uint32_t>((hf * 4) ^ (r & 7));          // column 0 of this half, swizzled
+        uint32_t st = static_cast<uint32_t>(grp), ph = 1;   // (at least two ring stages)
+        bool ok = true;
+        for (int ub = u0 + grp; ub < u1 && ok; ub += 2 * SK_PF) {
+#pragma unroll
+            for (int u = 0; u < SK_PF; ++u) {
+                if (ub + 2 * u >= u1) break;
+                uint4 v[2][4];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int gb = raw[u].g + (b ? blk : 0);
+                    uint32_t z = 8u;
+                    if (a.zeros) z = ((b && blk ? raw[u].z[1] : raw[u].z[0]) >> (4 * (gb & 7))) & 15u;
+                    const float df = raw[u].g & (1 << (29 + b))
+                                         ? __half2float(__ushort_as_half(b && blk ? raw[u].s[1] : raw[u].s[0])) * dscale : 0.0f;
+                    const __half2 dh2 = __floats2half2_rn(df, df);
+                    const uint32_t d = *reinterpret_cast<const uint32_t *>(&dh2);
+                    const uint32_t z0 = (0x6400u | z) * 0x00010001u;             // 1024 + z
+                    const uint32_t z1 = sk_sub(0x63806380u, z0);                 // 960 - (1024 + z) = -(64 + z)
+                    const uint32_t w[4] = {raw[u].q[b].x, raw[u].q[b].y, raw[u].q[b].z, raw[u].q[b].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t w8 = w[j] >> 8;
+                        // 1024 + c minus (1024 + z); (1024 + 16 c) / 16 minus (64 + z): both exact
+                        v[b][j].x = sk_mul(sk_sub((w[j] & 0x000F000Fu) | P, z0), d);
+                        v[b][j].y = sk_mul(sk_fma((w[j] & 0x00F000F0u) | P, 0x2C002C00u, z1), d);
+                        v[b][j].z = sk_mul(sk_sub((w8 & 0x000F000Fu) | P, z0), d);
+                        v[b][j].w = sk_mul(sk_fma((w8 & 0x00F000F0u) | P, 0x2C002C00u, z1), d);
+                    }
+                }
+                fetch(raw[u]);
+                ok = mbar_wait_warp(&empty[st], ph, abort_flag);
+                if (!ok) break;
+                // the eight lanes of a store phase (four rows, two halves) fall into eight 16-byte columns
+                uint8_t *dst = ring + st * stage + row_off;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<uint4 *>(dst + b * 16384 + ((sx0 ^ j) << 4)) = v[b][j];
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&a_full[st]);
+                st += 2;
+                if (st >= static_cast<uint32_t>(stages)) {
+                    st -= static_cast<uint32_t>(stages);
+                    ph ^= 1u;
+                }
+            }
+        }
+    } else if (warp == SK_WARP_TMA) {
+        // ---- token tiles
+        uint32_t st = 0, ph = 1;
+        int issued = 0;
+        int tt = u0 / a.ks / a.tiles, t = u0 / a.ks - tt * a.tiles, k = u0 % a.ks;
+        for (int u = u0; u < u1; ++u, ++issued) {
+            if (!mbar_wait_warp(&empty[st], ph, abort_flag)) break;
+            if (elect_one()) {
+                uint8_t *dst = ring + st * stage + SK_A_BYTES;
+                mbar_arrive_expect_tx(&b_full[st], static_cast<uint32_t>(b_bytes));
+                tma_load_2d(dst, &bmap, &b_full[st], k * 128, tt * a.n);
+                tma_load_2d(dst + a.n * 128, &bmap, &b_full[st], k * 128 + 64, tt * a.n);
+            }
+            __syncwarp();
+            if (++st == static_cast<uint32_t>(stages)) {
+                st = 0;
+                ph ^= 1u;
+            }
+            if (++k == a.ks) {
+                k = 0;
+                if (++t == a.tiles) {
+                    t = 0;
+                    ++tt;
+                }
+            }
+        }
+        if (lane == 0)                                // wait (bounded) for the copies in flight
+            for (int s = 0; s < stages; ++s)
+                if (issued > s)
+                    mbar_wait_drain(&b_full[(issued - 1 - s) % stages],
+                                    static_cast<uint32_t>(((issued - 1 - s) / stages) & 1));
+        __syncwarp();
+    } else if (warp == SK_WARP_MMA) {
+        const uint32_t idesc = idesc_f16_f32(128, a.n, false) | (GRAD ? 1u << 15 : 0u);
+        const uint32_t ring0 = smem_u32(ring), lead = elect_one() ? 1u : 0u;
+        const uint64_t da0 = GRAD ? sk_desc_mn(ring0) : sdesc_kmajor_sw128(ring0), db0 = sdesc_kmajor_sw128(ring0 + SK_A_BYTES);
+        uint32_t st = 0, ph = 0, seg = 0;
+        bool ok = true;
+        int k = u0 % a.ks;
+        bool fresh = true;                            // the first stage of a segment
+        for (int u = u0; u < u1; ++u) {
+            const uint32_t h = seg & 1u;
+            if (fresh) {
+                ok = mbar_wait_warp(&acc_empty[h], ((seg >> 1) & 1u) ^ 1u, abort_flag);
+                if (!ok) break;
+            }
+            ok = mbar_wait_warp(&b_full[st], ph, abort_flag) && mbar_wait_warp(&a_full[st], ph, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tmem_base + h * a.acc_cols;
+            const uint64_t da = sdesc_at(da0, st * stage), db = sdesc_at(db0, st * stage), db2 = sdesc_at(db, a.n * 128);
+            const bool end = k + 1 == a.ks || u + 1 == u1;
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                umma_f16_lead(lead, d, sdesc_at(da, GRAD ? s * 2048 : (s >> 2) * 16384 + (s & 3) * 32),
+                              sdesc_at(s < 4 ? db : db2, (s & 3) * 32), idesc, s > 0 ? 1u : (fresh ? 0u : 1u));
+            umma_commit_lead(lead, &empty[st]);
+            if (end) umma_commit_lead(lead, &acc_full[h]);
+            fresh = end;
+            if (end) ++seg;
+            if (++k == a.ks) k = 0;
+            if (++st == static_cast<uint32_t>(stages)) {
+                st = 0;
+                ph ^= 1u;
+            }
+        }
+        if (elect_one()) umma_commit(drain);
+        __syncwarp();
+        if (lane == 0) mbar_wait_drain(drain, 0);
+        __syncwarp();
+    } else {
+        // ---- results
+        const int e = threadIdx.x - SK_WARP_EPI * 32; // lane of the accumulator
+        const uint32_t quad = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const float sw = dq_scale(a.dmax);
+        uint32_t seg = 0, flip = 0;
+        int have = -1;                                // token tile whose scales are in tsc
+        for (int u = u0; u < u1; ++seg) {
+            const int T = u / a.ks, tt = T / a.tiles, t = T - tt * a.tiles;
+            const int b0 = T * a.ks, b1 = b0 + a.ks, end = b1 < u1 ? b1 : u1;
+            const bool whole = u == b0 && end == b1;
+            const int m0 = tt * a.n, mcount = static_cast<int>(a.M - m0 < a.n ? a.M - m0 : a.n);
+            const uint32_t h = seg & 1u, acc = tmem_base + quad + h * a.acc_cols;
+            if (tt != have) {
+                named_bar_sync(1, 128);
+                for (int m = e; m < mcount; m += 128) {
+                    const int ex = a.grow ? dgu_exp(__ldg(a.grow + m0 + m), a.inner, a.dmax) : 0;
+                    // forward: the token's own scale; gradient of the gated product: 2^e
+                    tsc[m] = GRAD && a.grow ? ldexpf(1.0f, ex) : __ldg(a.sx + m0 + m);
+                    if (EPI == EPI_GATED_BWD) tsd[m] = ldexpf(1.0f, -ex);
+                }
+                named_bar_sync(1, 128);
+                have = tt;
+            }
+            // one 16-token chunk of this lane to the result
+            auto finish = [&](int c, const float (&v)[16]) {
+                if (EPI == EPI_OUT) {
+                    const int64_t col = static_cast<int64_t>(t) * 128 + (e & ~7) + frag_perm8(e & 7);
+                    if (col < a.I) {
+                        const float s = a.s16 ? __half2float(__ushort_as_half(__ldg(a.s16 + col))) : 1.0f;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            if (c + k < mcount)
+                                a.out[(m0 + c + k) * a.I + col] =
+                                    __bfloat16_as_ushort(__float2bfloat16_rn(__fdividef((v[k] * tsc[c + k]) * sw, s)));
+                    }
+                } else {
+                    float *x = xbuf + flip * (16 * 128);
+                    flip ^= 1u;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) x[k * 128 + e] = v[k];
+                    named_bar_sync(1, 128);
+                    const int64_t f = static_cast<int64_t>(t) * 64 + (e & 63);
+                    if (f < a.F) {
+#pragma unroll
+                        for (int k8 = 0; k8 < 8; ++k8) {
+                            const int k = (e >> 6) * 8 + k8, m = c + k;
+                            if (m < mcount) {
+                                const float gv = (x[k * 128 + (e & 63)] * tsc[m]) * sw;
+                                const float uv = (x[k * 128 + 64 + (e & 63)] * tsc[m]) * sw;
+                                if (EPI == EPI_GATED) {
+                                    a.out[(m0 + m) * a.F + f] =
+                                        __bfloat16_as_ushort(__float2bfloat16_rn(act_value(gv, a.act) * uv));
+                                } else {
+                                    float da;
+                                    const float av = act_both(gv, a.act, da);
+                                    const float dv = sk_bf16(__ldg(a.dh + (m0 + m) * a.F + f)) * tsd[m];
+                                    uint16_t *dst = a.d16 + (m0 + m) * a.ldd + f;
+                                    dst[0] = __half_as_ushort(__float2half_rn((dv * uv) * da));
+                                    dst[a.F] = __half_as_ushort(__float2half_rn(dv * av));
+                                }
+                            }
+                        }
+                    }
+                }
+            };
+            // (one outcome for the four warps: they meet at barriers below)
+            if (!named_bar_and(1, 128, mbar_wait_sleep(&acc_full[h], (seg >> 1) & 1u, abort_flag))) break;
+            tc_fence_after();
+            // a shared tile's partial sums: this CTA's slot [n / 4][128] of four tokens
+            float4 *mine = a.part + static_cast<int64_t>(2 * blockIdx.x + (u0 > b0 ? 0 : 1)) * a.n * 32;
+            for (int c = 0; c < a.n; c += 16) {
+                uint32_t rv[16];
+                tmem_ld16_wait(acc + c, rv);
+                float v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(rv[k]);
+                if (whole) {
+                    finish(c, v);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        __stcg(mine + (c / 4 + k) * 128 + e, make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[h]);
+            if (!whole) {
+                int c0 = blockIdx.x, c1 = blockIdx.x; // the CTAs that share the tile
+                while (sk_first(a, c0) > b0) --c0;
+                while (sk_first(a, c1 + 1) < b1) ++c1;
+                __threadfence();
+                named_bar_sync(1, 128);
+                if (e == 0) *is_last = atomicAdd(&a.counter[T], 1u) == static_cast<unsigned>(c1 - c0);
+                named_bar_sync(1, 128);
+                if (*is_last) {
+                    __threadfence();
+                    for (int c = 0; c < a.n; c += 16) {
+                        float v[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) v[k] = 0.0f;
+#pragma unroll 4
+                        for (int ct = c0; ct <= c1; ++ct) {
+                            const float4 *p = a.part + static_cast<int64_t>(2 * ct + (sk_first(a, ct) > b0 ? 0 : 1)) * a.n * 32;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float4 w = __ldcg(p + (c / 4 + k) * 128 + e);
+                                v[4 * k] += w.x;
+                                v[4 * k + 1] += w.y;
+                                v[4 * k + 2] += w.z;
+                                v[4 * k + 3] += w.w;
+                            }
+                        }
+                        finish(c, v);
+                    }
+                }
+            }
+            u = end;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == SK_WARP_MMA) {
+        tc_fence_after();
+        tmem_dealloc(*tmem_slot, 512);
+    }
+}
+
+template <bool GRAD, int EPI>
+cudaError_t launch_sk(const CUtensorMap &bmap, const SkinnyArgs &a, int grid, cudaStream_t st) {
+    static bool attr_set[64] = {};                    // per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        e = cudaFuncSetAttribute(skinny_kernel<GRAD, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    const size_t smem = 1024 + static_cast<size_t>(a.stages) * (SK_A_BYTES + a.n * 256) + SK_TAIL;
+    skinny_kernel<GRAD, EPI><<<static_cast<unsigned>(grid), SK_THREADS, smem, st>>>(bmap, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+SkinnyPlan skinny_plan(int64_t M, int64_t tiles, int64_t k, int num_sms) {
+    SkinnyPlan p;
+    const int64_t tt = (M + 255) / 256;               // token tiles, of equal width
+    p.n = static_cast<int>(((M + tt - 1) / tt + 15) / 16 * 16);
+    p.token_tiles = static_cast<int>((M + p.n - 1) / p.n);
+    p.tiles = static_cast<int>(tiles);
+    p.ks = static_cast<int>((k + 127) / 128);
+    // CTAs: one per SM, but no more of them to a tile than pays: a stage costs about 400 ns of its
+    // CTA, each further CTA's partial sums about 10 ns a token in the one that adds them up.
+    const int64_t units = tiles * p.ks * p.token_tiles;
+    int64_t share = 1, best = INT64_MAX;
+    for (int64_t c = 1; c <= p.ks && c <= 64; ++c) {
+        const int64_t cost = (p.ks + c - 1) / c * 400 + (c > 1 ? c * p.n * 10 + 1000 : 0);
+        if (cost < best) {
+            best = cost;
+            share = c;
+        }
+    }
+    const int64_t most = tiles * p.token_tiles * share;
+    p.grid = static_cast<int>(most < num_sms ? most : num_sms);
+    if (p.grid > units) p.grid = static_cast<int>(units);
+    p.part_vecs = static_cast<int64_t>(2) * p.grid * p.n * 32;
+    p.counters = tiles * p.token_tiles;
+    return p;
+}
+
+cudaError_t launch_skinny(bool grad, int epi, const CUtensorMap &bmap, SkinnyArgs a, const SkinnyPlan &p, cudaStream_t st) {
+    a.n = p.n;
+    a.tiles = p.tiles;
+    a.ks = p.ks;
+    a.units = static_cast<int>(static_cast<int64_t>(p.tiles) * p.ks * p.token_tiles);
+    a.acc_cols = p.n <= 32 ? 32 : p.n <= 64 ? 64 : p.n <= 128 ? 128 : 256;
+    const int fit = (232448 - 1024 - SK_TAIL) / (SK_A_BYTES + p.n * 256);
+    a.stages = fit < SK_MAX_STAGES ? fit : SK_MAX_STAGES;
+    if (a.stages < 2) return cudaErrorInvalidConfiguration;
+    if (grad) return launch_sk<true, EPI_OUT>(bmap, a, p.grid, st);
+    return epi == EPI_GATED ? launch_sk<false, EPI_GATED>(bmap, a, p.grid, st)
+                            : launch_sk<false, EPI_GATED_BWD>(bmap, a, p.grid, st);
+}
+
+}  // namespace awq
