@@ -824,17 +824,17 @@ static awq_status_t gated_dense(const uint16_t *dh, const uint16_t *x, int64_t M
                                 cudaStream_t st) {
     const int64_t O = 2 * F, Fp = round64(F);
     Workspace ws(st);
-    size_t bytes = Workspace::up(2 * M * in) + Workspace::up(4 * M) + Workspace::up(4) + Workspace::up(2 * O * in);
+    size_t bytes = Workspace::up(2 * M * in) + Workspace::up(4 * M) + Workspace::up(4 * awq::DMAX_PARTS) + Workspace::up(2 * O * in);
     if (dh) bytes += Workspace::up(4 * M) + Workspace::up(2 * M * 2 * Fp);
     if (awq_status_t s = ws.reserve(bytes)) return s;
     uint16_t *xs = ws.take<uint16_t>(M * in);
     float *sx = ws.take<float>(M);
-    unsigned *dmax = ws.take<unsigned>(1);
+    unsigned *dmax = ws.take<unsigned>(awq::DMAX_PARTS);
     uint16_t *w16 = ws.take<uint16_t>(O * in);
     int *grow = dh ? ws.take<int>(M) : nullptr;
     uint16_t *d16 = dh ? ws.take<uint16_t>(M * 2 * Fp) : nullptr;
     AWQ_CUDA(awq::launch_rows16(x, s16, M, in, in, dh, F, scales, O * (in / group_size), false, xs, sx, grow,
-                                dmax, 1, st));
+                                dmax, st));
     AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, O, in, group_size, dmax, w16, st));
     awq::GemmArgs a{};
     a.M = M;
@@ -894,19 +894,18 @@ static awq_status_t gated_skinny(const uint16_t *dh, const uint16_t *x, int64_t 
     const awq::SkinnyPlan fp = awq::skinny_plan(M, (F + 63) / 64, in, sms);
     const awq::SkinnyPlan gp = awq::skinny_plan(M, (in + 127) / 128, O, sms);
     const int64_t parts = dh && gp.part_vecs > fp.part_vecs ? gp.part_vecs : fp.part_vecs;
-    const int64_t words = 1 + fp.counters + (dh ? gp.counters : 0);
     Workspace ws(st);
-    size_t bytes = Workspace::up(2 * M * in) + Workspace::up(4 * M) + Workspace::up(4 * words) + Workspace::up(16 * parts);
+    size_t bytes = Workspace::up(2 * M * in) + Workspace::up(4 * M) + Workspace::up(4 * awq::DMAX_PARTS) + Workspace::up(16 * parts);
     if (dh) bytes += Workspace::up(4 * M) + Workspace::up(2 * M * ldd);
     if (awq_status_t s = ws.reserve(bytes)) return s;
     uint16_t *xs = ws.take<uint16_t>(M * in);
     float *sx = ws.take<float>(M);
-    unsigned *dmax = ws.take<unsigned>(words);
+    unsigned *dmax = ws.take<unsigned>(awq::DMAX_PARTS);
     float4 *part = ws.take<float4>(parts);
     int *grow = dh ? ws.take<int>(M) : nullptr;
     uint16_t *d16 = dh ? ws.take<uint16_t>(M * ldd) : nullptr;
     AWQ_CUDA(awq::launch_rows16(x, s16, M, in, in, dh, F, scales, O * (in / group_size), true, xs, sx, grow, dmax,
-                                words, st));
+                                st));
     awq::SkinnyArgs a{};
     a.q = qweight;
     a.scales = scales;
@@ -926,7 +925,6 @@ static awq_status_t gated_skinny(const uint16_t *dh, const uint16_t *x, int64_t 
     a.d16 = d16;
     a.ldd = ldd;
     a.part = part;
-    a.counter = dmax + 1;
     CUtensorMap map;
     if (awq_status_t s = map_kmajor(&map, false, xs, in, M, in, fp.n)) return s;
     kt_reset(4);
@@ -935,7 +933,6 @@ static awq_status_t gated_skinny(const uint16_t *dh, const uint16_t *x, int64_t 
     kt_end(4, st);
     if (!dh) return AWQ_OK;
     a.s16 = s16;
-    a.counter = dmax + 1 + fp.counters;
     if (awq_status_t s = map_kmajor(&map, false, d16, O, M, ldd, gp.n)) return s;
     kt_begin(4, st);
     AWQ_CUDA(awq::launch_skinny(true, awq::EPI_OUT, map, a, gp, st));
@@ -1005,15 +1002,15 @@ awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, in
         const awq::SkinnyPlan p = awq::skinny_plan(M, (in + 127) / 128, out, sms);
         Workspace ws(st);
         if (awq_status_t s = ws.reserve(Workspace::up(2 * M * ld) + Workspace::up(4 * M) +
-                                        Workspace::up(4 * (1 + p.counters)) + Workspace::up(16 * p.part_vecs)))
+                                        Workspace::up(4 * awq::DMAX_PARTS) + Workspace::up(16 * p.part_vecs)))
             return s;
         uint16_t *d16 = ws.take<uint16_t>(M * ld);
         awq::SkinnyArgs a{};
         float *sx = ws.take<float>(M);
-        unsigned *dmax = ws.take<unsigned>(1 + p.counters);
+        unsigned *dmax = ws.take<unsigned>(awq::DMAX_PARTS);
         a.part = ws.take<float4>(p.part_vecs);
         AWQ_CUDA(awq::launch_rows16(dy, nullptr, M, out, ld, nullptr, 0, scales, out * (in / group_size), false, d16, sx,
-                                    nullptr, dmax, 1 + p.counters, st));
+                                    nullptr, dmax, st));
         a.q = qweight;
         a.scales = scales;
         a.zeros = zeros;
@@ -1025,7 +1022,6 @@ awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, in
         a.dmax = dmax;
         a.s16 = s16;
         a.out = dx;
-        a.counter = dmax + 1;
         CUtensorMap map;
         if (awq_status_t s = map_kmajor(&map, false, d16, out, M, ld, p.n)) return s;
         kt_reset(4);
@@ -1035,15 +1031,15 @@ awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, in
         return AWQ_OK;
     }
     Workspace ws(st);
-    if (awq_status_t s = ws.reserve(Workspace::up(2 * M * ld) + Workspace::up(4 * M) + Workspace::up(4) +
+    if (awq_status_t s = ws.reserve(Workspace::up(2 * M * ld) + Workspace::up(4 * M) + Workspace::up(4 * awq::DMAX_PARTS) +
                                     Workspace::up(2 * out * in)))
         return s;
     uint16_t *d16 = ws.take<uint16_t>(M * ld);
     float *sx = ws.take<float>(M);
-    unsigned *dmax = ws.take<unsigned>(1);
+    unsigned *dmax = ws.take<unsigned>(awq::DMAX_PARTS);
     uint16_t *w16 = ws.take<uint16_t>(out * in);
     AWQ_CUDA(awq::launch_rows16(dy, nullptr, M, out, ld, nullptr, 0, scales, out * (in / group_size), false, d16, sx,
-                                nullptr, dmax, 1, st));
+                                nullptr, dmax, st));
     AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, out, in, group_size, dmax, w16, st));
     awq::GemmArgs b{};
     b.M = M;

@@ -216,7 +216,7 @@ struct GemmArgs {
     int a_seg, b_seg;           // first K coordinate of the second segment in A and in B
     // scales
     const float *sx;            // [M]: A's row m carries 1 / sx[m] (a power of two)
-    const unsigned *dmax;       // the layer's largest |Delta| (the weights carry 2^-kW)
+    const unsigned *dmax;       // [DMAX_PARTS] largest |Delta| (the weights carry 2^-kW)
     const int *grow;            // [M]: exponent bound of the token's gradients (DGU_NONE: none)
     const uint16_t *s16;        // [N] fp16: divides column n (EPI_OUT)
     int inner;                  // in, of the gated product
@@ -242,11 +242,12 @@ cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, c
 cudaError_t launch_ce_final(const float2 *part, int nt, int64_t M, const int64_t *labels, int64_t V,
                             const float *tgt, float *loss, float *lse, cudaStream_t st);
 // Token rows to fp16 with a power-of-two scale each (out [M][ld], sx [M]); dh [M][F] with grow [M]
-// optional; *dmax = the layer's largest |Delta| as fp16 bits.  permute: the columns of each 8 in the
-// order (0,4,1,5,2,6,3,7).  `zeroed` words from dmax on start at zero (dmax itself, tile counters).
+// optional; dmax [DMAX_PARTS] = the largest |Delta| of the parts of the layer's scales, as fp16 bits.
+// permute: the columns of each 8 in the order (0,4,1,5,2,6,3,7).
+constexpr int DMAX_PARTS = 128;
 cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int64_t cols, int64_t ld,
                           const uint16_t *dh, int64_t F, const uint16_t *scales, int64_t n_scales, bool permute,
-                          uint16_t *out, float *sx, int *grow, unsigned *dmax, int64_t zeroed, cudaStream_t st);
+                          uint16_t *out, float *sx, int *grow, unsigned *dmax, cudaStream_t st);
 cudaError_t launch_dequant(const uint32_t *q, const uint16_t *scales, const uint32_t *zeros, int64_t O, int64_t I,
                            int gs, const unsigned *dmax, uint16_t *out, cudaStream_t st);
 cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t V, int64_t M, int64_t I,
@@ -258,7 +259,7 @@ cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t
 struct SkinnyPlan {
     int n, token_tiles;         // tokens per tile (a multiple of 16, <= 256), tiles of tokens
     int tiles, ks, grid;        // tiles of W, 128-deep stages of K, CTAs
-    int64_t part_vecs, counters;     // workspace: fp32 partial sums, by four; tile counters (zeroed)
+    int64_t part_vecs;          // workspace: fp32 partial sums, by four
 };
 // above SKINNY_MAX_M tokens, or 4 GB of codes: dequantise once, dense products
 constexpr int64_t SKINNY_MAX_M = 512;
@@ -271,7 +272,7 @@ struct SkinnyArgs {
     int64_t O, I, F, M;
     int lg;                     // log2 of the group size
     const float *sx;            // [M]: the token tile's row m carries 1 / sx[m]
-    const unsigned *dmax;       // the layer's largest |Delta| (the weights carry 2^-kW)
+    const unsigned *dmax;       // [DMAX_PARTS] largest |Delta| (the weights carry 2^-kW)
     const int *grow;            // [M] exponent bound of the token's gradients, or null
     const uint16_t *s16;        // [I]: divides column i (EPI_OUT)
     int inner, act;
@@ -280,9 +281,8 @@ struct SkinnyArgs {
     uint16_t *d16;              // [M][ldd]: gate gradients, then up gradients, fp16
     int64_t ldd;
     float4 *part;
-    unsigned *counter;
     // set by launch_skinny
-    int n, tiles, ks, units, acc_cols, stages;
+    int n, tiles, ks, units, acc_cols, stages, grid;
 };
 // bmap: the tokens' fp16 rows [M][K] (forward: columns of each 8 in the order (0,4,1,5,2,6,3,7)), box 64 x n.
 cudaError_t launch_skinny(bool grad, int epi, const CUtensorMap &bmap, SkinnyArgs a, const SkinnyPlan &p,

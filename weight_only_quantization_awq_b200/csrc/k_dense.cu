@@ -127,9 +127,10 @@ __device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, i
     const int half = a.bn / 2;
     const bool ok = row < a.M;
     const float sc = ok ? __ldg(a.sx + row) : 0.0f;
-    const float sw = dq_scale(a.dmax);
+    const int kw = dq_exp(a.dmax);
+    const float sw = ldexpf(1.0f, kw);
     // 2^-e of this token's gradients
-    const float sd = ok ? ldexpf(1.0f, -dgu_exp(__ldg(a.grow + row), a.inner, a.dmax)) : 0.0f;
+    const float sd = ok ? ldexpf(1.0f, -dgu_exp(__ldg(a.grow + row), a.inner, kw)) : 0.0f;
     const uint16_t *dh = a.dh + (ok ? row : 0) * a.F;
 #pragma unroll 1
     for (int c = 0; c < half; c += 16) {
@@ -171,8 +172,9 @@ __device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t
     const bool ok = row < a.M;
     float sc = 1.0f, sw = 1.0f;
     if (a.grow) {                                      // gated gradient: 2^e of the token
-        sc = ok ? ldexpf(1.0f, dgu_exp(__ldg(a.grow + row), a.inner, a.dmax)) : 0.0f;
-        sw = dq_scale(a.dmax);
+        const int kw = dq_exp(a.dmax);
+        sc = ok ? ldexpf(1.0f, dgu_exp(__ldg(a.grow + row), a.inner, kw)) : 0.0f;
+        sw = ldexpf(1.0f, kw);
     } else if (a.sx) {
         sc = ok ? __ldg(a.sx + row) : 0.0f;
         sw = dq_scale(a.dmax);

@@ -4,16 +4,18 @@
 #include <cuda_fp16.h>
 
 #include "awq_internal.h"
+#include "awq_ptx.cuh"
 #include "w4a16_act.cuh"
 
 namespace awq {
 
 namespace {
 
-// Largest |Delta| of the layer, as fp16 bits, into *dmax (zeroed by the caller).  A maximum does
-// not depend on the order of its terms.
-__device__ __forceinline__ void scales_max(const uint16_t *__restrict__ scales, int64_t n, int64_t first,
-                                           int64_t step, unsigned *dmax) {
+// Largest |Delta| of one of DMAX_PARTS parts of the layer's scales, as fp16 bits, into dmax[part]
+// (a block of 256 threads).
+__device__ __forceinline__ void scales_max(const uint16_t *__restrict__ scales, int64_t n, int part, unsigned *dmax) {
+    __shared__ unsigned wm[8];
+    const int64_t first = static_cast<int64_t>(part) * 256 + threadIdx.x, step = DMAX_PARTS * 256;
     // 16 bytes at a time from the first 16-byte boundary on; the ragged ends one by one
     unsigned mb = 0u;
     const int64_t head = ((16 - (reinterpret_cast<uintptr_t>(scales) & 15)) & 15) / 2;
@@ -30,7 +32,12 @@ __device__ __forceinline__ void scales_max(const uint16_t *__restrict__ scales, 
     for (int64_t i = first; i < rest; i += step)
         mb = max(mb, static_cast<unsigned>(__ldg(scales + (i < h ? i : vecs * 8 + i))) & 0x7FFFu);
     mb = __reduce_max_sync(0xffffffffu, mb);
-    if ((threadIdx.x & 31) == 0) atomicMax(dmax, mb);
+    if ((threadIdx.x & 31) == 0) wm[threadIdx.x >> 5] = mb;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int k = 1; k < 8; ++k) mb = max(mb, wm[k]);
+        dmax[part] = mb;
+    }
 }
 
 // v[0..8) = source row elements [c, c + 8), divided by s where given.
@@ -83,22 +90,22 @@ __device__ __forceinline__ float block_sum(float v, float *sm) {
     return v;
 }
 
-// Blocks [0, M): one token each.  out[m] = fp16((row / s) * 2^-k), k from the row's largest
+// Blocks from DMAX_PARTS on: one token each.  out[m] = fp16((row / s) * 2^-k), k from the row's largest
 // magnitude so that it lands in [2^14, 2^15); sx[m] = 2^k.  With dh: grow[m], an exponent
-// that bounds max |dh[m]| * ||row / s||.  Further blocks: the layer's largest |Delta|.
+// that bounds max |dh[m]| * ||row / s||.  The first blocks: the parts' largest |Delta|.
 __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ s16,
                                                      int64_t M, int64_t cols, int64_t ld,
                                                      const uint16_t *__restrict__ dh, int64_t F,
                                                      const uint16_t *__restrict__ scales, int64_t n_scales,
                                                      bool permute, uint16_t *__restrict__ out, float *__restrict__ sx,
                                                      int *__restrict__ grow, unsigned *__restrict__ dmax) {
-    if (blockIdx.x >= M) {
-        const int64_t nb = gridDim.x - M;
-        scales_max(scales, n_scales, (blockIdx.x - M) * blockDim.x + threadIdx.x, nb * blockDim.x, dmax);
+    griddep_launch_dependents();                      // the products that follow wait for this kernel themselves
+    if (blockIdx.x < DMAX_PARTS) {
+        scales_max(scales, n_scales, static_cast<int>(blockIdx.x), dmax);
         return;
     }
     __shared__ float sm[8];
-    const int64_t m = blockIdx.x;
+    const int64_t m = blockIdx.x - DMAX_PARTS;
     const uint16_t *r = x + m * cols;
     const bool vec = cols % 8 == 0;
     float mx = 0.0f;
@@ -218,12 +225,9 @@ cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t
 
 cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int64_t cols, int64_t ld,
                           const uint16_t *dh, int64_t F, const uint16_t *scales, int64_t n_scales, bool permute,
-                          uint16_t *out, float *sx, int *grow, unsigned *dmax, int64_t zeroed, cudaStream_t st) {
-    cudaError_t e = cudaMemsetAsync(dmax, 0, sizeof(unsigned) * zeroed, st);
-    if (e != cudaSuccess) return e;
-    const int64_t extra = (n_scales + 8191) / 8192 < 148 ? (n_scales + 8191) / 8192 : 148;
-    rows16_kernel<<<static_cast<unsigned>(M + extra), 256, 0, st>>>(x, s16, M, cols, ld, dh, F, scales, n_scales, permute, out,
-                                                                     sx, grow, dmax);
+                          uint16_t *out, float *sx, int *grow, unsigned *dmax, cudaStream_t st) {
+    rows16_kernel<<<static_cast<unsigned>(M + DMAX_PARTS), 256, 0, st>>>(x, s16, M, cols, ld, dh, F, scales, n_scales,
+                                                                        permute, out, sx, grow, dmax);
     return cudaGetLastError();
 }
 

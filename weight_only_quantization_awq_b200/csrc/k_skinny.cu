@@ -21,9 +21,9 @@
 // epilogue run beside the next tile's products.
 //
 // Split: the (tile, 128-deep stage) sequence is cut into equal contiguous ranges, one per CTA,
-// one CTA per SM.  A tile that several CTAs share leaves fp32 partial sums in the workspace; the last CTA
-// to arrive (a counter) adds them in the order of the CTAs, so the result does not depend on which
-// one that is.  Nobody waits for another CTA.
+// one CTA per SM.  A tile that several CTAs share leaves fp32 partial sums in the workspace, and a
+// second, small kernel adds them in the order of the CTAs and finishes the tile (four tokens a block:
+// the last CTA of a tile doing it alone took 10 to 20 us more).  Nobody waits for another CTA.
 //
 // The nibble pairs (e, e + 4) of a word become neighbouring fp16 values, so the 8 columns of a word
 // lie in the order (0,4,1,5,2,6,3,7).  Forward, the tokens' columns are stored in the same order;
@@ -81,7 +81,99 @@ __device__ __forceinline__ float sk_bf16(uint16_t b) { return __uint_as_float(st
 
 // First unit of CTA c's range.
 __device__ __forceinline__ int sk_first(const SkinnyArgs &a, int c) {
-    return static_cast<int>(static_cast<int64_t>(a.units) * c / static_cast<int>(gridDim.x));
+    return static_cast<int>(static_cast<int64_t>(a.units) * c / a.grid);
+}
+
+// The results of K tokens (the tile's tokens c .. c + K - 1) from the accumulator's 128 lanes, thread e
+// holding lane e's values.  tsc, tsd: the tile's token scales.  BAR: hardware barrier of the 128 threads.
+// x: [K][128] floats of shared memory (gated products: lanes 64-127 hold the up values of lanes 0-63).
+template <int EPI, int K, int BAR>
+__device__ __forceinline__ void sk_finish(const SkinnyArgs &a, int t, int m0, int mcount, int c, const float (&v)[K],
+                                          int e, float sw, const float *tsc, const float *tsd, float *x) {
+    if (EPI == EPI_OUT) {
+        const int64_t col = static_cast<int64_t>(t) * 128 + (e & ~7) + frag_perm8(e & 7);
+        if (col < a.I) {
+            const float s = a.s16 ? __half2float(__ushort_as_half(__ldg(a.s16 + col))) : 1.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (c + k < mcount)
+                    a.out[(m0 + c + k) * a.I + col] =
+                        __bfloat16_as_ushort(__float2bfloat16_rn(__fdividef((v[k] * tsc[c + k]) * sw, s)));
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k * 128 + e] = v[k];
+    named_bar_sync(BAR, 128);
+    const int64_t f = static_cast<int64_t>(t) * 64 + (e & 63);
+    if (f < a.F) {
+#pragma unroll
+        for (int k2 = 0; k2 < K / 2; ++k2) {
+            const int k = (e >> 6) * (K / 2) + k2, m = c + k;
+            if (m < mcount) {
+                const float gv = (x[k * 128 + (e & 63)] * tsc[m]) * sw;
+                const float uv = (x[k * 128 + 64 + (e & 63)] * tsc[m]) * sw;
+                if (EPI == EPI_GATED) {
+                    a.out[(m0 + m) * a.F + f] = __bfloat16_as_ushort(__float2bfloat16_rn(act_value(gv, a.act) * uv));
+                } else {
+                    float da;
+                    const float av = act_both(gv, a.act, da);
+                    const float dv = sk_bf16(__ldg(a.dh + (m0 + m) * a.F + f)) * tsd[m];
+                    uint16_t *dst = a.d16 + (m0 + m) * a.ldd + f;
+                    dst[0] = __half_as_ushort(__float2half_rn((dv * uv) * da));
+                    dst[a.F] = __half_as_ushort(__float2half_rn(dv * av));
+                }
+            }
+        }
+    }
+}
+
+// A token's scales: forward, its own; gradient of the gated product, 2^e; tsd: 2^-e of the gradients
+// that EPI_GATED_BWD writes.
+template <bool GRAD, int EPI>
+__device__ __forceinline__ void sk_token_scale(const SkinnyArgs &a, int m, int kw, float &sc, float &sd) {
+    const int ex = a.grow ? dgu_exp(__ldg(a.grow + m), a.inner, kw) : 0;
+    sc = GRAD && a.grow ? ldexpf(1.0f, ex) : __ldg(a.sx + m);
+    sd = EPI == EPI_GATED_BWD ? ldexpf(1.0f, -ex) : 0.0f;
+}
+
+// Tiles that several CTAs share: block (tile, four tokens), 128 threads.
+template <bool GRAD, int EPI>
+__global__ void __launch_bounds__(128) skinny_finish_kernel(const __grid_constant__ SkinnyArgs a) {
+    __shared__ float x[4 * 128], tsc[4], tsd[4];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int T = blockIdx.x, b0 = T * a.ks, b1 = b0 + a.ks;
+    // the CTAs that share the tile, [c0, c1]: ranges cover the units in order
+    int c0 = static_cast<int>(static_cast<int64_t>(b0) * a.grid / a.units);
+    while (c0 > 0 && sk_first(a, c0) > b0) --c0;
+    while (sk_first(a, c0 + 1) <= b0) ++c0;
+    int c1 = c0;
+    while (sk_first(a, c1 + 1) < b1) ++c1;
+    if (c0 == c1) return;                             // one CTA's own: done
+    const int e = threadIdx.x, c = blockIdx.y * 4;
+    const int tt = T / a.tiles, t = T - tt * a.tiles, m0 = tt * a.n;
+    const int mcount = static_cast<int>(a.M - m0 < a.n ? a.M - m0 : a.n);
+    if (c >= mcount) return;
+    const int kw = dq_exp(a.dmax);
+    if (e < 4) {
+        float sc = 0.0f, sd = 0.0f;
+        if (c + e < mcount) sk_token_scale<GRAD, EPI>(a, m0 + c + e, kw, sc, sd);
+        tsc[e] = sc;
+        tsd[e] = sd;
+    }
+    __syncthreads();
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int ct = c0; ct <= c1; ++ct) {
+        const float4 w =
+            __ldg(a.part + (static_cast<int64_t>(2 * ct + (sk_first(a, ct) > b0 ? 0 : 1)) * (a.n / 4) + blockIdx.y) * 128 + e);
+        v[0] += w.x;
+        v[1] += w.y;
+        v[2] += w.z;
+        v[3] += w.w;
+    }
+    sk_finish<EPI, 4, 0>(a, t, m0, mcount, c, v, e, ldexpf(1.0f, kw), tsc - c, tsd - c, x);
 }
 
 template <bool GRAD, int EPI>
@@ -99,8 +191,8 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
     uint64_t *acc_full = empty + SK_MAX_STAGES, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    volatile int *is_last = abort_flag + 1;
 
+    griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int u0 = sk_first(a, blockIdx.x), u1 = sk_first(a, blockIdx.x + 1);
 
@@ -116,7 +208,6 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
-        *is_last = 0;
         fence_mbar_init();
     }
     if (warp == SK_WARP_MMA) {
@@ -136,7 +227,6 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
         // stage, columns 32 h .. + 31 of both of its 64-column blocks
         const int grp = warp >> 3, r = (threadIdx.x & 255) >> 1, hf = threadIdx.x & 1;
         const int wpr = static_cast<int>(a.I / 8), nG = static_cast<int>(a.I >> a.lg), nzw = (nG + 7) / 8;
-        const float dscale = ldexpf(1.0f, -dq_exp(a.dmax));
         // Raw loads of the units to come: nothing touches a value before its unit, so nothing waits
         // for it earlier.  Addresses are 32-bit offsets from the three base pointers (the packed
         // matrix is below 4 GB); a row or column past the end reads the first word instead and gets
@@ -204,6 +294,10 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
         place();
 #pragma unroll
         for (int u = 0; u < SK_PF; ++u) fetch(raw[u]);
+        // The packed weights are the caller's, complete before the kernel in front of this one began
+        // (it is launched in plain stream order); the exponent comes from that kernel.
+        griddep_wait();
+        const float dscale = ldexpf(1.0f, -dq_exp(a.dmax));
         const uint32_t P = 0x64006400u;
         const uint32_t row_off = static_cast<uint32_t>(r * 128);
         const uint32_t sx0 = static_cast<uint32_t>((hf * 4) ^ (r & 7));          // column 0 of this half, swizzled
@@ -258,6 +352,7 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
         }
     } else if (warp == SK_WARP_TMA) {
         // ---- token tiles
+        griddep_wait();
         uint32_t st = 0, ph = 1;
         int issued = 0;
         int tt = u0 / a.ks / a.tiles, t = u0 / a.ks - tt * a.tiles, k = u0 % a.ks;
@@ -328,9 +423,11 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
         __syncwarp();
     } else {
         // ---- results
+        griddep_wait();
         const int e = threadIdx.x - SK_WARP_EPI * 32; // lane of the accumulator
         const uint32_t quad = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const float sw = dq_scale(a.dmax);
+        const int kw = dq_exp(a.dmax);
+        const float sw = ldexpf(1.0f, kw);
         uint32_t seg = 0, flip = 0;
         int have = -1;                                // token tile whose scales are in tsc
         for (int u = u0; u < u1; ++seg) {
@@ -339,59 +436,12 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
             const bool whole = u == b0 && end == b1;
             const int m0 = tt * a.n, mcount = static_cast<int>(a.M - m0 < a.n ? a.M - m0 : a.n);
             const uint32_t h = seg & 1u, acc = tmem_base + quad + h * a.acc_cols;
-            if (tt != have) {
+            if (whole && tt != have) {
                 named_bar_sync(1, 128);
-                for (int m = e; m < mcount; m += 128) {
-                    const int ex = a.grow ? dgu_exp(__ldg(a.grow + m0 + m), a.inner, a.dmax) : 0;
-                    // forward: the token's own scale; gradient of the gated product: 2^e
-                    tsc[m] = GRAD && a.grow ? ldexpf(1.0f, ex) : __ldg(a.sx + m0 + m);
-                    if (EPI == EPI_GATED_BWD) tsd[m] = ldexpf(1.0f, -ex);
-                }
+                for (int m = e; m < mcount; m += 128) sk_token_scale<GRAD, EPI>(a, m0 + m, kw, tsc[m], tsd[m]);
                 named_bar_sync(1, 128);
                 have = tt;
             }
-            // one 16-token chunk of this lane to the result
-            auto finish = [&](int c, const float (&v)[16]) {
-                if (EPI == EPI_OUT) {
-                    const int64_t col = static_cast<int64_t>(t) * 128 + (e & ~7) + frag_perm8(e & 7);
-                    if (col < a.I) {
-                        const float s = a.s16 ? __half2float(__ushort_as_half(__ldg(a.s16 + col))) : 1.0f;
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (c + k < mcount)
-                                a.out[(m0 + c + k) * a.I + col] =
-                                    __bfloat16_as_ushort(__float2bfloat16_rn(__fdividef((v[k] * tsc[c + k]) * sw, s)));
-                    }
-                } else {
-                    float *x = xbuf + flip * (16 * 128);
-                    flip ^= 1u;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k * 128 + e] = v[k];
-                    named_bar_sync(1, 128);
-                    const int64_t f = static_cast<int64_t>(t) * 64 + (e & 63);
-                    if (f < a.F) {
-#pragma unroll
-                        for (int k8 = 0; k8 < 8; ++k8) {
-                            const int k = (e >> 6) * 8 + k8, m = c + k;
-                            if (m < mcount) {
-                                const float gv = (x[k * 128 + (e & 63)] * tsc[m]) * sw;
-                                const float uv = (x[k * 128 + 64 + (e & 63)] * tsc[m]) * sw;
-                                if (EPI == EPI_GATED) {
-                                    a.out[(m0 + m) * a.F + f] =
-                                        __bfloat16_as_ushort(__float2bfloat16_rn(act_value(gv, a.act) * uv));
-                                } else {
-                                    float da;
-                                    const float av = act_both(gv, a.act, da);
-                                    const float dv = sk_bf16(__ldg(a.dh + (m0 + m) * a.F + f)) * tsd[m];
-                                    uint16_t *dst = a.d16 + (m0 + m) * a.ldd + f;
-                                    dst[0] = __half_as_ushort(__float2half_rn((dv * uv) * da));
-                                    dst[a.F] = __half_as_ushort(__float2half_rn(dv * av));
-                                }
-                            }
-                        }
-                    }
-                }
-            };
             // (one outcome for the four warps: they meet at barriers below)
             if (!named_bar_and(1, 128, mbar_wait_sleep(&acc_full[h], (seg >> 1) & 1u, abort_flag))) break;
             tc_fence_after();
@@ -404,47 +454,18 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
 #pragma unroll
                 for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(rv[k]);
                 if (whole) {
-                    finish(c, v);
+                    sk_finish<EPI, 16, 1>(a, t, m0, mcount, c, v, e, sw, tsc, tsd, xbuf + flip * (16 * 128));
+                    flip ^= 1u;
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        __stcg(mine + (c / 4 + k) * 128 + e, make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+                        mine[(c / 4 + k) * 128 + e] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 }
                 __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[h]);
-            if (!whole) {
-                int c0 = blockIdx.x, c1 = blockIdx.x; // the CTAs that share the tile
-                while (sk_first(a, c0) > b0) --c0;
-                while (sk_first(a, c1 + 1) < b1) ++c1;
-                __threadfence();
-                named_bar_sync(1, 128);
-                if (e == 0) *is_last = atomicAdd(&a.counter[T], 1u) == static_cast<unsigned>(c1 - c0);
-                named_bar_sync(1, 128);
-                if (*is_last) {
-                    __threadfence();
-                    for (int c = 0; c < a.n; c += 16) {
-                        float v[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) v[k] = 0.0f;
-#pragma unroll 4
-                        for (int ct = c0; ct <= c1; ++ct) {
-                            const float4 *p = a.part + static_cast<int64_t>(2 * ct + (sk_first(a, ct) > b0 ? 0 : 1)) * a.n * 32;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float4 w = __ldcg(p + (c / 4 + k) * 128 + e);
-                                v[4 * k] += w.x;
-                                v[4 * k + 1] += w.y;
-                                v[4 * k + 2] += w.z;
-                                v[4 * k + 3] += w.w;
-                            }
-                        }
-                        finish(c, v);
-                    }
-                }
-            }
             u = end;
         }
     }
@@ -457,7 +478,7 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
 }
 
 template <bool GRAD, int EPI>
-cudaError_t launch_sk(const CUtensorMap &bmap, const SkinnyArgs &a, int grid, cudaStream_t st) {
+cudaError_t launch_sk(const CUtensorMap &bmap, const SkinnyArgs &a, bool split, cudaStream_t st) {
     static bool attr_set[64] = {};                    // per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -468,8 +489,22 @@ cudaError_t launch_sk(const CUtensorMap &bmap, const SkinnyArgs &a, int grid, cu
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
     const size_t smem = 1024 + static_cast<size_t>(a.stages) * (SK_A_BYTES + a.n * 256) + SK_TAIL;
-    skinny_kernel<GRAD, EPI><<<static_cast<unsigned>(grid), SK_THREADS, smem, st>>>(bmap, a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.grid));
+    cfg.blockDim = dim3(SK_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, skinny_kernel<GRAD, EPI>, bmap, a);
+    if (e != cudaSuccess || !split) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(a.units / a.ks), static_cast<unsigned>(a.n / 4));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, skinny_finish_kernel<GRAD, EPI>, a);
 }
 
 }  // namespace
@@ -481,12 +516,12 @@ SkinnyPlan skinny_plan(int64_t M, int64_t tiles, int64_t k, int num_sms) {
     p.token_tiles = static_cast<int>((M + p.n - 1) / p.n);
     p.tiles = static_cast<int>(tiles);
     p.ks = static_cast<int>((k + 127) / 128);
-    // CTAs: one per SM, but no more of them to a tile than pays: a stage costs about 400 ns of its
-    // CTA, each further CTA's partial sums about 10 ns a token in the one that adds them up.
+    // CTAs: one per SM, but no more of them to a tile than pays: a stage costs its CTA about 400 ns,
+    // the second kernel 2.5 us, each further CTA's partial sums about 60 ns of it.
     const int64_t units = tiles * p.ks * p.token_tiles;
     int64_t share = 1, best = INT64_MAX;
     for (int64_t c = 1; c <= p.ks && c <= 64; ++c) {
-        const int64_t cost = (p.ks + c - 1) / c * 400 + (c > 1 ? c * p.n * 10 + 1000 : 0);
+        const int64_t cost = (p.ks + c - 1) / c * 400 + (c > 1 ? c * 60 + 2500 : 0);
         if (cost < best) {
             best = cost;
             share = c;
@@ -496,7 +531,6 @@ SkinnyPlan skinny_plan(int64_t M, int64_t tiles, int64_t k, int num_sms) {
     p.grid = static_cast<int>(most < num_sms ? most : num_sms);
     if (p.grid > units) p.grid = static_cast<int>(units);
     p.part_vecs = static_cast<int64_t>(2) * p.grid * p.n * 32;
-    p.counters = tiles * p.token_tiles;
     return p;
 }
 
@@ -505,13 +539,17 @@ cudaError_t launch_skinny(bool grad, int epi, const CUtensorMap &bmap, SkinnyArg
     a.tiles = p.tiles;
     a.ks = p.ks;
     a.units = static_cast<int>(static_cast<int64_t>(p.tiles) * p.ks * p.token_tiles);
+    a.grid = p.grid;
+    // whether some CTA's range ends inside a tile
+    bool split = false;
+    for (int c = 1; c < p.grid && !split; ++c) split = static_cast<int64_t>(a.units) * c / p.grid % p.ks != 0;
     a.acc_cols = p.n <= 32 ? 32 : p.n <= 64 ? 64 : p.n <= 128 ? 128 : 256;
     const int fit = (232448 - 1024 - SK_TAIL) / (SK_A_BYTES + p.n * 256);
     a.stages = fit < SK_MAX_STAGES ? fit : SK_MAX_STAGES;
     if (a.stages < 2) return cudaErrorInvalidConfiguration;
-    if (grad) return launch_sk<true, EPI_OUT>(bmap, a, p.grid, st);
-    return epi == EPI_GATED ? launch_sk<false, EPI_GATED>(bmap, a, p.grid, st)
-                            : launch_sk<false, EPI_GATED_BWD>(bmap, a, p.grid, st);
+    if (grad) return launch_sk<true, EPI_OUT>(bmap, a, split, st);
+    return epi == EPI_GATED ? launch_sk<false, EPI_GATED>(bmap, a, split, st)
+                            : launch_sk<false, EPI_GATED_BWD>(bmap, a, split, st);
 }
 
 }  // namespace awq

@@ -20,9 +20,12 @@ __device__ __forceinline__ int scale_exp(float mx, int top) {
 
 // The layer's exponent kW: dequantised weights are held as (code - z) * Delta * 2^-kW, with
 // 15 * max |Delta| * 2^-kW < 2^15, so they stay in fp16's normal range whatever the layer's
-// magnitude (max |Delta| as fp16 bits in *dmax; those of non-negative values order as the values).
+// magnitude.  dmax holds the maxima of DMAX_PARTS parts of the scales as fp16 bits (those of
+// non-negative values order as the values).  A converged warp's collective.
 __device__ __forceinline__ int dq_exp(const unsigned *dmax) {
-    return scale_exp(__half2float(__ushort_as_half(static_cast<unsigned short>(__ldg(dmax)))), 11);
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(dmax) + (threadIdx.x & 31));
+    const unsigned mb = __reduce_max_sync(0xffffffffu, max(max(v.x, v.y), max(v.z, v.w)));
+    return scale_exp(__half2float(__ushort_as_half(static_cast<unsigned short>(mb))), 11);
 }
 __device__ __forceinline__ float dq_scale(const unsigned *dmax) { return ldexpf(1.0f, dq_exp(dmax)); }
 
@@ -32,11 +35,11 @@ __device__ __forceinline__ float dq_scale(const unsigned *dmax) { return ldexpf(
 // (Cauchy-Schwarz), |act(g)| <= |g|, |act'| < 1.2, so the scaled values are below 2^15.  The bound is
 // typically 2^8 above the largest value, which leaves fp16's normal range 20 binades below that.
 constexpr int DGU_NONE = -100000;
-__device__ __forceinline__ int dgu_exp(int grow, int inner, const unsigned *dmax) {
+__device__ __forceinline__ int dgu_exp(int grow, int inner, int kw) {
     if (grow <= DGU_NONE) return 0;
     int r;
     frexpf(sqrtf(static_cast<float>(inner)) * 1.2f, &r);
-    const int k = grow + r + (dq_exp(dmax) + 15) - 15;   // 15 max |Delta| < 2^(kW + 15)
+    const int k = grow + r + (kw + 15) - 15;           // 15 max |Delta| < 2^(kW + 15)
     return k < -125 ? -125 : (k > 125 ? 125 : k);
 }
 
