@@ -257,7 +257,7 @@ cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t
 // the tensor cores (k_skinny.cu): forward EPI_GATED / EPI_GATED_BWD (64 gate and 64 up rows per tile, K
 // = in), gradient EPI_OUT (128 columns per tile, K = out)
 struct SkinnyPlan {
-    int n, token_tiles;         // tokens per tile (a multiple of 16, <= 256), tiles of tokens
+    int n, token_tiles;         // tokens per tile (a multiple of 16, <= 144), tiles of tokens
     int tiles, ks, grid;        // tiles of W, 128-deep stages of K, CTAs
     int64_t part_vecs;          // workspace: fp32 partial sums, by four
 };

@@ -4,7 +4,7 @@
 //   forward   D[o, m] = sum_i W[o, i] xs[m, i]     (the gated projections; A = W, K = in)
 //   gradient  D[i, m] = sum_o W[o, i] dy[m, o]     (A = W^T, K = out)
 //
-// with the tokens on the MMA's N side (N = tokens rounded to 16, at most 256), so that few tokens
+// with the tokens on the MMA's N side (N = tokens rounded to 16, at most 144), so that few tokens
 // cost few cycles, and 128 rows or columns of W on its M side.  Both directions share one stage:
 // 128 rows x 128 columns of W as fp16, two blocks of [128 rows][64 columns] in 128-byte swizzled
 // rows.  Read K-major, they are 128 rows of A and two 64-deep slabs of K; read MN-major, 128 columns
@@ -13,8 +13,8 @@
 // Bound: the packed weights from HBM for few tokens, the shared-memory traffic of the stages (32 KB
 // written and read per 128 x 128 weights, about 260 cycles, and the tokens' tile) above.
 //
-// Roles: 16 warps dequantise, in two groups that take the stages in turn, so that one group computes
-// while the other stores (a thread: 64 columns of one row, two 16-byte loads of codes fetched SK_PF
+// Roles: 24 warps dequantise, in three groups that take the stages in turn, so that one group computes
+// while another stores (a thread: 64 columns of one row, two 16-byte loads of codes fetched SK_PF
 // of its stages ahead into registers; shift, LOP3, exact HSUB2 or HFMA2 to code - z, HMUL2 by
 // Delta 2^-kW, eight 16-byte stores); one warp fetches the token tiles by TMA, one
 // issues the MMAs, four write the results from TMEM, whose two accumulators let a tile's
@@ -44,12 +44,16 @@ namespace awq {
 
 namespace {
 
-constexpr int SK_DQ_WARPS = 16;
-constexpr int SK_WARP_EPI = 16, SK_WARP_TMA = 20, SK_WARP_MMA = 21;   // 16-19: TMEM lane quadrants 0-3
-constexpr int SK_THREADS = 22 * 32;
+constexpr int SK_GROUPS = 3;                           // groups of eight dequantising warps
+constexpr int SK_DQ_WARPS = 8 * SK_GROUPS;
+constexpr int SK_WARP_EPI = SK_DQ_WARPS, SK_WARP_TMA = SK_DQ_WARPS + 4, SK_WARP_MMA = SK_DQ_WARPS + 5;   // four epilogue warps: TMEM lane quadrants 0-3
+constexpr int SK_THREADS = (SK_DQ_WARPS + 6) * 32;
 constexpr int SK_PF = 1;                              // units of packed codes in flight per thread (twice that per CTA)
 constexpr int SK_A_BYTES = 32768;                     // 128 x 128 fp16
 constexpr int SK_MAX_STAGES = 5;
+constexpr int SK_MAX_N = 144;                         // tokens per tile: the most with three stages
+static_assert(3 * (SK_A_BYTES + SK_MAX_N * 256) + 1024 + 2 * 16 * 128 * 4 + 2 * 256 * 4 + 512 <= 232448 && SK_GROUPS <= 3,
+              "a ring stage for each group");
 constexpr int SK_XBUF = 2 * 16 * 128 * 4;             // the epilogue's exchange of gate and up values
 constexpr int SK_TAIL = SK_XBUF + 2 * 256 * 4 + (4 * SK_MAX_STAGES + 5) * 8 + 32;
 
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
-            mbar_init(&a_full[s], SK_DQ_WARPS / 2);
+            mbar_init(&a_full[s], 8);                // the warps of one group
             mbar_init(&b_full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
     constexpr uint32_t tmem_base = 0;
 
     if (warp < SK_DQ_WARPS) {
-        // ---- dequantise: group `grp` of eight warps takes every second unit; thread = row r of the
+        // ---- dequantise: group `grp` of eight warps takes every SK_GROUPS-th unit; thread = row r of the
         // stage, columns 32 h .. + 31 of both of its 64-column blocks
         const int grp = warp >> 3, r = (threadIdx.x & 255) >> 1, hf = threadIdx.x & 1;
         const int wpr = static_cast<int>(a.I / 8), nG = static_cast<int>(a.I >> a.lg), nzw = (nG + 7) / 8;
@@ -240,10 +244,11 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
         int pt = (u0 + grp) / a.ks % a.tiles, pk = (u0 + grp) % a.ks;   // tile and K stage of the next load
         uint32_t qo = 0, so = 0, zo = 0;              // codes: words; scales: elements; zero words
         int g = 0, rem0 = 0, rem1 = 0;                // group of block 0; K positions left from its first, and block 1's (<= 0: none)
-        const uint32_t qstep = GRAD ? 256u * static_cast<uint32_t>(wpr) : 32u;   // two stages of K
-        const uint32_t sstep = GRAD ? 256u * static_cast<uint32_t>(nG) : 256u >> a.lg;
-        const uint32_t zstep = GRAD ? 256u * static_cast<uint32_t>(nzw) : 0u;
-        const int gstep = GRAD ? 0 : 256 >> a.lg;
+        constexpr uint32_t GK = 128 * SK_GROUPS;      // K positions from a group's unit to its next
+        const uint32_t qstep = GRAD ? GK * static_cast<uint32_t>(wpr) : GK / 8;
+        const uint32_t sstep = GRAD ? GK * static_cast<uint32_t>(nG) : GK >> a.lg;
+        const uint32_t zstep = GRAD ? GK * static_cast<uint32_t>(nzw) : 0u;
+        const int gstep = GRAD ? 0 : static_cast<int>(GK >> a.lg);
         const int blk = a.lg == 7 ? 0 : 64 >> a.lg;   // groups from block 0's columns to block 1's
         auto place = [&]() {
             int o, col;
@@ -275,14 +280,14 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
                 w.z[0] = __ldg(a.zeros + (r0 ? zo + (static_cast<uint32_t>(g) >> 3) : 0u));
                 if (blk) w.z[1] = __ldg(a.zeros + (r1 ? zo + (static_cast<uint32_t>(g + blk) >> 3) : 0u));
             }
-            pk += 2;
+            pk += SK_GROUPS;
             if (pk < a.ks) {
                 qo += qstep;
                 so += sstep;
                 zo += zstep;
                 g += gstep;
-                rem0 -= 256;
-                rem1 -= 256;
+                rem0 -= static_cast<int>(GK);
+                rem1 -= static_cast<int>(GK);
             } else {
                 while (pk >= a.ks) {                  // (K may be a single stage)
                     pk -= a.ks;
@@ -301,15 +306,18 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
         const uint32_t P = 0x64006400u;
         const uint32_t row_off = static_cast<uint32_t>(r * 128);
         const uint32_t sx0 = static_cast<uint32_t>((hf * 4) ^ (r & 7));          // column 0 of this half, swizzled
-        uint32_t st = static_cast<uint32_t>(grp), ph = 1;   // (at least two ring stages)
+        // Unit n of the CTA sits in ring stage n % stages, in the phase of its n / stages-th use.  A
+        // parity tells neighbouring phases apart only: unit n waits for unit n - stages, and unit n - 2
+        // stages must be done by then, which the group's last unit, n - SK_GROUPS, has waited for
+        // (units are consumed in order) if stages >= SK_GROUPS.
+        uint32_t st = static_cast<uint32_t>(grp), ph = 1;
         bool ok = true;
-        for (int ub = u0 + grp; ub < u1 && ok; ub += 2 * SK_PF) {
+        for (int ub = u0 + grp; ub < u1 && ok; ub += SK_GROUPS * SK_PF) {
 #pragma unroll
             for (int u = 0; u < SK_PF; ++u) {
-                if (ub + 2 * u >= u1) break;
-                uint4 v[2][4];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
+                if (ub + SK_GROUPS * u >= u1) break;
+                uint4 v[4];
+                auto dequant = [&](int b) {
                     const int gb = raw[u].g + (b ? blk : 0);
                     uint32_t z = 8u;
                     if (a.zeros) z = ((b && blk ? raw[u].z[1] : raw[u].z[0]) >> (4 * (gb & 7))) & 15u;
@@ -324,26 +332,27 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t w8 = w[j] >> 8;
                         // 1024 + c minus (1024 + z); (1024 + 16 c) / 16 minus (64 + z): both exact
-                        v[b][j].x = sk_mul(sk_sub((w[j] & 0x000F000Fu) | P, z0), d);
-                        v[b][j].y = sk_mul(sk_fma((w[j] & 0x00F000F0u) | P, 0x2C002C00u, z1), d);
-                        v[b][j].z = sk_mul(sk_sub((w8 & 0x000F000Fu) | P, z0), d);
-                        v[b][j].w = sk_mul(sk_fma((w8 & 0x00F000F0u) | P, 0x2C002C00u, z1), d);
+                        v[j].x = sk_mul(sk_sub((w[j] & 0x000F000Fu) | P, z0), d);
+                        v[j].y = sk_mul(sk_fma((w[j] & 0x00F000F0u) | P, 0x2C002C00u, z1), d);
+                        v[j].z = sk_mul(sk_sub((w8 & 0x000F000Fu) | P, z0), d);
+                        v[j].w = sk_mul(sk_fma((w8 & 0x00F000F0u) | P, 0x2C002C00u, z1), d);
                     }
-                }
-                fetch(raw[u]);
+                };
+                dequant(0);
                 ok = mbar_wait_warp(&empty[st], ph, abort_flag);
                 if (!ok) break;
                 // the eight lanes of a store phase (four rows, two halves) fall into eight 16-byte columns
                 uint8_t *dst = ring + st * stage + row_off;
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(dst + ((sx0 ^ j) << 4)) = v[j];
+                dequant(1);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<uint4 *>(dst + b * 16384 + ((sx0 ^ j) << 4)) = v[b][j];
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(dst + 16384 + ((sx0 ^ j) << 4)) = v[j];
+                fetch(raw[u]);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&a_full[st]);
-                st += 2;
+                st += SK_GROUPS;
                 if (st >= static_cast<uint32_t>(stages)) {
                     st -= static_cast<uint32_t>(stages);
                     ph ^= 1u;
@@ -511,7 +520,7 @@ cudaError_t launch_sk(const CUtensorMap &bmap, const SkinnyArgs &a, bool split, 
 
 SkinnyPlan skinny_plan(int64_t M, int64_t tiles, int64_t k, int num_sms) {
     SkinnyPlan p;
-    const int64_t tt = (M + 255) / 256;               // token tiles, of equal width
+    const int64_t tt = (M + SK_MAX_N - 1) / SK_MAX_N; // token tiles, of equal width
     p.n = static_cast<int>(((M + tt - 1) / tt + 15) / 16 * 16);
     p.token_tiles = static_cast<int>((M + p.n - 1) / p.n);
     p.tiles = static_cast<int>(tiles);
@@ -546,7 +555,7 @@ cudaError_t launch_skinny(bool grad, int epi, const CUtensorMap &bmap, SkinnyArg
     a.acc_cols = p.n <= 32 ? 32 : p.n <= 64 ? 64 : p.n <= 128 ? 128 : 256;
     const int fit = (232448 - 1024 - SK_TAIL) / (SK_A_BYTES + p.n * 256);
     a.stages = fit < SK_MAX_STAGES ? fit : SK_MAX_STAGES;
-    if (a.stages < 2) return cudaErrorInvalidConfiguration;
+    if (a.stages < SK_GROUPS) return cudaErrorInvalidConfiguration;
     if (grad) return launch_sk<true, EPI_OUT>(bmap, a, split, st);
     return epi == EPI_GATED ? launch_sk<false, EPI_GATED>(bmap, a, split, st)
                             : launch_sk<false, EPI_GATED_BWD>(bmap, a, split, st);
