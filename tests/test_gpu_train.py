@@ -112,6 +112,7 @@ SHAPES = [  # M, in, F, gs, zeros, s16, act
     (255, 256, 300, 32, True, True, "silu"),
     (257, 384, 1031, 128, True, True, "gelu"),
     (513, 2048, 704, 128, False, False, "silu"),
+    (600, 128, 2051, 64, True, True, "gelu"),
 ]
 
 
@@ -162,6 +163,7 @@ def test_gated_grad(awq, M, I, F, gs, zeros, s16, act):
     (7, 64, 1024, 128, False, True), (16, 1000, 192, 64, True, True), (19, 512, 1376 // 32 * 64, 64, False, True),
     (65, 2048, 256, 32, True, False), (130, 77, 640, 128, True, True), (256, 1031, 384, 128, False, True),
     (300, 4096, 512, 64, True, True), (700, 333, 2304, 128, True, False),
+    (600, 6001, 128, 64, True, True), (515, 1200, 4096, 128, False, True),
 ])
 def test_linear_grad(awq, M, O, I, gs, zeros, s16):
     w, D, s = packed(O, I, gs, zeros, s16, M + O)
@@ -186,7 +188,8 @@ def ce_case(M, V, I, seed, scale=0.05):
 
 
 CE_SHAPES = [(1, 1, 64), (1, 100, 128), (2, 257, 64), (3, 4096, 192), (13, 9973, 512), (128, 64, 1024),
-             (129, 1000, 320), (255, 5003, 64), (256, 256, 512), (300, 12345, 128), (511, 33, 2048)]
+             (129, 1000, 320), (255, 5003, 64), (256, 256, 512), (300, 12345, 128), (511, 33, 2048), (70, 20011, 256),
+             (2100, 16500, 64)]
 
 
 @pytest.mark.parametrize("M,V,I", CE_SHAPES)

@@ -825,7 +825,9 @@ static awq_status_t gated_dense(const uint16_t *dh, const uint16_t *x, int64_t M
     const int64_t O = 2 * F, Fp = round64(F);
     Workspace ws(st);
     size_t bytes = Workspace::up(2 * M * in) + Workspace::up(4 * M) + Workspace::up(4 * awq::DMAX_PARTS) + Workspace::up(2 * O * in);
-    if (dh) bytes += Workspace::up(4 * M) + Workspace::up(2 * M * 2 * Fp);
+    int splits = 1;
+    const int64_t parts = dh ? awq::gemm_part_vecs(M, in, 2 * Fp, sms, &splits) : 0;
+    if (dh) bytes += Workspace::up(4 * M) + Workspace::up(2 * M * 2 * Fp) + Workspace::up(16 * parts);
     if (awq_status_t s = ws.reserve(bytes)) return s;
     uint16_t *xs = ws.take<uint16_t>(M * in);
     float *sx = ws.take<float>(M);
@@ -833,10 +835,12 @@ static awq_status_t gated_dense(const uint16_t *dh, const uint16_t *x, int64_t M
     uint16_t *w16 = ws.take<uint16_t>(O * in);
     int *grow = dh ? ws.take<int>(M) : nullptr;
     uint16_t *d16 = dh ? ws.take<uint16_t>(M * 2 * Fp) : nullptr;
+    float4 *part4 = parts ? ws.take<float4>(parts) : nullptr;
     AWQ_CUDA(awq::launch_rows16(x, s16, M, in, in, dh, F, scales, O * (in / group_size), false, xs, sx, grow,
                                 dmax, st));
     AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, O, in, group_size, dmax, w16, st));
     awq::GemmArgs a{};
+    a.splits = 1;
     a.M = M;
     a.bn = awq::gemm_tile_cols(M, 2 * (dh ? Fp : F), sms);
     a.mt = ceil_div(M, 256);
@@ -863,6 +867,8 @@ static awq_status_t gated_dense(const uint16_t *dh, const uint16_t *x, int64_t M
     if (!dh) return AWQ_OK;
     // dx = ([dg | du] W) / s: K runs over the gate rows of W, then its up rows
     awq::GemmArgs b{};
+    b.splits = splits;
+    b.part4 = part4;
     b.M = M;
     b.N = in;
     b.bn = awq::gemm_tile_cols(M, in, sms);
@@ -1031,8 +1037,10 @@ awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, in
         return AWQ_OK;
     }
     Workspace ws(st);
+    int splits;
+    const int64_t parts = awq::gemm_part_vecs(M, in, out, sms, &splits);
     if (awq_status_t s = ws.reserve(Workspace::up(2 * M * ld) + Workspace::up(4 * M) + Workspace::up(4 * awq::DMAX_PARTS) +
-                                    Workspace::up(2 * out * in)))
+                                    Workspace::up(2 * out * in) + Workspace::up(16 * parts)))
         return s;
     uint16_t *d16 = ws.take<uint16_t>(M * ld);
     float *sx = ws.take<float>(M);
@@ -1042,6 +1050,8 @@ awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, in
                                 nullptr, dmax, st));
     AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, out, in, group_size, dmax, w16, st));
     awq::GemmArgs b{};
+    b.splits = splits;
+    b.part4 = parts ? ws.take<float4>(parts) : nullptr;
     b.M = M;
     b.N = in;
     b.bn = awq::gemm_tile_cols(M, in, sms);
@@ -1085,16 +1095,20 @@ awq_status_t awq_cross_entropy(const uint16_t *x, int64_t M, int64_t in, const u
     if (awq_status_t s = device_info(&sms)) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     awq::GemmArgs a{};
+    a.splits = 1;
     a.M = M;
     a.N = a.V = V;
+    a.x = x;
+    a.w = W;
+    a.inner = static_cast<int>(in);
     a.bn = awq::gemm_tile_cols(M, V, sms);
     a.mt = ceil_div(M, 256);
     a.nt = ceil_div(V, a.bn);
     a.nk[0] = static_cast<int>(in / 64);
     Workspace ws(st);
-    if (awq_status_t s = ws.reserve(Workspace::up(4 * M) + Workspace::up(sizeof(float2) * M * a.nt))) return s;
+    if (awq_status_t s = ws.reserve(Workspace::up(4 * M) + Workspace::up(sizeof(float2) * M * 2 * a.nt))) return s;
     a.tgt = ws.take<float>(M);
-    a.part = ws.take<float2>(M * a.nt);
+    a.part = ws.take<float2>(M * 2 * a.nt);
     a.labels = labels;
     awq::GemmMaps maps;
     if (awq_status_t s = map_kmajor(&maps.a, true, x, in, M, in, 128)) return s;
@@ -1103,7 +1117,7 @@ awq_status_t awq_cross_entropy(const uint16_t *x, int64_t M, int64_t in, const u
     kt_begin(4, st);
     AWQ_CUDA(awq::launch_gemm16(awq::EPI_CE, true, false, maps, a, sms, st));
     kt_end(4, st);
-    AWQ_CUDA(awq::launch_ce_final(a.part, a.nt, M, labels, V, a.tgt, loss, lse, st));
+    AWQ_CUDA(awq::launch_ce_final(a.part, 2 * a.nt, M, labels, V, a.tgt, loss, lse, st));
     return AWQ_OK;
 }
 
@@ -1131,8 +1145,12 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
     size_t bytes = Workspace::up(2 * M * ldd);
     if (pieces > 1) bytes += Workspace::up(4 * M * in);
     if (dW) bytes += Workspace::up(2 * M * in);
+    int splits;                                       // of dx's K, the piece's entries
+    const int64_t parts = awq::gemm_part_vecs(M, in, vc < V ? vc : V, sms, &splits);
+    bytes += Workspace::up(16 * parts);
     if (awq_status_t s = ws.reserve(bytes)) return s;
     uint16_t *d16 = ws.take<uint16_t>(M * ldd);
+    float4 *part4 = parts ? ws.take<float4>(parts) : nullptr;
     float *acc = pieces > 1 ? ws.take<float>(M * in) : nullptr;
     uint16_t *xz = nullptr;
     if (dW) {
@@ -1146,6 +1164,7 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
         const uint16_t *Wp = W + v0 * in;
         awq::GemmMaps maps;
         awq::GemmArgs a{};
+        a.splits = 1;
         a.M = M;
         a.N = n;
         a.V = V;
@@ -1163,6 +1182,10 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
         if (awq_status_t s = map_kmajor(&maps.b, true, Wp, in, n, in, a.bn / 2)) return s;
         AWQ_CUDA(awq::launch_gemm16(awq::EPI_CE_BWD, true, false, maps, a, sms, st));
         awq::GemmArgs b{};
+        // (the last piece may be short: eight slabs to a split there, too)
+        b.splits = ceil_div(n, 64) / 8 < splits ? ceil_div(n, 64) / 8 : splits;
+        if (b.splits < 2) b.splits = 1;
+        b.part4 = part4;
         b.M = M;
         b.N = in;
         b.bn = awq::gemm_tile_cols(M, in, sms);
@@ -1178,6 +1201,7 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
         AWQ_CUDA(awq::launch_gemm16(awq::EPI_OUT, true, false, maps, b, sms, st));
         if (dW) {
             awq::GemmArgs c{};
+            c.splits = 1;
             c.M = n;
             c.N = in;
             c.bn = awq::gemm_tile_cols(n, in, sms);

@@ -213,6 +213,8 @@ struct GemmArgs {
     int mt, nt;                 // tiles of 256 rows and of bn columns (EPI_GATED*: of bn / 2 gate columns)
     int bn;                     // tile columns of the pair
     int nk[2];                  // 64-deep K slabs of the two K segments
+    int splits;                 // K splits of each tile (EPI_OUT; 1 otherwise)
+    float4 *part4;              // their partial sums [tiles * splits][bn / 4][256]
     int a_seg, b_seg;           // first K coordinate of the second segment in A and in B
     // scales
     const float *sx;            // [M]: A's row m carries 1 / sx[m] (a power of two)
@@ -228,7 +230,8 @@ struct GemmArgs {
     int64_t V, v0;              // vocabulary; first entry of this piece
     const float *lse, *dloss;   // [M]
     float *tgt;                 // [M] the label's logit
-    float2 *part;               // [nt][M] (maximum, sum of exponentials)
+    float2 *part;               // [2 nt][M] (maximum, sum of exponentials) without the label's
+    const uint16_t *x, *w;      // the operands themselves, rows of `inner` columns (the labels' logits)
     // outputs
     uint16_t *out;              // bf16
     uint16_t *d16;              // [M][ldd] 16-bit gradients
@@ -237,6 +240,8 @@ struct GemmArgs {
     bool first, last;           // first: acc is not read; last: the result goes to out
 };
 int gemm_tile_cols(int64_t M, int64_t N, int num_sms);
+// K splits of an EPI_OUT product, and the float4 of workspace for their partial sums.
+int64_t gemm_part_vecs(int64_t M, int64_t N, int64_t k, int num_sms, int *splits);
 cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, const GemmArgs &a, int num_sms,
                           cudaStream_t st);
 cudaError_t launch_ce_final(const float2 *part, int nt, int64_t M, const int64_t *labels, int64_t V,

@@ -16,7 +16,8 @@
 // x bn columns (bn <= 256, a multiple of 32) on tcgen05.mma.cta_group::2, M = 256, N = bn,
 // K = 16.  Each CTA stages its own 128 rows of A and half of B's columns, 64 deep, by TMA into a
 // 192 KB ring (six stages at bn = 256); the accumulator has two 256-column halves of TMEM, so the epilogue of a
-// tile overlaps the main loop of the next.  Warps: 0 TMA, 1 MMA, 4-7 epilogue (lane = row).
+// tile overlaps the main loop of the next.  Warps: 0 TMA, 1 MMA, 4-11 epilogue (lane = row, two warps a
+// row's alternate 16-column chunks).
 // A K-major operand lies as [rows][64 k] in 128-byte swizzled rows; an operand read along its
 // rows (MN-major) as blocks of [64 k][64 n], 8 KB each, in the same swizzle.
 //
@@ -44,8 +45,8 @@ namespace {
 constexpr int GM_MAX_STAGES = 12;
 constexpr int GM_A_BYTES = 128 * SLAB_K * 2;          // 16 KB: this CTA's rows of A
 constexpr int GM_RING = 192 * 1024;                   // operand ring
-constexpr int GM_THREADS = 256;
-constexpr int GM_EPI_WARP0 = 4;
+constexpr int GM_THREADS = 384;
+constexpr int GM_EPI_WARP0 = 4;                       // warps 4-11: two per TMEM lane quadrant, alternate 16-column chunks
 constexpr int GM_BAND = 8;                            // row tiles walked together
 constexpr uint32_t GM_TMEM = 512;
 constexpr int GM_BARS = 2 * GM_MAX_STAGES + 4 + 1;
@@ -77,6 +78,11 @@ __device__ __forceinline__ Tile decode_tile(int t, int mt, int nt) {
     return o;
 }
 
+// First slab of K split i.
+__device__ __forceinline__ int split_at(int i, int nk, int splits) {
+    return static_cast<int>(static_cast<int64_t>(nk) * i / splits);
+}
+
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
@@ -101,13 +107,13 @@ __device__ __forceinline__ void store_bf16_16(uint16_t *p, const float (&v)[16],
 // loads are warp-wide: rows beyond M skip only the work between them, and every loop ends in a
 // warp barrier.
 
-__device__ __forceinline__ void epi_gated(const GemmArgs &a, uint32_t acc, int64_t row, int64_t f0) {
+__device__ __forceinline__ void epi_gated(const GemmArgs &a, uint32_t acc, int64_t row, int64_t f0, int par) {
     const int half = a.bn / 2;
     const float sc = row < a.M ? __ldg(a.sx + row) : 0.0f;
     const float sw = dq_scale(a.dmax);
     const bool vec = a.F % 8 == 0;
 #pragma unroll 1
-    for (int c = 0; c < half; c += 16) {
+    for (int c = 16 * par; c < half; c += 32) {
         uint32_t g[16], u[16];
         tmem_ld16_wait(acc + c, g);
         tmem_ld16_wait(acc + half + c, u);
@@ -123,7 +129,7 @@ __device__ __forceinline__ void epi_gated(const GemmArgs &a, uint32_t acc, int64
     }
 }
 
-__device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t f0) {
+__device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t f0, int par) {
     const int half = a.bn / 2;
     const bool ok = row < a.M;
     const float sc = ok ? __ldg(a.sx + row) : 0.0f;
@@ -132,13 +138,28 @@ __device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, i
     // 2^-e of this token's gradients
     const float sd = ok ? ldexpf(1.0f, -dgu_exp(__ldg(a.grow + row), a.inner, kw)) : 0.0f;
     const uint16_t *dh = a.dh + (ok ? row : 0) * a.F;
+    const bool vec = a.F % 8 == 0;
 #pragma unroll 1
-    for (int c = 0; c < half; c += 16) {
+    for (int c = 16 * par; c < half; c += 32) {
         uint32_t g[16], u[16];
         tmem_ld16_wait(acc + c, g);
         tmem_ld16_wait(acc + half + c, u);
         if (ok && f0 + c < a.Fp) {
         uint32_t pg[8], pu[8];
+        float dv[16];
+        if (vec && f0 + c + 16 <= a.F) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(dh + f0 + c);
+            const uint4 p0 = __ldg(p), p1 = __ldg(p + 1);
+            const uint32_t w[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                dv[2 * k] = __uint_as_float(w[k] << 16);
+                dv[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) dv[k] = f0 + c + k < a.F ? bf16f(__ldg(dh + f0 + c + k)) : 0.0f;
+        }
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
             float dg[2], du[2];
@@ -148,7 +169,7 @@ __device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, i
                 const float gv = (__uint_as_float(g[k + j]) * sc) * sw, uv = (__uint_as_float(u[k + j]) * sc) * sw;
                 float da;
                 const float av = act_both(gv, a.act, da);
-                const float d = f < a.F ? bf16f(__ldg(dh + f)) * sd : 0.0f;
+                const float d = dv[k + j] * sd;
                 // columns of the padding are exact zeros whatever the tile holds there
                 dg[j] = f < a.F ? (d * uv) * da : 0.0f;
                 du[j] = f < a.F ? d * av : 0.0f;
@@ -168,10 +189,25 @@ __device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, i
     }
 }
 
-__device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0) {
-    const bool ok = row < a.M;
-    float sc = 1.0f, sw = 1.0f;
-    if (a.grow) {                                      // gated gradient: 2^e of the token
+// A K split's partial sums: this unit's slot [bn / 4][256 rows] of four columns.
+__device__ __forceinline__ void epi_part(const GemmArgs &a, uint32_t acc, int unit, int r, int par) {
+    float4 *p = a.part4 + static_cast<int64_t>(unit) * (a.bn / 4) * 256;
+#pragma unroll 1
+    for (int c = 16 * par; c < a.bn; c += 32) {
+        uint32_t v[16];
+        tmem_ld16_wait(acc + c, v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            p[(c / 4 + k) * 256 + r] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                                   __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+        __syncwarp();
+    }
+}
+
+// A row's scale, as two factors that are normal floats each.  (Warp-wide: the layer's exponent.)
+__device__ __forceinline__ void out_scales(const GemmArgs &a, bool ok, int64_t row, float &sc, float &sw) {
+    sc = sw = 1.0f;
+    if (a.grow) {                                     // gated gradient: 2^e of the token
         const int kw = dq_exp(a.dmax);
         sc = ok ? ldexpf(1.0f, dgu_exp(__ldg(a.grow + row), a.inner, kw)) : 0.0f;
         sw = ldexpf(1.0f, kw);
@@ -179,90 +215,160 @@ __device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t
         sc = ok ? __ldg(a.sx + row) : 0.0f;
         sw = dq_scale(a.dmax);
     }
+}
+
+// C consecutive scaled columns n .. of a row: divided by s, added to the pieces before, stored.
+template <int C>
+__device__ __forceinline__ void out_columns(const GemmArgs &a, int64_t row, int64_t n, float (&v)[C]) {
+    if (a.s16) {
+#pragma unroll
+        for (int k = 0; k < C; k += 4) {
+            const uint2 sv = __ldg(reinterpret_cast<const uint2 *>(a.s16 + n + k));
+            const __half2 s0 = *reinterpret_cast<const __half2 *>(&sv.x), s1 = *reinterpret_cast<const __half2 *>(&sv.y);
+            v[k] = __fdividef(v[k], __low2float(s0));
+            v[k + 1] = __fdividef(v[k + 1], __high2float(s0));
+            v[k + 2] = __fdividef(v[k + 2], __low2float(s1));
+            v[k + 3] = __fdividef(v[k + 3], __high2float(s1));
+        }
+    }
+    if (a.acc) {
+        float4 *q = reinterpret_cast<float4 *>(a.acc + row * a.N + n);
+        if (!a.first) {
+#pragma unroll
+            for (int k = 0; k < C / 4; ++k) {
+                const float4 p = q[k];
+                v[4 * k] += p.x; v[4 * k + 1] += p.y; v[4 * k + 2] += p.z; v[4 * k + 3] += p.w;
+            }
+        }
+        if (!a.last) {
+#pragma unroll
+            for (int k = 0; k < C / 4; ++k) q[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            return;
+        }
+    }
+    uint2 *o = reinterpret_cast<uint2 *>(a.out + row * a.N + n);
+    if constexpr (C % 8 == 0) {
+#pragma unroll
+        for (int k = 0; k < C / 8; ++k)
+            reinterpret_cast<uint4 *>(o)[k] =
+                make_uint4(bf16x2(v[8 * k], v[8 * k + 1]), bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                           bf16x2(v[8 * k + 4], v[8 * k + 5]), bf16x2(v[8 * k + 6], v[8 * k + 7]));
+    } else {
+        o[0] = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+    }
+}
+
+__device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int par) {
+    const bool ok = row < a.M;
+    float sc, sw;
+    out_scales(a, ok, row, sc, sw);
 #pragma unroll 1
-    for (int c = 0; c < a.bn; c += 16) {
+    for (int c = 16 * par; c < a.bn; c += 32) {
         uint32_t r[16];
         tmem_ld16_wait(acc + c, r);
         if (ok && n0 + c < a.N) {                     // N is a multiple of 64: a 16-column chunk is in or out
-        float v[16];
+            float v[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = (__uint_as_float(r[k]) * sc) * sw;
-        if (a.s16) {
-            const uint4 *sp = reinterpret_cast<const uint4 *>(a.s16 + n0 + c);
-            const uint4 s0 = __ldg(sp), s1 = __ldg(sp + 1);
-            const uint32_t sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const __half2 h = *reinterpret_cast<const __half2 *>(&sv[k]);
-                v[2 * k] = v[2 * k] / __low2float(h);
-                v[2 * k + 1] = v[2 * k + 1] / __high2float(h);
-            }
-        }
-        if (a.acc) {
-            float4 *q = reinterpret_cast<float4 *>(a.acc + row * a.N + n0 + c);
-            if (!a.first) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 p = q[k];
-                    v[4 * k] += p.x; v[4 * k + 1] += p.y; v[4 * k + 2] += p.z; v[4 * k + 3] += p.w;
-                }
-            }
-            if (!a.last) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) q[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-            }
-        }
-        if (!a.acc || a.last) store_bf16_16(a.out + row * a.N + n0 + c, v, true, 16);
+            for (int k = 0; k < 16; ++k) v[k] = (__uint_as_float(r[k]) * sc) * sw;
+            out_columns<16>(a, row, n0 + c, v);
         }
         __syncwarp();
     }
+}
+
+// Split tiles: block (tile, four columns), thread = row; the splits in order.
+__global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant__ GemmArgs a) {
+    const Tile tl = decode_tile(static_cast<int>(blockIdx.x), a.mt, a.nt);
+    const int64_t row = static_cast<int64_t>(tl.m) * 256 + threadIdx.x;
+    const int64_t n = static_cast<int64_t>(tl.n) * a.bn + blockIdx.y * 4;
+    float sc, sw;
+    out_scales(a, row < a.M, row, sc, sw);
+    if (row >= a.M || n >= a.N) return;
+    const float4 *p = a.part4 + (static_cast<int64_t>(blockIdx.x) * a.splits * (a.bn / 4) + blockIdx.y) * 256 + threadIdx.x;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+    for (int i = 0; i < a.splits; ++i) {
+        const float4 w = __ldg(p + static_cast<int64_t>(i) * (a.bn / 4) * 256);
+        v[0] += w.x;
+        v[1] += w.y;
+        v[2] += w.z;
+        v[3] += w.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = (v[k] * sc) * sw;
+    out_columns<4>(a, row, n, v);
 }
 
 constexpr float LOG2E = 1.4426950408889634f;
 
-__device__ __forceinline__ void epi_ce(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int ntile) {
+__device__ __forceinline__ void epi_ce(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int ntile, int par) {
     const bool ok = row < a.M;
     const int64_t lab = ok ? __ldg(a.labels + row) : -1;
     float mx = -INFINITY, sum = 0.0f;
 #pragma unroll 1
-    for (int c = 0; c < a.bn; c += 16) {
+    for (int c = 16 * par; c < a.bn; c += 32) {
         uint32_t r[16];
         tmem_ld16_wait(acc + c, r);
         if (ok && n0 + c < a.N) {
-        float v[16], cm = -INFINITY;
+            float v[16], cm = -INFINITY;
+            const int64_t j = lab - n0 - c;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            v[k] = n0 + c + k < a.N ? __uint_as_float(r[k]) : -INFINITY;
-            cm = fmaxf(cm, v[k]);
-        }
-        const int64_t j = lab - n0 - c;
-        if (j >= 0 && j < 16 && lab < a.N) {
+            for (int k = 0; k < 16; ++k) {
+                // the label's own term joins in the last step (ce_final_kernel)
+                v[k] = n0 + c + k < a.N && j != k ? __uint_as_float(r[k]) : -INFINITY;
+                cm = fmaxf(cm, v[k]);
+            }
+            const float nm = fmaxf(mx, cm);
+            // a tile of nothing but -inf (or NaN) keeps a finite reference
+            const float ref = nm == -INFINITY ? 0.0f : nm;
+            float s = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-                if (j == k) a.tgt[row] = v[k];
-        }
-        const float nm = fmaxf(mx, cm);
-        // a tile of nothing but -inf (or NaN) keeps a finite reference
-        const float ref = nm == -INFINITY ? 0.0f : nm;
-        float s = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) s += exp2f((v[k] - ref) * LOG2E);
-        sum = sum * exp2f((mx - ref) * LOG2E) + s;
-        mx = nm;
+            for (int k = 0; k < 16; ++k) s += exp2f((v[k] - ref) * LOG2E);
+            sum = sum * exp2f((mx - ref) * LOG2E) + s;
+            mx = nm;
         }
         __syncwarp();
     }
-    if (ok) a.part[static_cast<int64_t>(ntile) * a.M + row] = make_float2(mx, sum);
+    if (ok) a.part[static_cast<int64_t>(2 * ntile + par) * a.M + row] = make_float2(mx, sum);
 }
 
-__device__ __forceinline__ void epi_ce_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0) {
+// The labels' logits in fp32 by the two warps that have no other work, a warp per token: products of
+// bf16 values are exact, so this is the fp32 rounding of a few additions per lane.  The tensor
+// cores' accumulation truncates (2.5e-6 of the loss at 4096 columns), which shows where the
+// label dominates its row; the other terms of the sum average it out.
+__device__ __forceinline__ void ce_labels(const GemmArgs &a, int first, int step) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t m = first; m < a.M; m += step) {
+        const int64_t lab = __ldg(a.labels + m);
+        if (lab < 0 || lab >= a.N) continue;
+        const uint4 *x = reinterpret_cast<const uint4 *>(a.x + m * a.inner);
+        const uint4 *w = reinterpret_cast<const uint4 *>(a.w + lab * a.inner);
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 4
+        for (int i = lane; i < a.inner / 8; i += 32) {
+            const uint4 p = __ldg(x + i), q = __ldg(w + i);
+            const uint32_t pv[4] = {p.x, p.y, p.z, p.w}, qv[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s0 = fmaf(__uint_as_float(pv[k] << 16), __uint_as_float(qv[k] << 16), s0);
+                s1 = fmaf(__uint_as_float(pv[k] & 0xFFFF0000u), __uint_as_float(qv[k] & 0xFFFF0000u), s1);
+            }
+        }
+        float s = s0 + s1;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        if (lane == 0) a.tgt[m] = s;
+    }
+}
+
+__device__ __forceinline__ void epi_ce_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int par) {
     const bool ok = row < a.M;
     const int64_t lab = ok ? __ldg(a.labels + row) : -1;
     const bool scored = lab >= 0 && lab < a.V;
     const float lse = ok ? __ldg(a.lse + row) : 0.0f;
     const float w = ok ? __ldg(a.dloss + row) : 0.0f;
 #pragma unroll 1
-    for (int c = 0; c < a.bn; c += 16) {
+    for (int c = 16 * par; c < a.bn; c += 32) {
         uint32_t r[16];
         tmem_ld16_wait(acc + c, r);
         if (ok && n0 + c < a.N) {
@@ -298,7 +404,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int tiles = a.mt * a.nt;
+    const int tiles = a.mt * a.nt * a.splits;          // units: the K splits of a tile are neighbours
     const int nk = a.nk[0] + a.nk[1];                  // 64-deep slabs of both K segments
     const int bh = a.bn / 2;                           // B columns of this CTA
     const int nb = (bh + 63) / 64;                     // blocks of 64 columns when B is MN-major
@@ -312,7 +418,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&acc_full[h], 1);
-            mbar_init(&acc_empty[h], 2 * 4);           // epilogue warps of both CTAs
+            mbar_init(&acc_empty[h], 2 * 8);           // epilogue warps of both CTAs
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -336,12 +442,13 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
         bool ok = true;
         const uint32_t bytes = GM_A_BYTES + (B_MN ? nb * 8192 : bh * 128);
         for (int t = pair; t < tiles && ok; t += pairs) {
-            const Tile tl = decode_tile(t, a.mt, a.nt);
+            const Tile tl = decode_tile(t / a.splits, a.mt, a.nt);
             const int m0 = tl.m * 256 + static_cast<int>(rank) * 128;
             const int n0 = EPI == EPI_GATED || EPI == EPI_GATED_BWD
                                ? tl.n * bh + static_cast<int>(rank) * static_cast<int>(a.F)   // gate | up rows
                                : tl.n * a.bn + static_cast<int>(rank) * bh;
-            for (int kb = 0; kb < nk; ++kb) {
+            const int k0 = split_at(t % a.splits, nk, a.splits), k1 = split_at(t % a.splits + 1, nk, a.splits);
+            for (int kb = k0; kb < k1; ++kb) {
                 ok = mbar_wait_warp(&empty[st], ph, abort_flag);
                 if (!ok) break;
                 const uint32_t bar = cluster_addr(&full[st], 0);
@@ -385,7 +492,8 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + h * 256;
-                for (int kb = 0; kb < nk; ++kb) {
+                const int k0 = split_at(t % a.splits, nk, a.splits), k1 = split_at(t % a.splits + 1, nk, a.splits);
+                for (int kb = k0; kb < k1; ++kb) {
                     ok = mbar_wait_warp(&full[st], ph, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
@@ -394,9 +502,9 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
                     for (int k = 0; k < SLAB_K / 16; ++k)
                         umma_f16_pair_lead(lead, d, A_MN ? sdesc_mnmajor_sw128(sa + k * 2048) : sdesc_kmajor_sw128(sa + k * 32),
                                           B_MN ? sdesc_mnmajor_sw128(sb + k * 2048) : sdesc_kmajor_sw128(sb + k * 32),
-                                           idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                                           idesc, (kb > k0 || k > 0) ? 1u : 0u);
                     umma_commit_pair_lead(lead, &empty[st], 0x3);
-                    if (kb == nk - 1) umma_commit_pair_lead(lead, &acc_full[h], 0x3);
+                    if (kb == k1 - 1) umma_commit_pair_lead(lead, &acc_full[h], 0x3);
                     if (++st == static_cast<uint32_t>(stages)) {
                         st = 0;
                         ph ^= 1u;
@@ -406,22 +514,30 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
             if (elect_one()) umma_commit_pair(drain, 0x3);
             __syncwarp();
         }
-    } else if (warp >= GM_EPI_WARP0) {
-        const int quad = warp & 3;
+    } else if (warp < GM_EPI_WARP0) {
+        if constexpr (EPI == EPI_CE)
+            ce_labels(a, static_cast<int>(blockIdx.x) * 2 + warp - 2, static_cast<int>(gridDim.x) * 2);
+    } else {
+        const int quad = warp & 3, par = (warp - GM_EPI_WARP0) >> 2;
         uint32_t ti = 0;
         for (int t = pair; t < tiles; t += pairs, ++ti) {
-            const Tile tl = decode_tile(t, a.mt, a.nt);
+            const Tile tl = decode_tile(t / a.splits, a.mt, a.nt);
             const uint32_t h = ti & 1u;
             const bool ok = mbar_wait_sleep(&acc_full[h], (ti >> 1) & 1u, abort_flag);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const uint32_t acc = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + h * 256;
             const int64_t row = static_cast<int64_t>(tl.m) * 256 + rank * 128 + quad * 32 + lane;
-            if constexpr (EPI == EPI_GATED) epi_gated(a, acc, row, static_cast<int64_t>(tl.n) * bh);
-            if constexpr (EPI == EPI_GATED_BWD) epi_gated_bwd(a, acc, row, static_cast<int64_t>(tl.n) * bh);
-            if constexpr (EPI == EPI_OUT) epi_out(a, acc, row, static_cast<int64_t>(tl.n) * a.bn);
-            if constexpr (EPI == EPI_CE) epi_ce(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, tl.n);
-            if constexpr (EPI == EPI_CE_BWD) epi_ce_bwd(a, acc, row, static_cast<int64_t>(tl.n) * a.bn);
+            if constexpr (EPI == EPI_GATED) epi_gated(a, acc, row, static_cast<int64_t>(tl.n) * bh, par);
+            if constexpr (EPI == EPI_GATED_BWD) epi_gated_bwd(a, acc, row, static_cast<int64_t>(tl.n) * bh, par);
+            if constexpr (EPI == EPI_OUT) {
+                if (a.splits > 1)
+                    epi_part(a, acc, t, static_cast<int>(rank) * 128 + quad * 32 + lane, par);
+                else
+                    epi_out(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par);
+            }
+            if constexpr (EPI == EPI_CE) epi_ce(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, tl.n, par);
+            if constexpr (EPI == EPI_CE_BWD) epi_ce_bwd(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[h], 0));
@@ -471,7 +587,7 @@ cudaError_t launch_t(const GemmMaps &maps, const GemmArgs &a, int num_sms, cudaS
         if (pairs < 1) return cudaErrorInvalidConfiguration;
         if (dev >= 0 && dev < 64) max_pairs[dev] = pairs;
     }
-    const int tiles = a.mt * a.nt;
+    const int tiles = a.mt * a.nt * a.splits;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
     return cudaLaunchKernelEx(&cfg, kernel, maps, a);
 }
@@ -498,8 +614,27 @@ int gemm_tile_cols(int64_t M, int64_t N, int num_sms) {
     return best;
 }
 
+int64_t gemm_part_vecs(int64_t M, int64_t N, int64_t k, int num_sms, int *splits) {
+    const int bn = gemm_tile_cols(M, N, num_sms);
+    const int64_t tiles = ((M + 255) / 256) * ((N + bn - 1) / bn), nk = (k + 63) / 64, pairs = num_sms / 2;
+    // Tiles that leave half of the pairs idle or more: K is split among them, at least 8 slabs (4 us)
+    // to a split, which the second kernel's 3 us are worth.
+    int64_t s = pairs / tiles;
+    s = s < nk / 8 ? s : nk / 8;
+    *splits = static_cast<int>(s < 2 ? 1 : s);
+    return *splits > 1 ? tiles * *splits * (bn / 4) * 256 : 0;
+}
+
 cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, const GemmArgs &a, int num_sms,
                           cudaStream_t st) {
+    if (a.splits > 1) {
+        const cudaError_t e = a_mn ? launch_t<EPI_OUT, true, true, true>(maps, a, num_sms, st)
+                              : bf16 ? launch_t<EPI_OUT, true, false, true>(maps, a, num_sms, st)
+                                     : launch_t<EPI_OUT, false, false, true>(maps, a, num_sms, st);
+        if (e != cudaSuccess) return e;
+        gemm_finish_kernel<<<dim3(static_cast<unsigned>(a.mt * a.nt), static_cast<unsigned>(a.bn / 4)), 256, 0, st>>>(a);
+        return cudaGetLastError();
+    }
     switch (epi) {
         case EPI_GATED: return launch_t<EPI_GATED, false, false, false>(maps, a, num_sms, st);
         case EPI_GATED_BWD: return launch_t<EPI_GATED_BWD, false, false, false>(maps, a, num_sms, st);
@@ -515,7 +650,7 @@ cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, c
 // ------------------------------------------------------------------ cross entropy, last step
 namespace {
 
-// One warp per token: the tiles' (maximum, sum) pairs to the log of the sum of exponentials, in
+// One warp per token: the half tiles' (maximum, sum) pairs to the log of the sum of exponentials, in
 // the order of the tiles for each lane and by a fixed tree across lanes.
 __global__ void __launch_bounds__(256) ce_final_kernel(const float2 *__restrict__ part, int nt, int64_t M,
                                                        const int64_t *__restrict__ labels, int64_t V,
@@ -539,10 +674,18 @@ __global__ void __launch_bounds__(256) ce_final_kernel(const float2 *__restrict_
         mx = nm;
     }
     if (lane == 0) {
-        const float l = mx + logf(sum);
         const int64_t lab = __ldg(labels + m);
-        lse[m] = l;
-        loss[m] = lab >= 0 && lab < V ? l - __ldg(tgt + m) : 0.0f;
+        if (lab < 0 || lab >= V) {
+            lse[m] = mx + logf(sum);
+            loss[m] = 0.0f;
+            return;
+        }
+        // with the label's term t, which `part` leaves out: loss = log(1 + sum e^(mx - t)),
+        // written so that neither a label far above the others nor one far below loses digits
+        const float t = __ldg(tgt + m), d = mx - t;
+        const float l = d > 0.0f ? d + logf(sum + expf(-d)) : log1pf(sum * expf(d));
+        loss[m] = l;
+        lse[m] = t + l;
     }
 }
 
