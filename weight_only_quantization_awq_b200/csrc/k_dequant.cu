@@ -108,8 +108,41 @@ __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict_
     const int64_t m = blockIdx.x - DMAX_PARTS;
     const uint16_t *r = x + m * cols;
     const bool vec = cols % 8 == 0;
+    constexpr int KEEP = 4;                           // chunks of a thread that stay in registers between the passes
+    float kept[KEEP][8];
     float mx = 0.0f;
-    for (int64_t c = threadIdx.x * 8; c < cols; c += blockDim.x * 8) {
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) {
+        const int64_t c = (i * 256 + threadIdx.x) * 8;
+        if (c < cols) {
+            row_chunk(r, s16, c, cols, vec, kept[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kept[i][e] = 0.0f;
+        }
+    }
+    float md = 0.0f;
+    if (grow) {                                       // the token's largest |dh|
+        const uint16_t *dr = dh + m * F;
+        if (F % 8 == 0) {
+            unsigned mb = 0u;                         // magnitudes of bf16 order as their bits
+#pragma unroll 4
+            for (int64_t f = threadIdx.x; f < F / 8; f += 256) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(dr) + f);
+                mb = __vmaxu2(mb, __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu),
+                                           __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
+            }
+            md = __uint_as_float(max(mb >> 16, mb & 0xFFFFu) << 16);
+        } else {
+            for (int64_t f = threadIdx.x; f < F; f += 256)
+                md = fmaxf(md, fabsf(__uint_as_float(static_cast<uint32_t>(__ldg(dr + f)) << 16)));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(kept[i][e]));
+    for (int64_t c = (KEEP * 256 + threadIdx.x) * 8; c < cols; c += 256 * 8) {
         float v[8];
         row_chunk(r, s16, c, cols, vec, v);
 #pragma unroll
@@ -119,9 +152,7 @@ __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict_
     const int k = scale_exp(mx, 15);
     const float sc = ldexpf(1.0f, -k);
     float sq = 0.0f;                                  // of the scaled values: no overflow
-    for (int64_t c = threadIdx.x * 8; c < cols; c += blockDim.x * 8) {
-        float v[8];
-        row_chunk(r, s16, c, cols, vec, v);
+    auto put = [&](int64_t c, const float (&v)[8]) {
         uint32_t h[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -132,14 +163,20 @@ __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict_
         }
         // ld is a multiple of 8: a last partial chunk stays inside its own row
         *reinterpret_cast<uint4 *>(out + m * ld + c) = make_uint4(h[0], h[1], h[2], h[3]);
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) {
+        const int64_t c = (i * 256 + threadIdx.x) * 8;
+        if (c < cols) put(c, kept[i]);
+    }
+    for (int64_t c = (KEEP * 256 + threadIdx.x) * 8; c < cols; c += 256 * 8) {
+        float v[8];
+        row_chunk(r, s16, c, cols, vec, v);
+        put(c, v);
     }
     if (threadIdx.x == 0) sx[m] = ldexpf(1.0f, k);
     if (grow) {
         sq = block_sum(sq, sm);
-        const uint16_t *dr = dh + m * F;
-        float md = 0.0f;
-        for (int64_t f = threadIdx.x; f < F; f += blockDim.x)
-            md = fmaxf(md, fabsf(__uint_as_float(static_cast<uint32_t>(__ldg(dr + f)) << 16)));
         md = block_max(md, sm);
         if (threadIdx.x == 0) {
             const float nx = sqrtf(sq);               // ||x / s|| = nx * 2^k
@@ -152,52 +189,47 @@ __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict_
 }
 
 // W16[o][i] = fp16((code - z) * Delta * 2^-kW): one rounding, the difference and the power of two
-// are exact.  A thread takes DQ_WORDS packed words (8 columns, one 16-byte store each), a block's
-// width apart, so every load and store of a warp is contiguous; their loads are in flight together.
-constexpr int DQ_WORDS = 4;
+// are exact.  A block takes DQ_ROWS rows, a thread the same packed word (8 columns, one 16-byte
+// store) of each: their loads are in flight together, and a warp's loads and stores are contiguous.
+constexpr int DQ_ROWS = 4;
 __global__ void __launch_bounds__(256) dequant_kernel(const uint32_t *__restrict__ q,
                                                       const uint16_t *__restrict__ scales,
-                                                      const uint32_t *__restrict__ zeros, int64_t words, int wpr,
-                                                      int lg, int nG, const unsigned *__restrict__ dmax,
+                                                      const uint32_t *__restrict__ zeros, int64_t O, int wpr, int lg,
+                                                      int nG, const unsigned *__restrict__ dmax,
                                                       uint16_t *__restrict__ out) {
     const float sw = ldexpf(1.0f, -dq_exp(dmax));
     const int nzw = (nG + 7) / 8;
-    const int64_t base = static_cast<int64_t>(blockIdx.x) * (256 * DQ_WORDS);
-    const int64_t o0 = base / wpr;                    // one 64-bit division a block
-    const int w0 = static_cast<int>(base - o0 * wpr);
-    uint32_t v[DQ_WORDS], zw[DQ_WORDS];
-    uint16_t sv[DQ_WORDS];
-    int gz[DQ_WORDS];
+    const int64_t o0 = static_cast<int64_t>(blockIdx.x) * DQ_ROWS;
+    const int rows = static_cast<int>(O - o0 < DQ_ROWS ? O - o0 : DQ_ROWS);
+    for (int w = threadIdx.x; w < wpr; w += blockDim.x) {
+        const int g = w >> (lg - 3);
+        uint32_t v[DQ_ROWS], zw[DQ_ROWS];
+        uint16_t sv[DQ_ROWS];
 #pragma unroll
-    for (int u = 0; u < DQ_WORDS; ++u) {
-        const int off = u * 256 + threadIdx.x;
-        if (base + off < words) {
-            const int w = w0 + off, dr = w / wpr, g = (w - dr * wpr) >> (lg - 3);
-            const int64_t o = o0 + dr;
-            v[u] = __ldcs(q + base + off);            // read once
+        for (int u = 0; u < DQ_ROWS; ++u) {
+            const int64_t o = o0 + (u < rows ? u : 0);
+            v[u] = __ldcs(q + o * wpr + w);           // read once
             sv[u] = __ldg(scales + o * nG + g);
             zw[u] = zeros ? __ldg(zeros + o * nzw + (g >> 3)) : 0x88888888u;
-            gz[u] = 4 * (g & 7);
         }
-    }
 #pragma unroll
-    for (int u = 0; u < DQ_WORDS; ++u) {
-        const int off = u * 256 + threadIdx.x;
-        if (base + off >= words) break;
-        const float d = __half2float(__ushort_as_half(sv[u])) * sw;
-        // nibbles (2e, 2e + 1) beside each other: 1024 + code as fp16 bits, minus (1024 + z) exactly
-        const uint32_t z = (0x6400u | ((zw[u] >> gz[u]) & 15u)) * 0x00010001u;
-        uint32_t h[4];
+        for (int u = 0; u < DQ_ROWS; ++u) {
+            if (u >= rows) break;
+            const float d = __half2float(__ushort_as_half(sv[u])) * sw;
+            // nibbles (2e, 2e + 1) beside each other: 1024 + code as fp16 bits, minus (1024 + z) exactly
+            const uint32_t z = (0x6400u | ((zw[u] >> (4 * (g & 7))) & 15u)) * 0x00010001u;
+            uint32_t h[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t b = v[u] >> (8 * e);
-            const uint32_t c = (b & 15u) | ((b << 12) & 0x000F0000u) | 0x64006400u;
-            const __half2 cz = __hsub2(*reinterpret_cast<const __half2 *>(&c), *reinterpret_cast<const __half2 *>(&z));
-            const float2 f = __half22float2(cz);
-            const __half2 hv = __floats2half2_rn(f.x * d, f.y * d);
-            h[e] = *reinterpret_cast<const uint32_t *>(&hv);
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t b = v[u] >> (8 * e);
+                const uint32_t c = (b & 15u) | ((b << 12) & 0x000F0000u) | 0x64006400u;
+                const __half2 cz = __hsub2(*reinterpret_cast<const __half2 *>(&c), *reinterpret_cast<const __half2 *>(&z));
+                const float2 f = __half22float2(cz);
+                const __half2 hv = __floats2half2_rn(f.x * d, f.y * d);
+                h[e] = *reinterpret_cast<const uint32_t *>(&hv);
+            }
+            *reinterpret_cast<uint4 *>(out + ((o0 + u) * wpr + w) * 8) = make_uint4(h[0], h[1], h[2], h[3]);
         }
-        *reinterpret_cast<uint4 *>(out + (base + off) * 8) = make_uint4(h[0], h[1], h[2], h[3]);
     }
 }
 
@@ -233,11 +265,9 @@ cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int
 
 cudaError_t launch_dequant(const uint32_t *q, const uint16_t *scales, const uint32_t *zeros, int64_t O, int64_t I,
                            int gs, const unsigned *dmax, uint16_t *out, cudaStream_t st) {
-    const int64_t words = O * (I / 8);
-    const int64_t blocks = (words + 256 * DQ_WORDS - 1) / (256 * DQ_WORDS);
-    dequant_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
-        q, scales, zeros, words, static_cast<int>(I / 8), gs == 32 ? 5 : (gs == 64 ? 6 : 7), static_cast<int>(I / gs),
-        dmax, out);
+    const int wpr = static_cast<int>(I / 8), threads = wpr < 256 ? (wpr + 31) / 32 * 32 : 256;
+    dequant_kernel<<<static_cast<unsigned>((O + DQ_ROWS - 1) / DQ_ROWS), threads, 0, st>>>(
+        q, scales, zeros, O, wpr, gs == 32 ? 5 : (gs == 64 ? 6 : 7), static_cast<int>(I / gs), dmax, out);
     return cudaGetLastError();
 }
 

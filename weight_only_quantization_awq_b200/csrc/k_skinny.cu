@@ -525,12 +525,13 @@ SkinnyPlan skinny_plan(int64_t M, int64_t tiles, int64_t k, int num_sms) {
     p.token_tiles = static_cast<int>((M + p.n - 1) / p.n);
     p.tiles = static_cast<int>(tiles);
     p.ks = static_cast<int>((k + 127) / 128);
-    // CTAs: one per SM, but no more of them to a tile than pays: a stage costs its CTA about 400 ns,
-    // the second kernel 2.5 us, each further CTA's partial sums about 60 ns of it.
+    // CTAs: one per SM, but no more of them to a tile than pays: a stage costs its CTA about 400 ns and
+    // the results of a whole tile 60 ns a token; the second kernel that shared tiles need takes
+    // 2.5 us, each CTA's partial sums about 60 ns of it.
     const int64_t units = tiles * p.ks * p.token_tiles;
     int64_t share = 1, best = INT64_MAX;
     for (int64_t c = 1; c <= p.ks && c <= 64; ++c) {
-        const int64_t cost = (p.ks + c - 1) / c * 400 + (c > 1 ? c * 60 + 2500 : 0);
+        const int64_t cost = (p.ks + c - 1) / c * 400 + (c > 1 ? c * 60 + 2500 : p.n * 60);
         if (cost < best) {
             best = cost;
             share = c;
