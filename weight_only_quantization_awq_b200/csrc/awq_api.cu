@@ -966,7 +966,7 @@ awq_status_t awq_gated_w4a16(const uint16_t *x, int64_t M, int64_t in, int64_t F
         kt_end(4, st);
         return AWQ_OK;
     }
-    if (awq::skinny_supported(M, 2 * F, in))
+    if (awq::skinny_supported(M, awq::SKINNY_MAX_M, 2 * F, in))
         return gated_skinny(nullptr, x, M, in, F, qweight, scales, zeros, s16, group_size, act, h, sms,
                             static_cast<cudaStream_t>(stream));
     return gated_dense(nullptr, x, M, in, F, qweight, scales, zeros, s16, group_size, act, h, sms,
@@ -985,7 +985,7 @@ awq_status_t awq_gated_w4a16_grad(const uint16_t *dh, const uint16_t *x, int64_t
     if (!aligned16(dh) || !aligned16(x) || !aligned16(dx)) return fail(AWQ_ERR_ALIGN, "misaligned pointer");
     int sms;
     if (awq_status_t s = device_info(&sms)) return s;
-    if (awq::skinny_supported(M, 2 * F, in))
+    if (awq::skinny_supported(M, awq::SKINNY_MAX_M_GATED_GRAD, 2 * F, in))
         return gated_skinny(dh, x, M, in, F, qweight, scales, zeros, s16, group_size, act, dx, sms,
                             static_cast<cudaStream_t>(stream));
     return gated_dense(dh, x, M, in, F, qweight, scales, zeros, s16, group_size, act, dx, sms,
@@ -1004,7 +1004,7 @@ awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, in
     if (awq_status_t s = device_info(&sms)) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t ld = round64(out);
-    if (awq::skinny_supported(M, out, in)) {
+    if (awq::skinny_supported(M, awq::SKINNY_MAX_M, out, in)) {
         const awq::SkinnyPlan p = awq::skinny_plan(M, (in + 127) / 128, out, sms);
         Workspace ws(st);
         if (awq_status_t s = ws.reserve(Workspace::up(2 * M * ld) + Workspace::up(4 * M) +
@@ -1096,28 +1096,31 @@ awq_status_t awq_cross_entropy(const uint16_t *x, int64_t M, int64_t in, const u
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     awq::GemmArgs a{};
     a.splits = 1;
-    a.M = M;
-    a.N = a.V = V;
+    const bool few = M <= awq::CE_T_MAX_M;            // the vocabulary on the rows, the tokens on the columns
+    a.V = V;
+    a.M = few ? V : M;
+    a.N = few ? M : V;
     a.x = x;
     a.w = W;
     a.inner = static_cast<int>(in);
-    a.bn = awq::gemm_tile_cols(M, V, sms);
-    a.mt = ceil_div(M, 256);
-    a.nt = ceil_div(V, a.bn);
+    a.bn = few ? static_cast<int>((M + 31) / 32 * 32) : awq::gemm_tile_cols(M, V, sms);
+    a.mt = ceil_div(a.M, 256);
+    a.nt = ceil_div(a.N, a.bn);
     a.nk[0] = static_cast<int>(in / 64);
+    const int parts = few ? 8 * a.mt : 2 * a.nt;      // partial (maximum, sum) pairs of a token
     Workspace ws(st);
-    if (awq_status_t s = ws.reserve(Workspace::up(4 * M) + Workspace::up(sizeof(float2) * M * 2 * a.nt))) return s;
+    if (awq_status_t s = ws.reserve(Workspace::up(4 * M) + Workspace::up(sizeof(float2) * M * parts))) return s;
     a.tgt = ws.take<float>(M);
-    a.part = ws.take<float2>(M * 2 * a.nt);
+    a.part = ws.take<float2>(M * parts);
     a.labels = labels;
     awq::GemmMaps maps;
-    if (awq_status_t s = map_kmajor(&maps.a, true, x, in, M, in, 128)) return s;
-    if (awq_status_t s = map_kmajor(&maps.b, true, W, in, V, in, a.bn / 2)) return s;
+    if (awq_status_t s = map_kmajor(&maps.a, true, few ? W : x, in, a.M, in, 128)) return s;
+    if (awq_status_t s = map_kmajor(&maps.b, true, few ? x : W, in, a.N, in, a.bn / 2)) return s;
     kt_reset(4);
     kt_begin(4, st);
-    AWQ_CUDA(awq::launch_gemm16(awq::EPI_CE, true, false, maps, a, sms, st));
+    AWQ_CUDA(awq::launch_gemm16(few ? awq::EPI_CE_T : awq::EPI_CE, true, false, maps, a, sms, st));
     kt_end(4, st);
-    AWQ_CUDA(awq::launch_ce_final(a.part, 2 * a.nt, M, labels, V, a.tgt, loss, lse, st));
+    AWQ_CUDA(awq::launch_ce_final(a.part, parts, few, M, labels, V, a.tgt, loss, lse, st));
     return AWQ_OK;
 }
 

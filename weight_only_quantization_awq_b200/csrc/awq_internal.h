@@ -204,7 +204,10 @@ cudaError_t launch_wait_selftest(long long limit, bool arrive, int *err, cudaStr
 // through packed weights and score a vocabulary (k_dense.cu), with their operand preparation
 // (k_dequant.cu)
 enum { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
-enum { EPI_GATED = 0, EPI_GATED_BWD = 1, EPI_OUT = 2, EPI_CE = 3, EPI_CE_BWD = 4 };
+enum { EPI_GATED = 0, EPI_GATED_BWD = 1, EPI_OUT = 2, EPI_CE = 3, EPI_CE_BWD = 4, EPI_CE_T = 5 };
+// Tokens up to which the vocabulary goes on the rows (32000 x 4096: 13 tokens 45 against 64 us, 128 tokens
+// 50 against 53: the products cost the columns, and 256 rows of tokens are mostly padding).
+constexpr int64_t CE_T_MAX_M = 128;
 struct GemmMaps {
     CUtensorMap a, b;           // K-major: box 64 k x 128 rows (b: bn / 2 rows); MN-major: box 64 x 64
 };
@@ -230,7 +233,7 @@ struct GemmArgs {
     int64_t V, v0;              // vocabulary; first entry of this piece
     const float *lse, *dloss;   // [M]
     float *tgt;                 // [M] the label's logit
-    float2 *part;               // [2 nt][M] (maximum, sum of exponentials) without the label's
+    float2 *part;               // [2 nt][M] (EPI_CE_T: [N][8 mt]) (maximum, sum of exponentials) without the label's
     const uint16_t *x, *w;      // the operands themselves, rows of `inner` columns (the labels' logits)
     // outputs
     uint16_t *out;              // bf16
@@ -244,7 +247,7 @@ int gemm_tile_cols(int64_t M, int64_t N, int num_sms);
 int64_t gemm_part_vecs(int64_t M, int64_t N, int64_t k, int num_sms, int *splits);
 cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, const GemmArgs &a, int num_sms,
                           cudaStream_t st);
-cudaError_t launch_ce_final(const float2 *part, int nt, int64_t M, const int64_t *labels, int64_t V,
+cudaError_t launch_ce_final(const float2 *part, int n, bool rows, int64_t M, const int64_t *labels, int64_t V,
                             const float *tgt, float *loss, float *lse, cudaStream_t st);
 // Token rows to fp16 with a power-of-two scale each (out [M][ld], sx [M]); dh [M][F] with grow [M]
 // optional; dmax [DMAX_PARTS] = the largest |Delta| of the parts of the layer's scales, as fp16 bits.
@@ -266,9 +269,12 @@ struct SkinnyPlan {
     int tiles, ks, grid;        // tiles of W, 128-deep stages of K, CTAs
     int64_t part_vecs;          // workspace: fp32 partial sums, by four
 };
-// above SKINNY_MAX_M tokens, or 4 GB of codes: dequantise once, dense products
-constexpr int64_t SKINNY_MAX_M = 512;
-inline bool skinny_supported(int64_t M, int64_t O, int64_t I) { return M <= SKINNY_MAX_M && O * I <= int64_t(1) << 32; }
+// Up to how many tokens, and below 4 GB of codes; above, the weights are dequantised once for dense
+// products.  Measured (us a call, this way against dense): 22016 x 4096 gated 320 tokens 118 / 124, 384
+// 129 / 125; its gradient, whose two products share the dequantised weights, 256 tokens 183 / 185, 320
+// 244 / 210; 4096 x 11008 gradient 320 tokens 75 / 77, 448 89 / 78.
+constexpr int64_t SKINNY_MAX_M = 352, SKINNY_MAX_M_GATED_GRAD = 256;
+inline bool skinny_supported(int64_t M, int64_t most, int64_t O, int64_t I) { return M <= most && O * I <= int64_t(1) << 32; }
 SkinnyPlan skinny_plan(int64_t M, int64_t tiles, int64_t k, int num_sms);
 struct SkinnyArgs {
     const uint32_t *q;

@@ -10,6 +10,7 @@
 //                  (B read along its rows: K is W's row) and the head's weight gradient;
 //   EPI_CE         logits = x W^T of one vocabulary tile: each row's maximum and sum of
 //                  exponentials over the tile, and the label's logit; the logits stay on chip;
+//   EPI_CE_T       the same for few tokens, the vocabulary on D's rows;
 //   EPI_CE_BWD     (exp(logit - lse) - [n = label]) * dloss as bf16, one piece of the vocabulary.
 //
 // CTA pairs (clusters of two, one CTA per SM, persistent over output tiles): a tile is 256 rows
@@ -332,15 +333,70 @@ __device__ __forceinline__ void epi_ce(const GemmArgs &a, uint32_t acc, int64_t 
     if (ok) a.part[static_cast<int64_t>(2 * ntile + par) * a.M + row] = make_float2(mx, sum);
 }
 
+// The same for few tokens, the vocabulary on the rows (D's row = entry, column = token): a warp
+// reduces its 32 entries of 16 tokens at a time.  Halving exchange: at each step a lane gives away half of
+// its tokens and takes the partner's part of the other half, 8 + 4 + 2 + 1 shuffles and one more
+// for 16 tokens; lane l then holds token l / 2.
+template <bool SUM>
+__device__ __forceinline__ float warp_reduce16(const float (&v)[16]) {
+    const int lane = threadIdx.x & 31;
+    auto op = [](float x, float y) { return SUM ? x + y : fmaxf(x, y); };
+    float a8[8], a4[4], a2[2];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float keep = lane & 16 ? v[8 + k] : v[k], give = lane & 16 ? v[k] : v[8 + k];
+        a8[k] = op(keep, __shfl_xor_sync(0xffffffffu, give, 16));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float keep = lane & 8 ? a8[4 + k] : a8[k], give = lane & 8 ? a8[k] : a8[4 + k];
+        a4[k] = op(keep, __shfl_xor_sync(0xffffffffu, give, 8));
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float keep = lane & 4 ? a4[2 + k] : a4[k], give = lane & 4 ? a4[k] : a4[2 + k];
+        a2[k] = op(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+    }
+    const float keep = lane & 2 ? a2[1] : a2[0], give = lane & 2 ? a2[0] : a2[1];
+    const float r = op(keep, __shfl_xor_sync(0xffffffffu, give, 2));
+    return op(r, __shfl_xor_sync(0xffffffffu, r, 1));
+}
+
+__device__ __forceinline__ void epi_ce_t(const GemmArgs &a, uint32_t acc, int64_t row, int slot, int par) {
+    const int lane = threadIdx.x & 31;
+    const bool ok = row < a.M;
+#pragma unroll 1
+    for (int c = 16 * par; c < a.bn; c += 32) {
+        uint32_t r[16];
+        tmem_ld16_wait(acc + c, r);
+        const int64_t m = c + (lane >> 1);            // the token this lane ends up with
+        const int64_t mine = m < a.N ? __ldg(a.labels + m) : -1;
+        float v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int64_t lab = __shfl_sync(0xffffffffu, mine, 2 * k);
+            v[k] = ok && lab != row ? __uint_as_float(r[k]) : -INFINITY;
+        }
+        const float mx = warp_reduce16<false>(v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float t = __shfl_sync(0xffffffffu, mx, 2 * k);
+            v[k] = exp2f((v[k] - (t == -INFINITY ? 0.0f : t)) * LOG2E);
+        }
+        const float sum = warp_reduce16<true>(v);
+        if (m < a.N && (lane & 1) == 0) a.part[m * (8 * a.mt) + slot] = make_float2(mx, sum);
+    }
+}
+
 // The labels' logits in fp32 by the two warps that have no other work, a warp per token: products of
 // bf16 values are exact, so this is the fp32 rounding of a few additions per lane.  The tensor
 // cores' accumulation truncates (2.5e-6 of the loss at 4096 columns), which shows where the
 // label dominates its row; the other terms of the sum average it out.
-__device__ __forceinline__ void ce_labels(const GemmArgs &a, int first, int step) {
+__device__ __forceinline__ void ce_labels(const GemmArgs &a, int64_t tokens, int first, int step) {
     const int lane = threadIdx.x & 31;
-    for (int64_t m = first; m < a.M; m += step) {
+    for (int64_t m = first; m < tokens; m += step) {
         const int64_t lab = __ldg(a.labels + m);
-        if (lab < 0 || lab >= a.N) continue;
+        if (lab < 0 || lab >= a.V) continue;
         const uint4 *x = reinterpret_cast<const uint4 *>(a.x + m * a.inner);
         const uint4 *w = reinterpret_cast<const uint4 *>(a.w + lab * a.inner);
         float s0 = 0.0f, s1 = 0.0f;
@@ -515,8 +571,8 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
             __syncwarp();
         }
     } else if (warp < GM_EPI_WARP0) {
-        if constexpr (EPI == EPI_CE)
-            ce_labels(a, static_cast<int>(blockIdx.x) * 2 + warp - 2, static_cast<int>(gridDim.x) * 2);
+        if constexpr (EPI == EPI_CE || EPI == EPI_CE_T)
+            ce_labels(a, EPI == EPI_CE ? a.M : a.N, static_cast<int>(blockIdx.x) * 2 + warp - 2, static_cast<int>(gridDim.x) * 2);
     } else {
         const int quad = warp & 3, par = (warp - GM_EPI_WARP0) >> 2;
         uint32_t ti = 0;
@@ -537,6 +593,8 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
                     epi_out(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par);
             }
             if constexpr (EPI == EPI_CE) epi_ce(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, tl.n, par);
+            if constexpr (EPI == EPI_CE_T)
+                epi_ce_t(a, acc, row, tl.m * 8 + static_cast<int>(rank) * 4 + quad, par);
             if constexpr (EPI == EPI_CE_BWD) epi_ce_bwd(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par);
             tc_fence_before();
             __syncwarp();
@@ -561,8 +619,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
 template <int EPI, bool BF16, bool A_MN, bool B_MN>
 cudaError_t launch_t(const GemmMaps &maps, const GemmArgs &a, int num_sms, cudaStream_t st) {
     auto *kernel = gemm16_kernel<EPI, BF16, A_MN, B_MN>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(GM_THREADS);
     cfg.dynamicSmemBytes = GM_SMEM;
@@ -581,6 +638,8 @@ cudaError_t launch_t(const GemmMaps &maps, const GemmArgs &a, int num_sms, cudaS
     if (e != cudaSuccess) return e;
     int pairs = dev >= 0 && dev < 64 ? max_pairs[dev] : 0;
     if (pairs == 0) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, GM_SMEM);
+        if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(static_cast<unsigned>(2 * (num_sms / 2)));
         e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
         if (e != cudaSuccess) return e;
@@ -639,6 +698,7 @@ cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, c
         case EPI_GATED: return launch_t<EPI_GATED, false, false, false>(maps, a, num_sms, st);
         case EPI_GATED_BWD: return launch_t<EPI_GATED_BWD, false, false, false>(maps, a, num_sms, st);
         case EPI_CE: return launch_t<EPI_CE, true, false, false>(maps, a, num_sms, st);
+        case EPI_CE_T: return launch_t<EPI_CE_T, true, false, false>(maps, a, num_sms, st);
         case EPI_CE_BWD: return launch_t<EPI_CE_BWD, true, false, false>(maps, a, num_sms, st);
         default:
             if (a_mn) return launch_t<EPI_OUT, true, true, true>(maps, a, num_sms, st);
@@ -650,50 +710,67 @@ cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, c
 // ------------------------------------------------------------------ cross entropy, last step
 namespace {
 
-// One warp per token: the half tiles' (maximum, sum) pairs to the log of the sum of exponentials, in
-// the order of the tiles for each lane and by a fixed tree across lanes.
-__global__ void __launch_bounds__(256) ce_final_kernel(const float2 *__restrict__ part, int nt, int64_t M,
+__device__ __forceinline__ void join(float &mx, float &sum, float om, float os) {
+    const float nm = fmaxf(mx, om), ref = nm == -INFINITY ? 0.0f : nm;
+    sum = sum * exp2f((mx - ref) * LOG2E) + os * exp2f((om - ref) * LOG2E);
+    mx = nm;
+}
+
+// The partial (maximum, sum) pairs of each token to the log of its sum of exponentials.  ROWS: one
+// token per block, pairs [token][n] (few tokens, many pairs); else eight tokens per block, pairs
+// [n][token], 64 contiguous bytes a pair.  Each thread takes its pairs in order, the threads meet in a
+// fixed tree.
+template <bool ROWS>
+__global__ void __launch_bounds__(256) ce_final_kernel(const float2 *__restrict__ part, int n, int64_t M,
                                                        const int64_t *__restrict__ labels, int64_t V,
                                                        const float *__restrict__ tgt, float *__restrict__ loss,
                                                        float *__restrict__ lse) {
-    const int64_t m = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (m >= M) return;
+    __shared__ float2 sm[8][8];
+    constexpr int T = ROWS ? 1 : 8;                   // tokens of the block
+    const int tok = threadIdx.x % T, at = threadIdx.x / T;
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * T + tok;
     float mx = -INFINITY, sum = 0.0f;
-    for (int t = lane; t < nt; t += 32) {
-        const float2 p = __ldg(part + static_cast<int64_t>(t) * M + m);
-        const float nm = fmaxf(mx, p.x), ref = nm == -INFINITY ? 0.0f : nm;
-        sum = sum * exp2f((mx - ref) * LOG2E) + p.y * exp2f((p.x - ref) * LOG2E);
-        mx = nm;
+    if (m < M) {
+#pragma unroll 4
+        for (int t = at; t < n; t += 256 / T) {
+            const float2 p = __ldg(ROWS ? part + m * n + t : part + static_cast<int64_t>(t) * M + m);
+            join(mx, sum, p.x, p.y);
+        }
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
+    for (int off = 16; off >= T; off >>= 1) {
         const float om = __shfl_xor_sync(0xffffffffu, mx, off), os = __shfl_xor_sync(0xffffffffu, sum, off);
-        const float nm = fmaxf(mx, om), ref = nm == -INFINITY ? 0.0f : nm;
-        sum = sum * exp2f((mx - ref) * LOG2E) + os * exp2f((om - ref) * LOG2E);
-        mx = nm;
+        join(mx, sum, om, os);
     }
-    if (lane == 0) {
-        const int64_t lab = __ldg(labels + m);
-        if (lab < 0 || lab >= V) {
-            lse[m] = mx + logf(sum);
-            loss[m] = 0.0f;
-            return;
-        }
-        // with the label's term t, which `part` leaves out: loss = log(1 + sum e^(mx - t)),
-        // written so that neither a label far above the others nor one far below loses digits
-        const float t = __ldg(tgt + m), d = mx - t;
-        const float l = d > 0.0f ? d + logf(sum + expf(-d)) : log1pf(sum * expf(d));
-        loss[m] = l;
-        lse[m] = t + l;
+    if ((threadIdx.x & 31) < T) sm[threadIdx.x >> 5][tok] = make_float2(mx, sum);
+    __syncthreads();
+    if (threadIdx.x >= T || m >= M) return;
+    mx = sm[0][tok].x;
+    sum = sm[0][tok].y;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) join(mx, sum, sm[w][tok].x, sm[w][tok].y);
+    const int64_t lab = __ldg(labels + m);
+    if (lab < 0 || lab >= V) {
+        lse[m] = mx + logf(sum);
+        loss[m] = 0.0f;
+        return;
     }
+    // with the label's term t, which `part` leaves out: loss = log(1 + sum e^(mx - t)), written so
+    // that neither a label far above the others nor one far below loses digits
+    const float t = __ldg(tgt + m), d = mx - t;
+    const float l = d > 0.0f ? d + logf(sum + expf(-d)) : log1pf(sum * expf(d));
+    loss[m] = l;
+    lse[m] = t + l;
 }
 
 }  // namespace
 
-cudaError_t launch_ce_final(const float2 *part, int nt, int64_t M, const int64_t *labels, int64_t V,
+cudaError_t launch_ce_final(const float2 *part, int n, bool rows, int64_t M, const int64_t *labels, int64_t V,
                             const float *tgt, float *loss, float *lse, cudaStream_t st) {
-    ce_final_kernel<<<static_cast<unsigned>((M + 7) / 8), 256, 0, st>>>(part, nt, M, labels, V, tgt, loss, lse);
+    if (rows)
+        ce_final_kernel<true><<<static_cast<unsigned>(M), 256, 0, st>>>(part, n, M, labels, V, tgt, loss, lse);
+    else
+        ce_final_kernel<false><<<static_cast<unsigned>((M + 7) / 8), 256, 0, st>>>(part, n, M, labels, V, tgt, loss, lse);
     return cudaGetLastError();
 }
 

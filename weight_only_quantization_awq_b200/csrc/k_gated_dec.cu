@@ -122,24 +122,19 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return r;
 }
 
-// x / s of the 8 columns of word w of one token.
-__device__ __forceinline__ void x_word(const uint16_t *xr, const uint16_t *s16, int w, float (&v)[8]) {
-    const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(xr) + w);
-    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+// 1 / s of the 8 columns of word w: products with it are within 2 ulp of fp32 of x / s, far below
+// the fp16 rounding that follows.
+__device__ __forceinline__ void inverse_s(const uint16_t *s16, int w, float (&r)[8]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        v[2 * e] = __uint_as_float(xw[e] << 16);
-        v[2 * e + 1] = __uint_as_float(xw[e] & 0xFFFF0000u);
-    }
+    for (int e = 0; e < 8; ++e) r[e] = 1.0f;
     if (s16) {
         const uint4 sv = __ldg(reinterpret_cast<const uint4 *>(s16) + w);
         const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const __half2 h = *reinterpret_cast<const __half2 *>(&sw[e]);
-            // a reciprocal and a product: 2 ulp of fp32, far below the fp16 rounding that follows
-            v[2 * e] *= rcp_approx(__low2float(h));
-            v[2 * e + 1] *= rcp_approx(__high2float(h));
+            r[2 * e] = rcp_approx(__low2float(h));
+            r[2 * e + 1] = rcp_approx(__high2float(h));
         }
     }
 }
@@ -224,71 +219,110 @@ __global__ void __launch_bounds__(GD_THREADS, 1) gated_dec_kernel(const GdArgs a
         };
 #pragma unroll
         for (int u = 0; u < GD_PF; ++u) fetch(wa[u], wb[u]);
-        // ---- scales and zero points of the pass's rows: a warp per row, a lane per group
-        for (int j = lane; j < p.groups; j += 32) {
-            const uint16_t *sj = a.scales + j;
-            const uint32_t *zj = a.zeros + (j >> 3);
-#pragma unroll 5
-            for (int r = warp; r < nt * 2 * GD_TILE; r += GD_WARPS) {
-                // row r of the pass: tile r / 32, then 8 gate rows, their 8 up rows, the next 8 of each
-                const int64_t f = static_cast<int64_t>(p0) * GD_TILE + ((r >> 4) << 3) + (r & 7);
-                const int64_t o = (r & 8 ? a.F : 0) + f;
-                float2 v = make_float2(0.0f, 0.0f);
-                if (f < a.F && j < nG) {
-                    const uint32_t z = a.zeros ? (__ldg(zj + o * nzw) >> (4 * (j & 7))) & 15u : 8u;
-                    v = make_float2(__half2float(__ushort_as_half(__ldg(sj + o * nG))), static_cast<float>(z));
+        // ---- scales and zero points of the pass's rows, a warp per row and a lane per group: asked for
+        // here, put in place after the activations, so that the two latencies overlap
+        constexpr int SR = 10;                        // rows of a warp in flight
+        uint16_t sraw[SR];
+        uint32_t zraw[SR];
+        const int srows = nt * 2 * GD_TILE;
+        auto scale_row = [&](int r) -> int64_t {      // row r of the pass: tile r / 32, then 8 gate rows, their 8 up rows, the next 8 of each
+            const int64_t f = static_cast<int64_t>(p0) * GD_TILE + ((r >> 4) << 3) + (r & 7);
+            return f < a.F ? (r & 8 ? a.F : 0) + f : -1;
+        };
+        auto ask = [&](int r0, int j) {
+#pragma unroll
+            for (int i = 0; i < SR; ++i) {
+                const int r = r0 + i * GD_WARPS;
+                sraw[i] = 0;
+                zraw[i] = 0x88888888u;
+                if (r < srows && j < nG) {
+                    const int64_t o = scale_row(r);
+                    if (o >= 0) {
+                        sraw[i] = __ldg(a.scales + o * nG + j);
+                        if (a.zeros) zraw[i] = __ldg(a.zeros + o * nzw + (j >> 3));
+                    }
                 }
-                scm[r * p.rs + j] = v;
             }
-        }
+        };
+        auto put = [&](int r0, int j) {
+#pragma unroll
+            for (int i = 0; i < SR; ++i) {
+                const int r = r0 + i * GD_WARPS;
+                if (r < srows && j < p.groups)
+                    scm[r * p.rs + j] = make_float2(__half2float(__ushort_as_half(sraw[i])),
+                                                    static_cast<float>((zraw[i] >> (4 * (j & 7))) & 15u));
+            }
+        };
+        ask(warp, lane);
 
-        // ---- activations, once: (token, word) pairs, a thread each
+        // ---- activations, once: a lane per packed word, the warps over (block of words, tokens)
         if (p0 == t0) {
             const int words = nC * 16;                // padded width, a multiple of 16
             if (threadIdx.x == 0) xsm[nC * 16 * a.M] = make_uint4(0u, 0u, 0u, 0u);
             for (int i = threadIdx.x; i < p.groups * NT * 8; i += GD_THREADS)   // the columns of no token
                 if (i % (NT * 8) >= a.M) sums[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const int tasks = a.M * words;
-#pragma unroll 2
-            for (int i0 = 0; i0 < tasks; i0 += GD_THREADS) {
-                const int i = i0 + threadIdx.x, m = i / words, w = i - m * words;
-                float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-                if (i < tasks && w < wpr) x_word(a.x + static_cast<int64_t>(m) * a.I, a.s16, w, v);
-                float mx = fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
-                                 fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
+            // one token: 32 words a warp; more: 16 words of two tokens, whose 1 / s a lane forms once
+            const int bw = a.M == 1 ? 32 : 16, tpw = a.M == 1 ? 1 : 2;
+            for (int w0 = warp * bw; w0 < words; w0 += GD_WARPS * bw) {
+                const int w = w0 + (lane & (bw - 1));
+                const bool inside = w < wpr;
+                float rs[8];
+                inverse_s(a.s16, inside ? w : 0, rs);
+                int tt, jj;
+                word_place<GS>(w & 15, tt, jj);
+                uint4 *xd = xsm + (((w >> 4) * 4 + jj) * a.M) * 4 + tt;
+#pragma unroll 4
+                for (int mb = 0; mb < a.M; mb += tpw) {
+                    const int m = mb + (tpw == 2 ? lane >> 4 : 0);
+                    const bool real = inside && m < a.M;
+                    const uint4 xv = real ? __ldg(reinterpret_cast<const uint4 *>(a.x + static_cast<int64_t>(m) * a.I) + w)
+                                          : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+                    float v[8];
 #pragma unroll
-                for (int off = GS / 16; off > 0; off >>= 1)   // a group's words are GS / 8 neighbouring lanes
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const int k = pow2_above(mx);
-                const float sc = __int_as_float((127 - k) << 23);
-                uint32_t h[4];
-                float even = 0.0f, odd = 0.0f;
+                    for (int e = 0; e < 4; ++e) {
+                        v[2 * e] = __uint_as_float(xw[e] << 16) * rs[2 * e];
+                        v[2 * e + 1] = __uint_as_float(xw[e] & 0xFFFF0000u) * rs[2 * e + 1];
+                    }
+                    float mx = fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
+                                     fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    __half2 hv = __floats2half2_rn(v[e] * sc, v[e + 4] * sc);
-                    if (e & 1) hv = __hmul2(hv, __floats2half2_rn(0.0625f, 0.0625f));
-                    h[e] = *reinterpret_cast<const uint32_t *>(&hv);
-                    const float2 f = __half22float2(hv);
-                    (e & 1 ? odd : even) += f.x + f.y;
-                }
-                float t1s = even + odd, t2s = fmaf(16.0f, odd, even);
+                    for (int off = GS / 16; off > 0; off >>= 1)   // a group's words are GS / 8 neighbouring lanes
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    const int k = pow2_above(mx);
+                    const float sc = __int_as_float((127 - k) << 23);
+                    uint32_t h[4];
+                    float even = 0.0f, odd = 0.0f;
 #pragma unroll
-                for (int off = GS / 16; off > 0; off >>= 1) {
-                    t1s += __shfl_xor_sync(0xffffffffu, t1s, off);
-                    t2s += __shfl_xor_sync(0xffffffffu, t2s, off);
-                }
-                if (i < tasks) {
-                    int tt, jj;
-                    word_place<GS>(w & 15, tt, jj);
-                    xsm[(((w >> 4) * 4 + jj) * a.M + m) * 4 + tt] = make_uint4(h[0], h[1], h[2], h[3]);
-                    if ((w & (GS / 8 - 1)) == 0)
-                        sums[(w / (GS / 8)) * (NT * 8) + m] =
-                            make_float4(1024.0f * t1s, t2s, __int_as_float((127 + k) << 23), 0.0f);
+                    for (int e = 0; e < 4; ++e) {
+                        __half2 hv = __floats2half2_rn(v[e] * sc, v[e + 4] * sc);
+                        if (e & 1) hv = __hmul2(hv, __floats2half2_rn(0.0625f, 0.0625f));
+                        h[e] = *reinterpret_cast<const uint32_t *>(&hv);
+                        const float2 f = __half22float2(hv);
+                        (e & 1 ? odd : even) += f.x + f.y;
+                    }
+                    float t1s = even + odd, t2s = fmaf(16.0f, odd, even);
+#pragma unroll
+                    for (int off = GS / 16; off > 0; off >>= 1) {
+                        t1s += __shfl_xor_sync(0xffffffffu, t1s, off);
+                        t2s += __shfl_xor_sync(0xffffffffu, t2s, off);
+                    }
+                    if (w < words && m < a.M) {
+                        xd[m * 4] = make_uint4(h[0], h[1], h[2], h[3]);
+                        if ((w & (GS / 8 - 1)) == 0)
+                            sums[(w / (GS / 8)) * (NT * 8) + m] =
+                                make_float4(1024.0f * t1s, t2s, __int_as_float((127 + k) << 23), 0.0f);
+                    }
                 }
             }
             if (threadIdx.x < 2 && part > GD_EARLY) l2_prefetch_range(mine + GD_EARLY, part - GD_EARLY);
         }
-
+        put(warp, lane);
+        for (int j = lane; j < p.groups; j += 32)     // what one round did not cover
+            for (int r = warp + (j == lane ? SR * GD_WARPS : 0); r < srows; r += SR * GD_WARPS) {
+                ask(r, j);
+                put(r, j);
+            }
         __syncthreads();
 
         // ---- this warp's steps
