@@ -35,7 +35,7 @@ namespace {
 
 constexpr int GD_WARPS = 16;
 constexpr int GD_THREADS = GD_WARPS * 32;
-constexpr int GD_PF = 2;                              // steps of weights in flight per warp
+constexpr int GD_PF = 1;                              // steps of weights in flight per warp (two: registers spill, 4% slower)
 constexpr int GD_TILE = 16;                           // columns of h per tile
 constexpr int GD_MAX_TILES = 32;                      // tiles of one pass of a CTA
 constexpr uint32_t GD_EARLY = 65536;                  // bytes of gate and of up rows asked for first

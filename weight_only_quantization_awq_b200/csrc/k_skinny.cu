@@ -14,7 +14,7 @@
 // written and read per 128 x 128 weights, about 260 cycles, and the tokens' tile) above.
 //
 // Roles: 24 warps dequantise, in three groups that take the stages in turn, so that one group computes
-// while another stores (a thread: 64 columns of one row, two 16-byte loads of codes fetched SK_PF
+// while another stores (a thread: 32 columns of two rows, two 16-byte loads of codes fetched SK_PF
 // of its stages ahead into registers; shift, LOP3, exact HSUB2 or HFMA2 to code - z, HMUL2 by
 // Delta 2^-kW, eight 16-byte stores); one warp fetches the token tiles by TMA, one
 // issues the MMAs, four write the results from TMEM, whose two accumulators let a tile's
@@ -227,42 +227,45 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
     constexpr uint32_t tmem_base = 0;
 
     if (warp < SK_DQ_WARPS) {
-        // ---- dequantise: group `grp` of eight warps takes every SK_GROUPS-th unit; thread = row r of the
-        // stage, columns 32 h .. + 31 of both of its 64-column blocks
-        const int grp = warp >> 3, r = (threadIdx.x & 255) >> 1, hf = threadIdx.x & 1;
+        // ---- dequantise: group `grp` of eight warps takes every SK_GROUPS-th unit; thread = 32 columns
+        // 32 q4 .. + 31 of rows r and r + 64 of the stage.  The four lanes of a row read its 64 bytes of
+        // codes in one instruction: with a lane per half row and block instead, twice as many cache
+        // lines an instruction made the L1 pipe the limit (77% busy).
+        const int grp = warp >> 3, r = (threadIdx.x & 255) >> 2, q4 = threadIdx.x & 3;
         const int wpr = static_cast<int>(a.I / 8), nG = static_cast<int>(a.I >> a.lg), nzw = (nG + 7) / 8;
         // Raw loads of the units to come: nothing touches a value before its unit, so nothing waits
         // for it earlier.  Addresses are 32-bit offsets from the three base pointers (the packed
         // matrix is below 4 GB); a row or column past the end reads the first word instead and gets
         // a scale of zero.
         struct Raw {
-            uint4 q[2];                               // codes of the two blocks
+            uint4 q[2];                               // codes of the two rows
             uint16_t s[2];
             uint32_t z[2];
-            int g;                                    // group of block 0's columns; bits 29, 30: block 0, 1 is real
+            int g;                                    // the columns' group; bits 29, 30: row r, r + 64 is real
         } raw[SK_PF];
         int pt = (u0 + grp) / a.ks % a.tiles, pk = (u0 + grp) % a.ks;   // tile and K stage of the next load
-        uint32_t qo = 0, so = 0, zo = 0;              // codes: words; scales: elements; zero words
-        int g = 0, rem0 = 0, rem1 = 0;                // group of block 0; K positions left from its first, and block 1's (<= 0: none)
+        uint32_t qo = 0, so = 0, zo = 0;              // of row r; codes: words; scales: elements; zero words
+        int g = 0, rem0 = 0, rem1 = 0;                // group; K positions left from row r's, row r + 64's first (<= 0: none)
         constexpr uint32_t GK = 128 * SK_GROUPS;      // K positions from a group's unit to its next
         const uint32_t qstep = GRAD ? GK * static_cast<uint32_t>(wpr) : GK / 8;
         const uint32_t sstep = GRAD ? GK * static_cast<uint32_t>(nG) : GK >> a.lg;
         const uint32_t zstep = GRAD ? GK * static_cast<uint32_t>(nzw) : 0u;
         const int gstep = GRAD ? 0 : static_cast<int>(GK >> a.lg);
-        const int blk = a.lg == 7 ? 0 : 64 >> a.lg;   // groups from block 0's columns to block 1's
+        // from row r to row r + 64 of the stage: gate row to up row, or 64 rows of K
+        const uint32_t drow = GRAD ? 64u : static_cast<uint32_t>(a.F);
+        const uint32_t dq = drow * static_cast<uint32_t>(wpr), ds = drow * static_cast<uint32_t>(nG),
+                       dz = drow * static_cast<uint32_t>(nzw);
         auto place = [&]() {
             int o, col;
             if (GRAD) {
                 o = pk * 128 + r;
-                col = pt * 128 + hf * 32;
-                rem0 = col < static_cast<int>(a.I) ? static_cast<int>(a.O) - o : 0;
-                rem1 = col + 64 < static_cast<int>(a.I) ? rem0 : -(1 << 30);
-            } else {                                  // 64 gate rows, then their up rows
-                const int f = pt * 64 + (r & 63);
-                o = (r >> 6) * static_cast<int>(a.F) + f;
-                col = pk * 128 + hf * 32;
-                rem0 = f < static_cast<int>(a.F) ? static_cast<int>(a.I) - col : 0;
+                col = pt * 128 + q4 * 32;
+                rem0 = col < static_cast<int>(a.I) ? static_cast<int>(a.O) - o : -(1 << 30);
                 rem1 = rem0 - 64;
+            } else {                                  // 64 gate rows, then their up rows
+                o = pt * 64 + r;
+                col = pk * 128 + q4 * 32;
+                rem0 = rem1 = o < static_cast<int>(a.F) ? static_cast<int>(a.I) - col : -(1 << 30);
             }
             g = col >> a.lg;
             qo = static_cast<uint32_t>(o) * static_cast<uint32_t>(wpr) + (static_cast<uint32_t>(col) >> 3);
@@ -273,12 +276,13 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
             const bool r0 = rem0 > 0, r1 = rem1 > 0;
             w.g = g | (r0 ? 1 << 29 : 0) | (r1 ? 1 << 30 : 0);
             w.q[0] = __ldcs(reinterpret_cast<const uint4 *>(a.q + (r0 ? qo : 0u)));
-            w.q[1] = __ldcs(reinterpret_cast<const uint4 *>(a.q + (r1 ? qo + 8u : 0u)));
+            w.q[1] = __ldcs(reinterpret_cast<const uint4 *>(a.q + (r1 ? qo + dq : 0u)));
             w.s[0] = __ldg(a.scales + (r0 ? so : 0u));
-            if (blk) w.s[1] = __ldg(a.scales + (r1 ? so + blk : 0u));
+            w.s[1] = __ldg(a.scales + (r1 ? so + ds : 0u));
             if (a.zeros) {
-                w.z[0] = __ldg(a.zeros + (r0 ? zo + (static_cast<uint32_t>(g) >> 3) : 0u));
-                if (blk) w.z[1] = __ldg(a.zeros + (r1 ? zo + (static_cast<uint32_t>(g + blk) >> 3) : 0u));
+                const uint32_t zw = zo + (static_cast<uint32_t>(g) >> 3);
+                w.z[0] = __ldg(a.zeros + (r0 ? zw : 0u));
+                w.z[1] = __ldg(a.zeros + (r1 ? zw + dz : 0u));
             }
             pk += SK_GROUPS;
             if (pk < a.ks) {
@@ -304,8 +308,12 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
         griddep_wait();
         const float dscale = ldexpf(1.0f, -dq_exp(a.dmax));
         const uint32_t P = 0x64006400u;
-        const uint32_t row_off = static_cast<uint32_t>(r * 128);
-        const uint32_t sx0 = static_cast<uint32_t>((hf * 4) ^ (r & 7));          // column 0 of this half, swizzled
+        // block of columns, row, and the first of this quarter's four 16-byte columns, swizzled.  The upper
+        // block's lanes store their words in the order 2, 3, 0, 1, so that the eight lanes of a store
+        // phase (two rows, four quarters) fall into eight 16-byte columns.
+        const bool rot = q4 >= 2;
+        const uint32_t row_off = static_cast<uint32_t>((q4 >> 1) * 16384 + r * 128);
+        const uint32_t sx0 = static_cast<uint32_t>(((q4 & 1) * 4) ^ (r & 7) ^ (rot ? 2 : 0));
         // Unit n of the CTA sits in ring stage n % stages, in the phase of its n / stages-th use.  A
         // parity tells neighbouring phases apart only: unit n waits for unit n - stages, and unit n - 2
         // stages must be done by then, which the group's last unit, n - SK_GROUPS, has waited for
@@ -318,16 +326,15 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
                 if (ub + SK_GROUPS * u >= u1) break;
                 uint4 v[4];
                 auto dequant = [&](int b) {
-                    const int gb = raw[u].g + (b ? blk : 0);
                     uint32_t z = 8u;
-                    if (a.zeros) z = ((b && blk ? raw[u].z[1] : raw[u].z[0]) >> (4 * (gb & 7))) & 15u;
-                    const float df = raw[u].g & (1 << (29 + b))
-                                         ? __half2float(__ushort_as_half(b && blk ? raw[u].s[1] : raw[u].s[0])) * dscale : 0.0f;
+                    if (a.zeros) z = (raw[u].z[b] >> (4 * (raw[u].g & 7))) & 15u;
+                    const float df = raw[u].g & (1 << (29 + b)) ? __half2float(__ushort_as_half(raw[u].s[b])) * dscale : 0.0f;
                     const __half2 dh2 = __floats2half2_rn(df, df);
                     const uint32_t d = *reinterpret_cast<const uint32_t *>(&dh2);
                     const uint32_t z0 = (0x6400u | z) * 0x00010001u;             // 1024 + z
                     const uint32_t z1 = sk_sub(0x63806380u, z0);                 // 960 - (1024 + z) = -(64 + z)
-                    const uint32_t w[4] = {raw[u].q[b].x, raw[u].q[b].y, raw[u].q[b].z, raw[u].q[b].w};
+                    const uint4 qv = raw[u].q[b];
+                    const uint32_t w[4] = {rot ? qv.z : qv.x, rot ? qv.w : qv.y, rot ? qv.x : qv.z, rot ? qv.y : qv.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t w8 = w[j] >> 8;
@@ -341,13 +348,12 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
                 dequant(0);
                 ok = mbar_wait_warp(&empty[st], ph, abort_flag);
                 if (!ok) break;
-                // the eight lanes of a store phase (four rows, two halves) fall into eight 16-byte columns
                 uint8_t *dst = ring + st * stage + row_off;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(dst + ((sx0 ^ j) << 4)) = v[j];
                 dequant(1);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(dst + 16384 + ((sx0 ^ j) << 4)) = v[j];
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(dst + 64 * 128 + ((sx0 ^ j) << 4)) = v[j];
                 fetch(raw[u]);
                 fence_proxy_async_smem();
                 __syncwarp();
