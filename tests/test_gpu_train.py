@@ -240,3 +240,264 @@ def test_cross_entropy_grad(awq, M, V, I, want_dw):
         dW_r = d.T @ x8
         e = ed.T @ x8.abs() + acc(M) * (d.abs().T @ x8.abs())
         within(dW, dW_r, e + UBF * (dW_r.abs() + e) + 1e-38, "dW")
+
+
+# ------------------------------------------------------------------ what the formulas leave open
+def ffn(seed, M=40, I=256, F=320, gs=64):
+    w, D, s = packed(2 * F, I, gs, True, True, seed)
+    return w, D, s, rand(M, I, seed + 1), rand(M, F, seed + 2, 1e-3)
+
+
+def every_call(awq, M, seed=7):
+    """One call of each operator on its own inputs, as functions that return their outputs."""
+    w, D, s, x, dh = ffn(seed, M=M)
+    wl, _, _ = packed(192, 256, 64, False, True, seed + 3)
+    dy = rand(M, 192, seed + 4, 1e-4)
+    xc, W, labels = ce_case(M, 5003, 128, seed + 5)
+    _, lse = awq.awq_cross_entropy(xc, W, labels)
+    dloss = torch.full((M,), 1.0 / M, device="cuda")
+    return {
+        "gated": lambda: (awq.awq_gated_w4a16(x, *w, group_size=64),),
+        "gated_grad": lambda: (awq.awq_gated_w4a16_grad(dh, x, *w, group_size=64),),
+        "linear_grad": lambda: (awq.awq_linear_w4a16_grad(dy, *wl, group_size=64),),
+        "ce": lambda: awq.awq_cross_entropy(xc, W, labels),
+        "ce_grad": lambda: awq.awq_cross_entropy_grad(xc, W, labels, lse, dloss),
+    }
+
+
+# tokens of every path: decode, dequantised on the way (one and several token tiles), dense
+PATHS = [1, 11, 40, 200, 400]
+
+
+@pytest.mark.parametrize("M", PATHS)
+def test_same_bits_again_and_on_another_stream(awq, M):
+    for name, call in every_call(awq, M).items():
+        first = [t.clone() for t in call()]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            other = call()
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b, c in zip(first, call(), other):
+            assert torch.equal(a, b) and torch.equal(a, c), name
+
+
+@pytest.mark.parametrize("M", PATHS)
+def test_captured_and_replayed(awq, M):
+    calls = every_call(awq, M)
+    want = {n: [t.clone() for t in c()] for n, c in calls.items()}
+    torch.cuda.synchronize()
+    graphs = {}
+    for n, c in calls.items():                       # two graphs of each call, replayed in turn
+        pair = []
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                outs = c()
+            pair.append((g, outs))
+        graphs[n] = pair
+    for _ in range(2):
+        for n, pair in graphs.items():
+            for g, outs in pair:
+                for t in outs:
+                    t.fill_(float("nan"))
+                g.replay()
+    torch.cuda.synchronize()
+    for n, pair in graphs.items():
+        for _, outs in pair:
+            for a, b in zip(want[n], outs):
+                assert torch.equal(a, b), n
+
+
+def test_calls_on_two_streams_at_once(awq):
+    a, b = every_call(awq, 40, seed=7), every_call(awq, 40, seed=50)
+    want = {n: ([t.clone() for t in a[n]()], [t.clone() for t in b[n]()]) for n in a}
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for n in a:
+            with torch.cuda.stream(s1):
+                x = a[n]()
+            with torch.cuda.stream(s2):
+                y = b[n]()
+            got.append((n, x, y))
+    torch.cuda.synchronize()
+    for n, x, y in got:
+        for t, w in zip(x, want[n][0]):
+            assert torch.equal(t, w), n
+        for t, w in zip(y, want[n][1]):
+            assert torch.equal(t, w), n
+
+
+@pytest.mark.parametrize("M", PATHS[1:])
+def test_a_bad_token_stays_alone(awq, M):
+    """NaN and infinities of one token reach that token's results only."""
+    w, _, _, x, dh = ffn(9, M=M)
+    good_h = awq.awq_gated_w4a16(x, *w, group_size=64)
+    good_dx = awq.awq_gated_w4a16_grad(dh, x, *w, group_size=64)
+    bad = x.clone()
+    bad[1, 3], bad[1, 200] = float("nan"), float("inf")
+    bad[M - 1] = float("-inf")
+    h = awq.awq_gated_w4a16(bad, *w, group_size=64)
+    dx = awq.awq_gated_w4a16_grad(dh, bad, *w, group_size=64)
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[1] = keep[M - 1] = False
+    assert torch.equal(h[keep], good_h[keep]) and torch.equal(dx[keep], good_dx[keep])
+    assert not torch.isfinite(h[1].float()).all()
+    wl, _, _ = packed(192, 256, 64, False, True, 12)
+    dy = rand(M, 192, 13, 1e-4)
+    good = awq.awq_linear_w4a16_grad(dy, *wl, group_size=64)
+    dy[1, 5] = float("nan")
+    got = awq.awq_linear_w4a16_grad(dy, *wl, group_size=64)
+    keep[M - 1] = True
+    assert torch.equal(got[keep], good[keep]) and torch.isnan(got[1].float()).any()
+
+
+@pytest.mark.parametrize("M", [5, 64, 300])
+def test_unscored_tokens_may_hold_anything(awq, M):
+    x, W, labels = ce_case(M, 1000, 192, 21)
+    labels[:] = torch.arange(M, device="cuda")
+    labels[1], labels[2], labels[3], labels[4] = -100, 1000, -(2 ** 62), 2 ** 62
+    off = [1, 2, 3, 4]
+    _, lse = awq.awq_cross_entropy(x, W, labels)
+    dloss = torch.full((M,), 0.25, device="cuda")
+    want = awq.awq_cross_entropy_grad(x, W, labels, lse, dloss)
+    bad, bad_d = x.clone(), dloss.clone()
+    bad[1], bad[2], bad[3] = float("nan"), float("inf"), 3e38
+    bad_d[1], bad_d[4] = float("nan"), float("inf")
+    loss, bad_lse = awq.awq_cross_entropy(bad, W, labels)
+    assert (loss[off] == 0).all() and torch.isfinite(loss).all()
+    got = awq.awq_cross_entropy_grad(bad, W, labels, bad_lse, bad_d)
+    assert (got[0][off] == 0).all()
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[off] = False
+    assert torch.equal(got[0][keep], want[0][keep]) and torch.equal(got[1], want[1])
+
+
+def test_all_tokens_unscored(awq):
+    x, W, labels = ce_case(33, 1000, 128, 22)
+    labels[:] = -100
+    loss, lse = awq.awq_cross_entropy(x, W, labels)
+    dx, dW = awq.awq_cross_entropy_grad(x, W, labels, lse, torch.ones(33, device="cuda"))
+    assert (loss == 0).all() and (dx == 0).all() and (dW == 0).all() and torch.isfinite(lse).all()
+
+
+def test_certain_and_hopeless_labels(awq):
+    """A label far above its rivals keeps the digits of its small loss, one far below keeps its large one,
+    and a token with the same label as another adds to the same row of dW."""
+    I, V = 128, 300
+    W = torch.zeros(V, I, device="cuda", dtype=torch.bfloat16)
+    W[7, 0] = 1.0
+    x = torch.zeros(4, I, device="cuda", dtype=torch.bfloat16)
+    x[0, 0], x[1, 0], x[2, 0], x[3, 0] = 20.0, -20.0, 200.0, -200.0
+    labels = torch.full((4,), 7, device="cuda")
+    loss, lse = awq.awq_cross_entropy(x, W, labels)
+    l = x.to(F8) @ W.to(F8).T
+    want = torch.logsumexp(l, 1) - l[:, 7]
+    want[0] = math.log1p((V - 1) * math.exp(-20.0))
+    want[2] = math.log1p((V - 1) * math.exp(-200.0))   # 0 in fp32
+    # exp and log1p to a few units of fp32; 2 ulp of ex2 and its argument
+    assert ((loss.to(F8) - want).abs() <= 2.0 ** -20 * want + 1e-38).all()
+    dx, dW = awq.awq_cross_entropy_grad(x, W, labels, lse, torch.ones(4, device="cuda"))
+    # row 7 of dW: sum over tokens of (p - 1) x, p = 2^-...: tokens 1 and 3 dominate
+    p = torch.exp(l - torch.logsumexp(l, 1, keepdim=True))[:, 7] - 1
+    ref = (p[:, None] * x.to(F8)).sum(0)
+    assert abs(float(dW[7, 0]) - float(ref[0])) <= 2 * UBF * float((p.abs() * x[:, 0].to(F8).abs()).sum())
+
+
+@pytest.mark.parametrize("M", PATHS)
+@pytest.mark.parametrize("wscale,xscale,dscale", [(2.0 ** -12, 2.0 ** -40, 2.0 ** -60), (8.0, 2.0 ** 20, 2.0 ** 30),
+                                                  (0.01, 2.0 ** -100, 1.0)])
+def test_extreme_magnitudes(awq, M, wscale, xscale, dscale):
+    """Powers of two far from 1 in weights, activations and gradients: nothing overflows or is flushed on
+    the way (linear in each factor where the activation is linear: GELU of a large or tiny gate)."""
+    O, I = 160, 256
+    w, D, s = packed(O, I, 128, True, True, 33, scale=wscale)
+    dy = (rand(M, O, 34).float() * dscale).to(torch.bfloat16)
+    ref, tol = dx_ref(dy.to(F8), torch.zeros_like(dy, dtype=F8), D, s, O)
+    within(awq.awq_linear_w4a16_grad(dy, *w), ref, tol, "dx")
+    x = (rand(M, I, 35).float() * xscale).to(torch.bfloat16)
+    ref, tol, _ = gated_ref(x, D, s, "silu")
+    inside = ref.abs() < 1e37
+    h = awq.awq_gated_w4a16(x, *w).to(F8)
+    tol = tol + 2.0 ** -133                          # bf16 subnormals
+    assert ((h - ref).abs()[inside] <= tol[inside]).all()
+
+
+@pytest.mark.parametrize("M,rows", [(1, 8), (11, 16), (40, 64), (400, 512)])
+def test_memory_behind_the_results_is_left_alone(awq, M, rows):
+    w, _, _, x, dh = ffn(41, M=M)
+    for call, cols in ((lambda out: awq.awq_gated_w4a16(x, *w, group_size=64, out=out), 320),
+                       (lambda out: awq.awq_gated_w4a16_grad(dh, x, *w, group_size=64, out=out), 256)):
+        buf = torch.full((rows, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+        call(buf[:M])
+        assert (buf[M:] == 7.0).all() and not (buf[:M] == 7.0).all()
+
+
+def test_gradients_against_differences(awq):
+    """<dx, v> against central differences of the 64-bit forward along v."""
+    M, I, F = 6, 128, 96
+    for act in ("silu", "gelu", "gelu_tanh"):
+        w, D, s = packed(2 * F, I, 64, True, True, 61)
+        x, dh = rand(M, I, 62), rand(M, F, 63)
+        dx = awq.awq_gated_w4a16_grad(dh, x, *w, group_size=64, act=act).to(F8)
+        v = rand(M, I, 64).to(F8)
+
+        def f(t):
+            gu = ((x.to(F8) + t * v) / s) @ D.T
+            return (act64(gu[:, :F], act)[0] * gu[:, F:] * dh.to(F8)).sum()
+        e = 1e-6
+        num = float((f(e) - f(-e)) / (2 * e))
+        # elementwise bound of test_gated_grad, summed over |v| in the root-mean-square sense
+        assert abs(float((dx * v).sum()) - num) <= 2.0 ** -7 * float(((dx * v) ** 2).sum().sqrt()) * 4
+    x, W, labels = ce_case(6, 257, 64, 65)
+    loss, lse = awq.awq_cross_entropy(x, W, labels)
+    dloss = torch.ones(6, device="cuda")
+    dx, dW = awq.awq_cross_entropy_grad(x, W, labels, lse, dloss)
+    scored = labels >= 0
+
+    def g(xx, WW):
+        l = xx @ WW.T
+        return (torch.logsumexp(l, 1) - l.gather(1, labels.clamp(min=0)[:, None])[:, 0])[scored].sum()
+    e = 1e-6
+    vx, vW = rand(6, 64, 66).to(F8), rand(257, 64, 67).to(F8)
+    num = float((g(x.to(F8) + e * vx, W.to(F8)) - g(x.to(F8) - e * vx, W.to(F8))) / (2 * e))
+    assert abs(float((dx.to(F8) * vx).sum()) - num) <= 2.0 ** -7 * float(((dx.to(F8) * vx) ** 2).sum().sqrt()) * 4
+    num = float((g(x.to(F8), W.to(F8) + e * vW) - g(x.to(F8), W.to(F8) - e * vW)) / (2 * e))
+    assert abs(float((dW.to(F8) * vW).sum()) - num) <= 2.0 ** -7 * float(((dW.to(F8) * vW) ** 2).sum().sqrt()) * 4
+
+
+@pytest.mark.parametrize("M", [3, 60, 300])
+def test_block_and_head_together(awq, M):
+    """x -> gated -> down projection -> head -> loss and all the way back through packed layers, against
+    64-bit autograd on the weights that the packed storage stands for."""
+    I, F, V = 256, 448, 1500
+    w, D, s = packed(2 * F, I, 128, True, True, 71)
+    wd, Dd, sd = packed(I, F, 64, False, True, 72)
+    x = rand(M, I, 73)
+    _, W, labels = ce_case(M, V, I, 74)
+    h = awq.awq_gated_w4a16(x, *w)
+    y = awq.awq_linear_w4a16(h, *wd, group_size=64)
+    y = (y.float() / y.float().norm(dim=1, keepdim=True) * 16).to(torch.bfloat16)
+    loss, lse = awq.awq_cross_entropy(y, W, labels)
+    n = int((labels >= 0).sum())
+    dy, _ = awq.awq_cross_entropy_grad(y, W, labels, lse, torch.full((M,), 1.0 / max(n, 1), device="cuda"), want_dw=False)
+    dh = awq.awq_linear_w4a16_grad(dy, *wd, group_size=64)
+    dx = awq.awq_gated_w4a16_grad(dh, x, *w)
+    # 64 bits, the rounded activations between the calls taken as they are
+    y8 = y.to(F8).requires_grad_(True)
+    lg = y8 @ W.to(F8).T
+    scored = labels >= 0
+    ref = (torch.logsumexp(lg, 1) - lg.gather(1, labels.clamp(min=0)[:, None])[:, 0])[scored].sum() / max(n, 1)
+    assert abs(float(loss.sum()) / max(n, 1) - float(ref.detach())) <= 1e-5 * abs(float(ref.detach())) + 1e-6
+    dy8 = torch.autograd.grad(ref, y8)[0]
+    dh8 = (dy8 @ Dd) / sd
+    x8 = x.to(F8).requires_grad_(True)
+    gu = (x8 / s) @ D.T
+    hh = torch.nn.functional.silu(gu[:, :F]) * gu[:, F:]
+    dx8 = torch.autograd.grad((hh * dh8).sum(), x8)[0]
+    for got, want in ((dy, dy8), (dh, dh8), (dx, dx8)):
+        # three calls in a row, each rounding its result to bf16 (2^-8) and its operands to fp16 or bf16:
+        # relative error in the 2-norm below 2^-8 a call and operand
+        assert float((got.to(F8) - want).norm()) <= 6 * UBF * float(want.norm())

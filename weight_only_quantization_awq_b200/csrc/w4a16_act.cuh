@@ -43,7 +43,8 @@ __device__ __forceinline__ int dgu_exp(int grow, int inner, int kw) {
     return k < -125 ? -125 : (k > 125 ? 125 : k);
 }
 
-__device__ __forceinline__ float act_sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
+// (2 ulp; exp(-g) = inf below about -88 gives 0)
+__device__ __forceinline__ float act_sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
 // act(g) and its derivative:
 //   SiLU        g sig(g);                 sig (1 + g (1 - sig))
