@@ -825,8 +825,8 @@ static awq_status_t gated_dense(const uint16_t *dh, const uint16_t *x, int64_t M
     const int64_t O = 2 * F, Fp = round64(F);
     Workspace ws(st);
     size_t bytes = Workspace::up(2 * M * in) + Workspace::up(4 * M) + Workspace::up(4 * awq::DMAX_PARTS) + Workspace::up(2 * O * in);
-    int splits = 1;
-    const int64_t parts = dh ? awq::gemm_part_vecs(M, in, 2 * Fp, sms, &splits) : 0;
+    const awq::GemmPlan gp = dh ? awq::gemm_plan(M, in, 2 * Fp, sms) : awq::GemmPlan{};
+    const int64_t parts = gp.part_vecs;
     if (dh) bytes += Workspace::up(4 * M) + Workspace::up(2 * M * 2 * Fp) + Workspace::up(16 * parts);
     if (awq_status_t s = ws.reserve(bytes)) return s;
     uint16_t *xs = ws.take<uint16_t>(M * in);
@@ -867,11 +867,11 @@ static awq_status_t gated_dense(const uint16_t *dh, const uint16_t *x, int64_t M
     if (!dh) return AWQ_OK;
     // dx = ([dg | du] W) / s: K runs over the gate rows of W, then its up rows
     awq::GemmArgs b{};
-    b.splits = splits;
+    b.splits = gp.splits;
     b.part4 = part4;
     b.M = M;
     b.N = in;
-    b.bn = awq::gemm_tile_cols(M, in, sms);
+    b.bn = gp.bn;
     b.mt = ceil_div(M, 256);
     b.nt = ceil_div(in, b.bn);
     b.nk[0] = b.nk[1] = static_cast<int>(Fp / 64);
@@ -1037,8 +1037,8 @@ awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, in
         return AWQ_OK;
     }
     Workspace ws(st);
-    int splits;
-    const int64_t parts = awq::gemm_part_vecs(M, in, out, sms, &splits);
+    const awq::GemmPlan gp = awq::gemm_plan(M, in, out, sms);
+    const int64_t parts = gp.part_vecs;
     if (awq_status_t s = ws.reserve(Workspace::up(2 * M * ld) + Workspace::up(4 * M) + Workspace::up(4 * awq::DMAX_PARTS) +
                                     Workspace::up(2 * out * in) + Workspace::up(16 * parts)))
         return s;
@@ -1050,11 +1050,11 @@ awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, in
                                 nullptr, dmax, st));
     AWQ_CUDA(awq::launch_dequant(qweight, scales, zeros, out, in, group_size, dmax, w16, st));
     awq::GemmArgs b{};
-    b.splits = splits;
+    b.splits = gp.splits;
     b.part4 = parts ? ws.take<float4>(parts) : nullptr;
     b.M = M;
     b.N = in;
-    b.bn = awq::gemm_tile_cols(M, in, sms);
+    b.bn = gp.bn;
     b.mt = ceil_div(M, 256);
     b.nt = ceil_div(in, b.bn);
     b.nk[0] = ceil_div(out, 64);
@@ -1148,8 +1148,9 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
     size_t bytes = Workspace::up(2 * M * ldd);
     if (pieces > 1) bytes += Workspace::up(4 * M * in);
     if (dW) bytes += Workspace::up(2 * M * in);
-    int splits;                                       // of dx's K, the piece's entries
-    const int64_t parts = awq::gemm_part_vecs(M, in, vc < V ? vc : V, sms, &splits);
+    const awq::GemmPlan gp = awq::gemm_plan(M, in, vc < V ? vc : V, sms);   // dx: K is the piece's entries
+    const int64_t parts = gp.part_vecs;
+    const bool few = M <= awq::CE_BWD_T_MAX_M;            // the vocabulary on the rows, the tokens on the columns
     bytes += Workspace::up(16 * parts);
     if (awq_status_t s = ws.reserve(bytes)) return s;
     uint16_t *d16 = ws.take<uint16_t>(M * ldd);
@@ -1168,30 +1169,30 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
         awq::GemmMaps maps;
         awq::GemmArgs a{};
         a.splits = 1;
-        a.M = M;
-        a.N = n;
+        a.M = few ? n : M;
+        a.N = few ? M : n;
         a.V = V;
         a.v0 = v0;
-        a.bn = awq::gemm_tile_cols(M, n, sms);
-        a.mt = ceil_div(M, 256);
-        a.nt = ceil_div(n, a.bn);
+        a.bn = few ? static_cast<int>((M + 31) / 32 * 32) : awq::gemm_tile_cols(M, n, sms);
+        a.mt = ceil_div(a.M, 256);
+        a.nt = ceil_div(a.N, a.bn);
         a.nk[0] = static_cast<int>(in / 64);
         a.labels = labels;
         a.lse = lse;
         a.dloss = dloss;
         a.d16 = d16;
         a.ldd = ldd;
-        if (awq_status_t s = map_kmajor(&maps.a, true, x, in, M, in, 128)) return s;
-        if (awq_status_t s = map_kmajor(&maps.b, true, Wp, in, n, in, a.bn / 2)) return s;
-        AWQ_CUDA(awq::launch_gemm16(awq::EPI_CE_BWD, true, false, maps, a, sms, st));
+        if (awq_status_t s = map_kmajor(&maps.a, true, few ? Wp : x, in, a.M, in, 128)) return s;
+        if (awq_status_t s = map_kmajor(&maps.b, true, few ? x : Wp, in, a.N, in, a.bn / 2)) return s;
+        AWQ_CUDA(awq::launch_gemm16(few ? awq::EPI_CE_BWD_T : awq::EPI_CE_BWD, true, false, maps, a, sms, st));
         awq::GemmArgs b{};
         // (the last piece may be short: eight slabs to a split there, too)
-        b.splits = ceil_div(n, 64) / 8 < splits ? ceil_div(n, 64) / 8 : splits;
+        b.splits = ceil_div(n, 64) / 8 < gp.splits ? ceil_div(n, 64) / 8 : gp.splits;
         if (b.splits < 2) b.splits = 1;
         b.part4 = part4;
         b.M = M;
         b.N = in;
-        b.bn = awq::gemm_tile_cols(M, in, sms);
+        b.bn = gp.bn;
         b.mt = ceil_div(M, 256);
         b.nt = ceil_div(in, b.bn);
         b.nk[0] = ceil_div(n, 64);

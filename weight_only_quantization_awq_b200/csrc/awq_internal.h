@@ -204,10 +204,13 @@ cudaError_t launch_wait_selftest(long long limit, bool arrive, int *err, cudaStr
 // through packed weights and score a vocabulary (k_dense.cu), with their operand preparation
 // (k_dequant.cu)
 enum { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2 };
-enum { EPI_GATED = 0, EPI_GATED_BWD = 1, EPI_OUT = 2, EPI_CE = 3, EPI_CE_BWD = 4, EPI_CE_T = 5 };
+enum { EPI_GATED = 0, EPI_GATED_BWD = 1, EPI_OUT = 2, EPI_CE = 3, EPI_CE_BWD = 4, EPI_CE_T = 5, EPI_CE_BWD_T = 6 };
 // Tokens up to which the vocabulary goes on the rows (32000 x 4096: 13 tokens 45 against 64 us, 128 tokens
 // 50 against 53: the products cost the columns, and 256 rows of tokens are mostly padding).
 constexpr int64_t CE_T_MAX_M = 128;
+// The same for the gradients of the logits (40062 x 1024, one token: 23 against 31 us; 1007 x 384, 111 tokens 11.5
+// against 6.5: a token's row is written 64 bytes at a time).
+constexpr int64_t CE_BWD_T_MAX_M = 64;
 struct GemmMaps {
     CUtensorMap a, b;           // K-major: box 64 k x 128 rows (b: bn / 2 rows); MN-major: box 64 x 64
 };
@@ -243,8 +246,12 @@ struct GemmArgs {
     bool first, last;           // first: acc is not read; last: the result goes to out
 };
 int gemm_tile_cols(int64_t M, int64_t N, int num_sms);
-// K splits of an EPI_OUT product, and the float4 of workspace for their partial sums.
-int64_t gemm_part_vecs(int64_t M, int64_t N, int64_t k, int num_sms, int *splits);
+// Tile columns and K splits of an EPI_OUT product, and the float4 of workspace for its partial sums.
+struct GemmPlan {
+    int bn, splits;
+    int64_t part_vecs;
+};
+GemmPlan gemm_plan(int64_t M, int64_t N, int64_t k, int num_sms);
 cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, const GemmArgs &a, int num_sms,
                           cudaStream_t st);
 cudaError_t launch_ce_final(const float2 *part, int n, bool rows, int64_t M, const int64_t *labels, int64_t V,

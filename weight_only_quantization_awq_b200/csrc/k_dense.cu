@@ -10,7 +10,7 @@
 //                  (B read along its rows: K is W's row) and the head's weight gradient;
 //   EPI_CE         logits = x W^T of one vocabulary tile: each row's maximum and sum of
 //                  exponentials over the tile, and the label's logit; the logits stay on chip;
-//   EPI_CE_T       the same for few tokens, the vocabulary on D's rows;
+//   EPI_CE_T, EPI_CE_BWD_T   the same and the next for few tokens, the vocabulary on D's rows;
 //   EPI_CE_BWD     (exp(logit - lse) - [n = label]) * dloss as bf16, one piece of the vocabulary.
 //
 // CTA pairs (clusters of two, one CTA per SM, persistent over output tiles): a tile is 256 rows
@@ -443,6 +443,32 @@ __device__ __forceinline__ void epi_ce_bwd(const GemmArgs &a, uint32_t acc, int6
     }
 }
 
+// The gradients of few tokens, the vocabulary on the rows: the lanes of a warp are 32 neighbouring
+// entries of a token's row.
+__device__ __forceinline__ void epi_ce_bwd_t(const GemmArgs &a, uint32_t acc, int64_t row, int par) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int c = 16 * par; c < a.bn; c += 32) {
+        uint32_t r[16];
+        tmem_ld16_wait(acc + c, r);
+        // lane k holds token c + k's label, log-sum and weight
+        const int64_t m = c + (lane & 15);
+        const bool in = m < a.N;
+        const int64_t lab = in ? __ldg(a.labels + m) : -1;
+        const float lse = in ? __ldg(a.lse + m) : 0.0f, w = in ? __ldg(a.dloss + m) : 0.0f;
+        const int rel = lab >= 0 && lab < a.V ? static_cast<int>(lab) : -1;   // V <= 2^24
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int lk = __shfl_sync(0xffffffffu, rel, k);
+            const float sk = __shfl_sync(0xffffffffu, lse, k), wk = __shfl_sync(0xffffffffu, w, k);
+            float p = exp2f((__uint_as_float(r[k]) - sk) * LOG2E);
+            if (lk == a.v0 + row) p -= 1.0f;
+            if (row < a.M && c + k < a.N)
+                a.d16[(c + k) * a.ldd + row] = __bfloat16_as_ushort(__float2bfloat16_rn(lk >= 0 ? p * wk : 0.0f));
+        }
+    }
+}
+
 template <int EPI, bool BF16, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(GM_THREADS, 1)
     gemm16_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs a) {
@@ -595,6 +621,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
             if constexpr (EPI == EPI_CE) epi_ce(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, tl.n, par);
             if constexpr (EPI == EPI_CE_T)
                 epi_ce_t(a, acc, row, tl.m * 8 + static_cast<int>(rank) * 4 + quad, par);
+            if constexpr (EPI == EPI_CE_BWD_T) epi_ce_bwd_t(a, acc, row, par);
             if constexpr (EPI == EPI_CE_BWD) epi_ce_bwd(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par);
             tc_fence_before();
             __syncwarp();
@@ -653,18 +680,19 @@ cudaError_t launch_t(const GemmMaps &maps, const GemmArgs &a, int num_sms, cudaS
 
 }  // namespace
 
-// Tile columns: of the multiples of 32 up to 256 the one with the least waves x time of a 64-deep
-// slab.  Measured slab times (cycles at 1.9 GHz, 2048 tokens, K-major and MN-major B alike): 64
+// Measured cycles (at 1.9 GHz) of a 64-deep slab of a tile bn columns wide, K-major and MN-major B alike: 64
 // columns 410-450, 128 460-490, 192 530-560, 224 610, 256 690-720: a handshake and the A tile cost
-// about 350 cycles beside one cycle a column, until the MMAs themselves take over at 224.
+// about 350 beside one a column, until the MMAs themselves take over at 224.
+static int slab_cycles(int bn) { return bn <= 192 ? 350 + bn : 272 * bn / 100; }
+
+// Tile columns: of the multiples of 32 up to 256 the one with the least waves x time of a slab.
 int gemm_tile_cols(int64_t M, int64_t N, int num_sms) {
     const int64_t mt = (M + 255) / 256, pairs = num_sms / 2;
     int best = 256;
     int64_t cost = INT64_MAX;
     for (int bn = 256; bn >= 64; bn -= 32) {
         const int64_t tiles = mt * ((N + bn - 1) / bn);
-        const int slab = bn <= 192 ? 350 + bn : 272 * bn / 100;
-        const int64_t c = (tiles + pairs - 1) / pairs * slab;
+        const int64_t c = (tiles + pairs - 1) / pairs * slab_cycles(bn);
         if (c < cost) {
             cost = c;
             best = bn;
@@ -673,15 +701,26 @@ int gemm_tile_cols(int64_t M, int64_t N, int num_sms) {
     return best;
 }
 
-int64_t gemm_part_vecs(int64_t M, int64_t N, int64_t k, int num_sms, int *splits) {
-    const int bn = gemm_tile_cols(M, N, num_sms);
-    const int64_t tiles = ((M + 255) / 256) * ((N + bn - 1) / bn), nk = (k + 63) / 64, pairs = num_sms / 2;
-    // Tiles that leave half of the pairs idle or more: K is split among them, at least 8 slabs (4 us)
-    // to a split, which the second kernel's 3 us are worth.
-    int64_t s = pairs / tiles;
-    s = s < nk / 8 ? s : nk / 8;
-    *splits = static_cast<int>(s < 2 ? 1 : s);
-    return *splits > 1 ? tiles * *splits * (bn / 4) * 256 : 0;
+GemmPlan gemm_plan(int64_t M, int64_t N, int64_t k, int num_sms) {
+    const int64_t mt = (M + 255) / 256, pairs = num_sms / 2, nk = (k + 63) / 64;
+    GemmPlan p{256, 1, 0};
+    int64_t cost = INT64_MAX;
+    for (int bn = 256; bn >= 64; bn -= 32) {
+        const int64_t tiles = mt * ((N + bn - 1) / bn);
+        // Tiles that leave pairs idle: K is split among them, at least 8 slabs to a split; the second
+        // kernel costs about 3 us.
+        int64_t s = pairs / tiles;
+        s = s < nk / 8 ? s : nk / 8;
+        if (s < 2) s = 1;
+        const int64_t c = (tiles * s + pairs - 1) / pairs * ((nk + s - 1) / s) * slab_cycles(bn) + (s > 1 ? 6000 : 0);
+        if (c < cost) {
+            cost = c;
+            p.bn = bn;
+            p.splits = static_cast<int>(s);
+            p.part_vecs = s > 1 ? tiles * s * (bn / 4) * 256 : 0;
+        }
+    }
+    return p;
 }
 
 cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, const GemmArgs &a, int num_sms,
@@ -699,6 +738,7 @@ cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, c
         case EPI_GATED_BWD: return launch_t<EPI_GATED_BWD, false, false, false>(maps, a, num_sms, st);
         case EPI_CE: return launch_t<EPI_CE, true, false, false>(maps, a, num_sms, st);
         case EPI_CE_T: return launch_t<EPI_CE_T, true, false, false>(maps, a, num_sms, st);
+        case EPI_CE_BWD_T: return launch_t<EPI_CE_BWD_T, true, false, false>(maps, a, num_sms, st);
         case EPI_CE_BWD: return launch_t<EPI_CE_BWD, true, false, false>(maps, a, num_sms, st);
         default:
             if (a_mn) return launch_t<EPI_OUT, true, true, true>(maps, a, num_sms, st);
