@@ -1107,7 +1107,7 @@ awq_status_t awq_cross_entropy(const uint16_t *x, int64_t M, int64_t in, const u
     a.mt = ceil_div(a.M, 256);
     a.nt = ceil_div(a.N, a.bn);
     a.nk[0] = static_cast<int>(in / 64);
-    const int parts = few ? 8 * a.mt : 2 * a.nt;      // partial (maximum, sum) pairs of a token
+    const int parts = few ? 8 * a.mt : 4 * a.nt;      // partial (maximum, sum) pairs of a token
     Workspace ws(st);
     if (awq_status_t s = ws.reserve(Workspace::up(4 * M) + Workspace::up(sizeof(float2) * M * parts))) return s;
     a.tgt = ws.take<float>(M);

@@ -236,7 +236,7 @@ struct GemmArgs {
     int64_t V, v0;              // vocabulary; first entry of this piece
     const float *lse, *dloss;   // [M]
     float *tgt;                 // [M] the label's logit
-    float2 *part;               // [2 nt][M] (EPI_CE_T: [N][8 mt]) (maximum, sum of exponentials) without the label's
+    float2 *part;               // [4 nt][M] (EPI_CE_T: [N][8 mt]) (maximum, sum of exponentials) without the label's
     const uint16_t *x, *w;      // the operands themselves, rows of `inner` columns (the labels' logits)
     // outputs
     uint16_t *out;              // bf16

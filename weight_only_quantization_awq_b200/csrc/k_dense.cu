@@ -17,8 +17,8 @@
 // x bn columns (bn <= 256, a multiple of 32) on tcgen05.mma.cta_group::2, M = 256, N = bn,
 // K = 16.  Each CTA stages its own 128 rows of A and half of B's columns, 64 deep, by TMA into a
 // 192 KB ring (six stages at bn = 256); the accumulator has two 256-column halves of TMEM, so the epilogue of a
-// tile overlaps the main loop of the next.  Warps: 0 TMA, 1 MMA, 4-11 epilogue (lane = row, two warps a
-// row's alternate 16-column chunks).
+// tile overlaps the main loop of the next.  Warps: 0 TMA, 1 MMA, from 4 on the epilogue (lane =
+// row, two or four warps taking a row's 16-column chunks in turn).
 // A K-major operand lies as [rows][64 k] in 128-byte swizzled rows; an operand read along its
 // rows (MN-major) as blocks of [64 k][64 n], 8 KB each, in the same swizzle.
 //
@@ -46,8 +46,17 @@ namespace {
 constexpr int GM_MAX_STAGES = 12;
 constexpr int GM_A_BYTES = 128 * SLAB_K * 2;          // 16 KB: this CTA's rows of A
 constexpr int GM_RING = 192 * 1024;                   // operand ring
-constexpr int GM_THREADS = 384;
-constexpr int GM_EPI_WARP0 = 4;                       // warps 4-11: two per TMEM lane quadrant, alternate 16-column chunks
+constexpr int GM_EPI_WARP0 = 4;                       // the epilogue's warps: a row's 16-column chunks dealt to those of its quadrant
+// Warps per TMEM lane quadrant; EPI_CE keeps 256 columns of a row in its threads' registers.
+template <int EPI>
+constexpr int GM_EPI_Q = EPI == EPI_CE ? 4 : 2;
+template <int EPI>
+constexpr int GM_THREADS = (GM_EPI_WARP0 + 4 * GM_EPI_Q<EPI>) * 32;
+// The cross entropy's logits are accumulated GM_KCHUNK slabs (1024 columns) at a time on the tensor cores
+// and added up in registers: the tensor cores truncate each 16-column step towards zero, and over
+// a whole row the losses came out 1e-6 of themselves too low.
+template <int EPI>
+constexpr int GM_KCHUNK = EPI == EPI_CE || EPI == EPI_CE_T ? 16 : 1 << 30;
 constexpr int GM_BAND = 8;                            // row tiles walked together
 constexpr uint32_t GM_TMEM = 512;
 constexpr int GM_BARS = 2 * GM_MAX_STAGES + 4 + 1;
@@ -302,35 +311,47 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
 
 constexpr float LOG2E = 1.4426950408889634f;
 
-__device__ __forceinline__ void epi_ce(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int ntile, int par) {
-    const bool ok = row < a.M;
-    const int64_t lab = ok ? __ldg(a.labels + row) : -1;
-    float mx = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-    for (int c = 16 * par; c < a.bn; c += 32) {
-        uint32_t r[16];
-        tmem_ld16_wait(acc + c, r);
-        if (ok && n0 + c < a.N) {
-            float v[16], cm = -INFINITY;
-            const int64_t j = lab - n0 - c;
+// The logits of a row's chunks in registers, chunk i = columns 16 (sub + W i) .. + 15.
+constexpr int CE_CHUNKS = 4;
+
+// Add this K chunk's accumulator to them.
+template <int W>
+__device__ __forceinline__ void ce_gather(uint32_t acc, int bn, int sub, float (&v)[CE_CHUNKS][16]) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                // the label's own term joins in the last step (ce_final_kernel)
-                v[k] = n0 + c + k < a.N && j != k ? __uint_as_float(r[k]) : -INFINITY;
-                cm = fmaxf(cm, v[k]);
-            }
-            const float nm = fmaxf(mx, cm);
-            // a tile of nothing but -inf (or NaN) keeps a finite reference
-            const float ref = nm == -INFINITY ? 0.0f : nm;
-            float s = 0.0f;
+    for (int i = 0; i < CE_CHUNKS; ++i) {
+        const int c = 16 * (sub + W * i);
+        if (c < bn) {
+            uint32_t r[16];
+            tmem_ld16_wait(acc + c, r);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) s += exp2f((v[k] - ref) * LOG2E);
-            sum = sum * exp2f((mx - ref) * LOG2E) + s;
-            mx = nm;
+            for (int k = 0; k < 16; ++k) v[i][k] += __uint_as_float(r[k]);
         }
-        __syncwarp();
     }
-    if (ok) a.part[static_cast<int64_t>(2 * ntile + par) * a.M + row] = make_float2(mx, sum);
+}
+
+__device__ __forceinline__ void epi_ce(const GemmArgs &a, float (&v)[CE_CHUNKS][16], int64_t row, int64_t n0, int slot,
+                                       int sub) {
+    if (row >= a.M) return;
+    const int64_t lab = __ldg(a.labels + row);
+    float mx = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CE_CHUNKS; ++i) {
+        const int c = 16 * (sub + 4 * i);
+        const int64_t left = c < a.bn ? a.N - n0 - c : 0, j = lab - n0 - c;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            // the label's own term joins in the last step (ce_final_kernel)
+            if (k >= left || j == k) v[i][k] = -INFINITY;
+            mx = fmaxf(mx, v[i][k]);
+        }
+    }
+    // a tile of nothing but -inf (or NaN) keeps a finite reference
+    const float ref = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+    for (int i = 0; i < CE_CHUNKS; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sum += exp2f((v[i][k] - ref) * LOG2E);
+    a.part[static_cast<int64_t>(slot) * a.M + row] = make_float2(mx, sum);
 }
 
 // The same for few tokens, the vocabulary on the rows (D's row = entry, column = token): a warp
@@ -362,36 +383,36 @@ __device__ __forceinline__ float warp_reduce16(const float (&v)[16]) {
     return op(r, __shfl_xor_sync(0xffffffffu, r, 1));
 }
 
-__device__ __forceinline__ void epi_ce_t(const GemmArgs &a, uint32_t acc, int64_t row, int slot, int par) {
+__device__ __forceinline__ void epi_ce_t(const GemmArgs &a, float (&v)[CE_CHUNKS][16], int64_t row, int slot, int sub) {
     const int lane = threadIdx.x & 31;
     const bool ok = row < a.M;
-#pragma unroll 1
-    for (int c = 16 * par; c < a.bn; c += 32) {
-        uint32_t r[16];
-        tmem_ld16_wait(acc + c, r);
-        const int64_t m = c + (lane >> 1);            // the token this lane ends up with
-        const int64_t mine = m < a.N ? __ldg(a.labels + m) : -1;
-        float v[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const int64_t lab = __shfl_sync(0xffffffffu, mine, 2 * k);
-            v[k] = ok && lab != row ? __uint_as_float(r[k]) : -INFINITY;
-        }
-        const float mx = warp_reduce16<false>(v);
+    for (int i = 0; i < CE_CHUNKS; ++i) {
+        const int c = 16 * (sub + 2 * i);
+        if (c < a.bn) {
+            const int64_t m = c + (lane >> 1);        // the token this lane ends up with
+            const int64_t mine = m < a.N ? __ldg(a.labels + m) : -1;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float t = __shfl_sync(0xffffffffu, mx, 2 * k);
-            v[k] = exp2f((v[k] - (t == -INFINITY ? 0.0f : t)) * LOG2E);
+            for (int k = 0; k < 16; ++k) {
+                const int64_t lab = __shfl_sync(0xffffffffu, mine, 2 * k);
+                if (!ok || lab == row) v[i][k] = -INFINITY;
+            }
+            const float mx = warp_reduce16<false>(v[i]);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float t = __shfl_sync(0xffffffffu, mx, 2 * k);
+                v[i][k] = exp2f((v[i][k] - (t == -INFINITY ? 0.0f : t)) * LOG2E);
+            }
+            const float sum = warp_reduce16<true>(v[i]);
+            if (m < a.N && (lane & 1) == 0) a.part[m * (8 * a.mt) + slot] = make_float2(mx, sum);
         }
-        const float sum = warp_reduce16<true>(v);
-        if (m < a.N && (lane & 1) == 0) a.part[m * (8 * a.mt) + slot] = make_float2(mx, sum);
     }
 }
 
 // The labels' logits in fp32 by the two warps that have no other work, a warp per token: products of
 // bf16 values are exact, so this is the fp32 rounding of a few additions per lane.  The tensor
-// cores' accumulation truncates (2.5e-6 of the loss at 4096 columns), which shows where the
-// label dominates its row; the other terms of the sum average it out.
+// cores' truncation shows most where the label dominates its row (2.5e-6 of the loss at 4096
+// columns without this); the other terms of the sum average it out.
 __device__ __forceinline__ void ce_labels(const GemmArgs &a, int64_t tokens, int first, int step) {
     const int lane = threadIdx.x & 31;
     for (int64_t m = first; m < tokens; m += step) {
@@ -470,7 +491,7 @@ __device__ __forceinline__ void epi_ce_bwd_t(const GemmArgs &a, uint32_t acc, in
 }
 
 template <int EPI, bool BF16, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(GM_THREADS, 1)
+__global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
     gemm16_kernel(const __grid_constant__ GemmMaps maps, const __grid_constant__ GemmArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>(
@@ -500,7 +521,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&acc_full[h], 1);
-            mbar_init(&acc_empty[h], 2 * 8);           // epilogue warps of both CTAs
+            mbar_init(&acc_empty[h], 2 * 4 * GM_EPI_Q<EPI>);   // epilogue warps of both CTAs
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -517,7 +538,9 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    // All 512 columns: the allocation starts at column 0, and a constant base keeps the MMAs' operands
+    // in uniform registers.
+    constexpr uint32_t tmem_base = 0;
 
     if (warp == 0) {
         uint32_t st = 0, ph = 1;
@@ -568,28 +591,30 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
             const uint64_t db0 = B_MN ? sdesc_mnmajor_sw128(ring0 + GM_A_BYTES) : sdesc_kmajor_sw128(ring0 + GM_A_BYTES);
             uint32_t st = 0, ph = 0, ti = 0;
             bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs, ++ti) {
-                const uint32_t h = ti & 1u;
-                ok = mbar_wait_warp(&acc_empty[h], ((ti >> 1) & 1u) ^ 1u, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t d = tmem_base + h * 256;
+            for (int t = pair; t < tiles && ok; t += pairs) {
                 const int k0 = split_at(t % a.splits, nk, a.splits), k1 = split_at(t % a.splits + 1, nk, a.splits);
-                for (int kb = k0; kb < k1; ++kb) {
-                    ok = mbar_wait_warp(&full[st], ph, abort_flag);
+                for (int kc = k0; kc < k1 && ok; kc += GM_KCHUNK<EPI>, ++ti) {
+                    const uint32_t h = ti & 1u;
+                    const int ke = k1 - kc < GM_KCHUNK<EPI> ? k1 : kc + GM_KCHUNK<EPI>;
+                    ok = mbar_wait_warp(&acc_empty[h], ((ti >> 1) & 1u) ^ 1u, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sa = ring0 + st * stage, sb = sa + GM_A_BYTES;
+                    const uint32_t d = tmem_base + h * 256;
+                    for (int kb = kc; kb < ke; ++kb) {
+                        ok = mbar_wait_warp(&full[st], ph, abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t da = sdesc_at(da0, st * stage), db = sdesc_at(db0, st * stage);
 #pragma unroll
-                    for (int k = 0; k < SLAB_K / 16; ++k)
-                        umma_f16_pair_lead(lead, d, A_MN ? sdesc_mnmajor_sw128(sa + k * 2048) : sdesc_kmajor_sw128(sa + k * 32),
-                                          B_MN ? sdesc_mnmajor_sw128(sb + k * 2048) : sdesc_kmajor_sw128(sb + k * 32),
-                                           idesc, (kb > k0 || k > 0) ? 1u : 0u);
-                    umma_commit_pair_lead(lead, &empty[st], 0x3);
-                    if (kb == k1 - 1) umma_commit_pair_lead(lead, &acc_full[h], 0x3);
-                    if (++st == static_cast<uint32_t>(stages)) {
-                        st = 0;
-                        ph ^= 1u;
+                        for (int k = 0; k < SLAB_K / 16; ++k)
+                            umma_f16_pair_lead(lead, d, sdesc_at(da, A_MN ? k * 2048 : k * 32),
+                                               sdesc_at(db, B_MN ? k * 2048 : k * 32), idesc, (kb > kc || k > 0) ? 1u : 0u);
+                        umma_commit_pair_lead(lead, &empty[st], 0x3);
+                        if (kb == ke - 1) umma_commit_pair_lead(lead, &acc_full[h], 0x3);
+                        if (++st == static_cast<uint32_t>(stages)) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
                     }
                 }
             }
@@ -601,15 +626,44 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
             ce_labels(a, EPI == EPI_CE ? a.M : a.N, static_cast<int>(blockIdx.x) * 2 + warp - 2, static_cast<int>(gridDim.x) * 2);
     } else {
         const int quad = warp & 3, par = (warp - GM_EPI_WARP0) >> 2;
+        const uint32_t acc0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
         uint32_t ti = 0;
-        for (int t = pair; t < tiles; t += pairs, ++ti) {
-            const Tile tl = decode_tile(t / a.splits, a.mt, a.nt);
-            const uint32_t h = ti & 1u;
-            const bool ok = mbar_wait_sleep(&acc_full[h], (ti >> 1) & 1u, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) break;
+        bool ok = true;
+        auto await = [&]() {                          // the next accumulator half
+            ok = __all_sync(0xffffffffu, mbar_wait_sleep(&acc_full[ti & 1u], (ti >> 1) & 1u, abort_flag));
             tc_fence_after();
-            const uint32_t acc = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + h * 256;
+            return ok;
+        };
+        auto release = [&]() {                        // ... may be overwritten
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[ti & 1u], 0));
+            ++ti;
+        };
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            const Tile tl = decode_tile(t / a.splits, a.mt, a.nt);
             const int64_t row = static_cast<int64_t>(tl.m) * 256 + rank * 128 + quad * 32 + lane;
+            if constexpr (EPI == EPI_CE || EPI == EPI_CE_T) {
+                float v[CE_CHUNKS][16];
+#pragma unroll
+                for (int i = 0; i < CE_CHUNKS; ++i)
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[i][k] = 0.0f;
+                for (int kc = 0; kc < nk && ok; kc += GM_KCHUNK<EPI>) {
+                    if (!await()) break;
+                    ce_gather<GM_EPI_Q<EPI>>(acc0 + (ti & 1u) * 256, a.bn, par, v);
+                    release();
+                }
+                if (!ok) break;
+                if constexpr (EPI == EPI_CE)
+                    epi_ce(a, v, row, static_cast<int64_t>(tl.n) * a.bn, 4 * tl.n + par, par);
+                else
+                    epi_ce_t(a, v, row, tl.m * 8 + static_cast<int>(rank) * 4 + quad, par);
+                __syncwarp();
+                continue;
+            }
+            if (!await()) break;
+            const uint32_t acc = acc0 + (ti & 1u) * 256;
             if constexpr (EPI == EPI_GATED) epi_gated(a, acc, row, static_cast<int64_t>(tl.n) * bh, par);
             if constexpr (EPI == EPI_GATED_BWD) epi_gated_bwd(a, acc, row, static_cast<int64_t>(tl.n) * bh, par);
             if constexpr (EPI == EPI_OUT) {
@@ -618,14 +672,9 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
                 else
                     epi_out(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par);
             }
-            if constexpr (EPI == EPI_CE) epi_ce(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, tl.n, par);
-            if constexpr (EPI == EPI_CE_T)
-                epi_ce_t(a, acc, row, tl.m * 8 + static_cast<int>(rank) * 4 + quad, par);
             if constexpr (EPI == EPI_CE_BWD_T) epi_ce_bwd_t(a, acc, row, par);
             if constexpr (EPI == EPI_CE_BWD) epi_ce_bwd(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[h], 0));
+            release();
         }
     }
 
@@ -639,7 +688,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
     cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, GM_TMEM);
+        tmem_dealloc_pair(*tmem_slot, GM_TMEM);
     }
 }
 
@@ -648,7 +697,7 @@ cudaError_t launch_t(const GemmMaps &maps, const GemmArgs &a, int num_sms, cudaS
     auto *kernel = gemm16_kernel<EPI, BF16, A_MN, B_MN>;
     cudaError_t e;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(GM_THREADS);
+    cfg.blockDim = dim3(GM_THREADS<EPI>);
     cfg.dynamicSmemBytes = GM_SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
