@@ -18,7 +18,7 @@ def skinny_plan(M, tiles, k):
     n = -(-(-(-M // tt)) // 16) * 16
     tt = -(-M // n)
     ks = -(-k // 128)
-    cost = {c: -(-ks // c) * 400 + (c * 60 + 2500 if c > 1 else n * 60) for c in range(1, min(ks, 64) + 1)}
+    cost = {c: -(-ks // c) * 600 + (c * 60 + 3000 if c > 1 else 0) for c in range(1, min(ks, 64) + 1)}
     share = min(cost, key=cost.get)
     units = tiles * ks * tt
     return n, tt, ks, min(tiles * tt * share, SMS, units), units
@@ -35,7 +35,7 @@ def test_skinny_ranges_cover_every_stage_once(M, tiles, k):
     n, tt, ks, grid, units = skinny_plan(M, tiles, k)
     assert n % 16 == 0 and n <= MAX_N and n * tt >= M and n * (tt - 1) < M
     stages = min((232448 - 1024 - TAIL) // (A_BYTES + n * 256), MAX_STAGES)
-    assert stages >= GROUPS
+    assert stages >= GROUPS and 6 * (2 * 16 * 128 * 4 + 2 * 256 * 4) <= stages * (A_BYTES + n * 256)
     assert 1024 + stages * (A_BYTES + n * 256) + TAIL <= 232448
     seen, slots = [], {}
     for c in range(grid):

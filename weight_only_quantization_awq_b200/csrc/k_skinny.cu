@@ -18,7 +18,8 @@
 // of its stages ahead into registers; shift, LOP3, exact HSUB2 or HFMA2 to code - z, HMUL2 by
 // Delta 2^-kW, eight 16-byte stores); one warp fetches the token tiles by TMA, one
 // issues the MMAs, four write the results from TMEM, whose two accumulators let a tile's
-// epilogue run beside the next tile's products.
+// epilogue run beside the next tile's products.  Where every CTA has whole tiles (small layers), its last
+// tile's results, which nothing runs beside, are shared out among these four and the dequantising warps.
 //
 // Split: the (tile, 128-deep stage) sequence is cut into equal contiguous ranges, one per CTA,
 // one CTA per SM.  A tile that several CTAs share leaves fp32 partial sums in the workspace, and a
@@ -55,7 +56,10 @@ constexpr int SK_MAX_N = 144;                         // tokens per tile: the mo
 static_assert(3 * (SK_A_BYTES + SK_MAX_N * 256) + 1024 + 2 * 16 * 128 * 4 + 2 * 256 * 4 + 512 <= 232448 && SK_GROUPS <= 3,
               "a ring stage for each group");
 constexpr int SK_XBUF = 2 * 16 * 128 * 4;             // the epilogue's exchange of gate and up values
-constexpr int SK_TAIL = SK_XBUF + 2 * 256 * 4 + (4 * SK_MAX_STAGES + 5) * 8 + 32;
+constexpr int SK_SETS = 1 + SK_DQ_WARPS / 4;          // sets of four warps, one per TMEM lane quadrant
+constexpr int SK_SET_BYTES = SK_XBUF + 2 * 256 * 4;   // a set's exchange and token scales
+static_assert((SK_SETS - 1) * SK_SET_BYTES <= 3 * (SK_A_BYTES + 16 * 256), "the dequantising sets' lie in the ring");
+constexpr int SK_TAIL = SK_SET_BYTES + (4 * SK_MAX_STAGES + 5) * 8 + 32;
 
 __device__ __forceinline__ uint64_t sk_desc_mn(uint32_t saddr) {
     uint64_t d = 0;
@@ -89,11 +93,11 @@ __device__ __forceinline__ int sk_first(const SkinnyArgs &a, int c) {
 }
 
 // The results of K tokens (the tile's tokens c .. c + K - 1) from the accumulator's 128 lanes, thread e
-// holding lane e's values.  tsc, tsd: the tile's token scales.  BAR: hardware barrier of the 128 threads.
+// holding lane e's values.  tsc, tsd: the tile's token scales.  bar: hardware barrier of the 128 threads.
 // x: [K][128] floats of shared memory (gated products: lanes 64-127 hold the up values of lanes 0-63).
-template <int EPI, int K, int BAR>
+template <int EPI, int K>
 __device__ __forceinline__ void sk_finish(const SkinnyArgs &a, int t, int m0, int mcount, int c, const float (&v)[K],
-                                          int e, float sw, const float *tsc, const float *tsd, float *x) {
+                                          int e, float sw, const float *tsc, const float *tsd, float *x, int bar) {
     if (EPI == EPI_OUT) {
         const int64_t col = static_cast<int64_t>(t) * 128 + (e & ~7) + frag_perm8(e & 7);
         if (col < a.I) {
@@ -108,7 +112,7 @@ __device__ __forceinline__ void sk_finish(const SkinnyArgs &a, int t, int m0, in
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) x[k * 128 + e] = v[k];
-    named_bar_sync(BAR, 128);
+    named_bar_sync(bar, 128);
     const int64_t f = static_cast<int64_t>(t) * 64 + (e & 63);
     if (f < a.F) {
 #pragma unroll
@@ -177,10 +181,11 @@ __global__ void __launch_bounds__(128) skinny_finish_kernel(const __grid_constan
         v[2] += w.z;
         v[3] += w.w;
     }
-    sk_finish<EPI, 4, 0>(a, t, m0, mcount, c, v, e, ldexpf(1.0f, kw), tsc - c, tsd - c, x);
+    sk_finish<EPI, 4>(a, t, m0, mcount, c, v, e, ldexpf(1.0f, kw), tsc - c, tsd - c, x, 0);
 }
 
-template <bool GRAD, int EPI>
+// WHOLE: no tile is shared, and the last tile's results are shared out among the sets of warps.
+template <bool GRAD, int EPI, bool WHOLE>
 __global__ void __launch_bounds__(SK_THREADS, 1)
     skinny_kernel(const __grid_constant__ CUtensorMap bmap, const __grid_constant__ SkinnyArgs a) {
     extern __shared__ uint8_t smem_raw[];
@@ -365,6 +370,39 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
                 }
             }
         }
+        if (WHOLE) {
+            // The last tile's results: this set's chunks of 16 tokens.  Its buffers lie in the ring, which the
+            // MMAs have read by then.  (The barrier that every MMA is done has a single phase, unlike
+            // acc_full, whose phases these warps have not followed.)
+            const int e = threadIdx.x & 127, set = 1 + static_cast<int>(threadIdx.x >> 7), kw = dq_exp(a.dmax);
+            const int T = (u1 - 1) / a.ks, tt = T / a.tiles, t = T - tt * a.tiles;
+            const int m0 = tt * a.n, mcount = static_cast<int>(a.M - m0 < a.n ? a.M - m0 : a.n);
+            float sc[2] = {0.0f, 0.0f}, sd[2] = {0.0f, 0.0f};
+            for (int i = 0; i < 2; ++i)
+                if (e + 128 * i < mcount) sk_token_scale<GRAD, EPI>(a, m0 + e + 128 * i, kw, sc[i], sd[i]);
+            if (ok) ok = mbar_wait_warp(drain, 0, abort_flag);
+            if (named_bar_and(1 + set, 128, ok && !*abort_flag)) {
+                tc_fence_after();
+                float *xs = reinterpret_cast<float *>(ring + (set - 1) * SK_SET_BYTES), *ss = xs + 2 * 16 * 128;
+                for (int i = 0; i < 2; ++i) {
+                    ss[e + 128 * i] = sc[i];
+                    ss[256 + e + 128 * i] = sd[i];
+                }
+                named_bar_sync(1 + set, 128);
+                const uint32_t acc = tmem_base + (static_cast<uint32_t>(e & 96) << 16) +
+                                     (static_cast<uint32_t>(T - u0 / a.ks) & 1u) * a.acc_cols;
+                uint32_t flip = 0;
+                for (int c = 16 * set; c < a.n; c += 16 * SK_SETS, flip ^= 1u) {
+                    uint32_t rv[16];
+                    tmem_ld16_wait(acc + c, rv);
+                    float v[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(rv[k]);
+                    sk_finish<EPI, 16>(a, t, m0, mcount, c, v, e, ldexpf(1.0f, kw), ss, ss + 256, xs + flip * (16 * 128), 1 + set);
+                    __syncwarp();
+                }
+            }
+        }
     } else if (warp == SK_WARP_TMA) {
         // ---- token tiles
         griddep_wait();
@@ -448,7 +486,7 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
         for (int u = u0; u < u1; ++seg) {
             const int T = u / a.ks, tt = T / a.tiles, t = T - tt * a.tiles;
             const int b0 = T * a.ks, b1 = b0 + a.ks, end = b1 < u1 ? b1 : u1;
-            const bool whole = u == b0 && end == b1;
+            const bool whole = WHOLE || (u == b0 && end == b1);
             const int m0 = tt * a.n, mcount = static_cast<int>(a.M - m0 < a.n ? a.M - m0 : a.n);
             const uint32_t h = seg & 1u, acc = tmem_base + quad + h * a.acc_cols;
             if (whole && tt != have) {
@@ -462,14 +500,14 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
             tc_fence_after();
             // a shared tile's partial sums: this CTA's slot [n / 4][128] of four tokens
             float4 *mine = a.part + static_cast<int64_t>(2 * blockIdx.x + (u0 > b0 ? 0 : 1)) * a.n * 32;
-            for (int c = 0; c < a.n; c += 16) {
+            for (int c = 0; c < a.n; c += WHOLE && end == u1 ? 16 * SK_SETS : 16) {
                 uint32_t rv[16];
                 tmem_ld16_wait(acc + c, rv);
                 float v[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(rv[k]);
                 if (whole) {
-                    sk_finish<EPI, 16, 1>(a, t, m0, mcount, c, v, e, sw, tsc, tsd, xbuf + flip * (16 * 128));
+                    sk_finish<EPI, 16>(a, t, m0, mcount, c, v, e, sw, tsc, tsd, xbuf + flip * (16 * 128), 1);
                     flip ^= 1u;
                 } else {
 #pragma unroll
@@ -494,14 +532,15 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
 
 template <bool GRAD, int EPI>
 cudaError_t launch_sk(const CUtensorMap &bmap, const SkinnyArgs &a, bool split, cudaStream_t st) {
-    static bool attr_set[64] = {};                    // per device
+    static bool attr_set[64][2] = {};                 // per device
+    auto *kernel = split ? skinny_kernel<GRAD, EPI, false> : skinny_kernel<GRAD, EPI, true>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(skinny_kernel<GRAD, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    if (dev < 0 || dev >= 64 || !attr_set[dev][split]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
         if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+        if (dev >= 0 && dev < 64) attr_set[dev][split] = true;
     }
     const size_t smem = 1024 + static_cast<size_t>(a.stages) * (SK_A_BYTES + a.n * 256) + SK_TAIL;
     cudaLaunchConfig_t cfg = {};
@@ -514,7 +553,7 @@ cudaError_t launch_sk(const CUtensorMap &bmap, const SkinnyArgs &a, bool split, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, skinny_kernel<GRAD, EPI>, bmap, a);
+    e = cudaLaunchKernelEx(&cfg, kernel, bmap, a);
     if (e != cudaSuccess || !split) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(a.units / a.ks), static_cast<unsigned>(a.n / 4));
     cfg.blockDim = dim3(128);
@@ -531,13 +570,12 @@ SkinnyPlan skinny_plan(int64_t M, int64_t tiles, int64_t k, int num_sms) {
     p.token_tiles = static_cast<int>((M + p.n - 1) / p.n);
     p.tiles = static_cast<int>(tiles);
     p.ks = static_cast<int>((k + 127) / 128);
-    // CTAs: one per SM, but no more of them to a tile than pays: a stage costs its CTA about 400 ns and
-    // the results of a whole tile 60 ns a token; the second kernel that shared tiles need takes
-    // 2.5 us, each CTA's partial sums about 60 ns of it.
+    // CTAs: one per SM, but no more of them to a tile than pays: a stage costs its CTA about 600 ns; the
+    // second kernel that shared tiles need takes 3 us, each CTA's partial sums about 60 ns of it.
     const int64_t units = tiles * p.ks * p.token_tiles;
     int64_t share = 1, best = INT64_MAX;
     for (int64_t c = 1; c <= p.ks && c <= 64; ++c) {
-        const int64_t cost = (p.ks + c - 1) / c * 400 + (c > 1 ? c * 60 + 2500 : p.n * 60);
+        const int64_t cost = (p.ks + c - 1) / c * 600 + (c > 1 ? c * 60 + 3000 : 0);
         if (cost < best) {
             best = cost;
             share = c;
