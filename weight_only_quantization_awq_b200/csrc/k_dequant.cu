@@ -12,10 +12,11 @@ namespace awq {
 namespace {
 
 // Largest |Delta| of one of DMAX_PARTS parts of the layer's scales, as fp16 bits, into dmax[part]
-// (a block of 256 threads).
+// (a block of 256 or 512 threads).
 __device__ __forceinline__ void scales_max(const uint16_t *__restrict__ scales, int64_t n, int part, unsigned *dmax) {
-    __shared__ unsigned wm[8];
-    const int64_t first = static_cast<int64_t>(part) * 256 + threadIdx.x, step = DMAX_PARTS * 256;
+    __shared__ unsigned wm[16];
+    const int T = static_cast<int>(blockDim.x);
+    const int64_t first = static_cast<int64_t>(part) * T + threadIdx.x, step = static_cast<int64_t>(DMAX_PARTS) * T;
     // 16 bytes at a time from the first 16-byte boundary on; the ragged ends one by one
     unsigned mb = 0u;
     const int64_t head = ((16 - (reinterpret_cast<uintptr_t>(scales) & 15)) & 15) / 2;
@@ -35,32 +36,39 @@ __device__ __forceinline__ void scales_max(const uint16_t *__restrict__ scales, 
     if ((threadIdx.x & 31) == 0) wm[threadIdx.x >> 5] = mb;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int k = 1; k < 8; ++k) mb = max(mb, wm[k]);
+        for (int k = 1; k < T / 32; ++k) mb = max(mb, wm[k]);
         dmax[part] = mb;
     }
 }
 
-// v[0..8) = source row elements [c, c + 8), divided by s where given.
-__device__ __forceinline__ void row_chunk(const uint16_t *__restrict__ r, const uint16_t *__restrict__ s16, int64_t c,
-                                          int64_t cols, bool vec, float (&v)[8]) {
-    if (vec) {
-        const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(r + c));
-        const uint32_t w[4] = {xv.x, xv.y, xv.z, xv.w};
+// Row elements [c, c + 8) as bf16 bits, zeros past the end.
+__device__ __forceinline__ uint4 row_chunk(const uint16_t *__restrict__ r, int64_t c, int64_t cols, bool vec) {
+    if (c >= cols) return make_uint4(0u, 0u, 0u, 0u);
+    if (vec) return __ldg(reinterpret_cast<const uint4 *>(r + c));
+    uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(w[e] << 16);
-            v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-        }
-    } else {
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = c + 2 * e < cols ? __ldg(r + c + 2 * e) : 0u;
+        const uint32_t hi = c + 2 * e + 1 < cols ? __ldg(r + c + 2 * e + 1) : 0u;
+        w[e] = lo | hi << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// v[0..8) = the chunk's values, divided by s where given.
+__device__ __forceinline__ void row_values(const uint4 &x, const uint16_t *__restrict__ s16, int64_t c, float (&v)[8]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? __uint_as_float(static_cast<uint32_t>(__ldg(r + c + e)) << 16) : 0.0f;
+    for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(w[e] << 16);
+        v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
     }
     if (s16) {                                        // cols is a multiple of 64 here
         const uint4 sv = __ldg(reinterpret_cast<const uint4 *>(s16 + c));
-        const uint32_t w[4] = {sv.x, sv.y, sv.z, sv.w};
+        const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const __half2 h = *reinterpret_cast<const __half2 *>(&w[e]);
+            const __half2 h = *reinterpret_cast<const __half2 *>(&sw[e]);
             // (2 ulp: far below the fp16 rounding that follows)
             v[2 * e] = __fdividef(v[2 * e], __low2float(h));
             v[2 * e + 1] = __fdividef(v[2 * e + 1], __high2float(h));
@@ -93,7 +101,7 @@ __device__ __forceinline__ float block_sum(float v, float *sm) {
 // Blocks from DMAX_PARTS on: one token each.  out[m] = fp16((row / s) * 2^-k), k from the row's largest
 // magnitude so that it lands in [2^14, 2^15); sx[m] = 2^k.  With dh: grow[m], an exponent
 // that bounds max |dh[m]| * ||row / s||.  The first blocks: the parts' largest |Delta|.
-__global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ s16,
+__global__ void __launch_bounds__(512) rows16_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ s16,
                                                      int64_t M, int64_t cols, int64_t ld,
                                                      const uint16_t *__restrict__ dh, int64_t F,
                                                      const uint16_t *__restrict__ scales, int64_t n_scales,
@@ -104,55 +112,50 @@ __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict_
         scales_max(scales, n_scales, static_cast<int>(blockIdx.x), dmax);
         return;
     }
-    __shared__ float sm[8];
+    __shared__ float sm[16];
     const int64_t m = blockIdx.x - DMAX_PARTS;
     const uint16_t *r = x + m * cols;
     const bool vec = cols % 8 == 0;
+    const int T = static_cast<int>(blockDim.x);
     constexpr int KEEP = 4;                           // chunks of a thread that stay in registers between the passes
-    float kept[KEEP][8];
-    float mx = 0.0f;
+    uint4 kept[KEEP];
+    float mx = 0.0f, v[8];
 #pragma unroll
-    for (int i = 0; i < KEEP; ++i) {
-        const int64_t c = (i * 256 + threadIdx.x) * 8;
-        if (c < cols) {
-            row_chunk(r, s16, c, cols, vec, kept[i]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) kept[i][e] = 0.0f;
-        }
-    }
+    for (int i = 0; i < KEEP; ++i) kept[i] = row_chunk(r, (i * T + threadIdx.x) * 8, cols, vec);
     float md = 0.0f;
     if (grow) {                                       // the token's largest |dh|
         const uint16_t *dr = dh + m * F;
         if (F % 8 == 0) {
             unsigned mb = 0u;                         // magnitudes of bf16 order as their bits
 #pragma unroll 4
-            for (int64_t f = threadIdx.x; f < F / 8; f += 256) {
+            for (int64_t f = threadIdx.x; f < F / 8; f += T) {
                 const uint4 q = __ldg(reinterpret_cast<const uint4 *>(dr) + f);
                 mb = __vmaxu2(mb, __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu),
                                            __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
             }
             md = __uint_as_float(max(mb >> 16, mb & 0xFFFFu) << 16);
         } else {
-            for (int64_t f = threadIdx.x; f < F; f += 256)
+            for (int64_t f = threadIdx.x; f < F; f += T)
                 md = fmaxf(md, fabsf(__uint_as_float(static_cast<uint32_t>(__ldg(dr + f)) << 16)));
         }
     }
-#pragma unroll
-    for (int i = 0; i < KEEP; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(kept[i][e]));
-    for (int64_t c = (KEEP * 256 + threadIdx.x) * 8; c < cols; c += 256 * 8) {
-        float v[8];
-        row_chunk(r, s16, c, cols, vec, v);
+    auto largest = [&](int64_t c, const uint4 &x8) {
+        row_values(x8, s16, c, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
+    };
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) {
+        const int64_t c = (i * T + threadIdx.x) * 8;
+        if (c < cols) largest(c, kept[i]);
     }
+    for (int64_t c = (KEEP * T + threadIdx.x) * 8; c < cols; c += T * 8) largest(c, row_chunk(r, c, cols, vec));
     mx = block_max(mx, sm);
     const int k = scale_exp(mx, 15);
     const float sc = ldexpf(1.0f, -k);
     float sq = 0.0f;                                  // of the scaled values: no overflow
-    auto put = [&](int64_t c, const float (&v)[8]) {
+    auto put = [&](int64_t c, const uint4 &x8) {
+        row_values(x8, s16, c, v);
         uint32_t h[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -166,14 +169,10 @@ __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict_
     };
 #pragma unroll
     for (int i = 0; i < KEEP; ++i) {
-        const int64_t c = (i * 256 + threadIdx.x) * 8;
+        const int64_t c = (i * T + threadIdx.x) * 8;
         if (c < cols) put(c, kept[i]);
     }
-    for (int64_t c = (KEEP * 256 + threadIdx.x) * 8; c < cols; c += 256 * 8) {
-        float v[8];
-        row_chunk(r, s16, c, cols, vec, v);
-        put(c, v);
-    }
+    for (int64_t c = (KEEP * T + threadIdx.x) * 8; c < cols; c += T * 8) put(c, row_chunk(r, c, cols, vec));
     if (threadIdx.x == 0) sx[m] = ldexpf(1.0f, k);
     if (grow) {
         sq = block_sum(sq, sm);
@@ -188,10 +187,14 @@ __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict_
     }
 }
 
-// W16[o][i] = fp16((code - z) * Delta * 2^-kW): one rounding, the difference and the power of two
-// are exact.  A block takes DQ_ROWS rows, a thread the same packed word (8 columns, one 16-byte
-// store) of each: their loads are in flight together, and a warp's loads and stores are contiguous.
-constexpr int DQ_ROWS = 4;
+__device__ __forceinline__ __half2 dq_h2(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
+__device__ __forceinline__ uint32_t dq_u32(__half2 v) { return *reinterpret_cast<const uint32_t *>(&v); }
+
+// W16[o][i] = fp16((code - z) * Delta * 2^-kW): the difference is exact, the product rounded once (and
+// Delta 2^-kW itself only below 2^-14, that is below 2^-24 of the largest).  A
+// block takes DQ_ROWS rows, a thread the same packed word (8 columns, one 16-byte store) of each: their
+// loads are in flight together, and a warp's loads and stores are contiguous.
+constexpr int DQ_ROWS = 2;
 __global__ void __launch_bounds__(256) dequant_kernel(const uint32_t *__restrict__ q,
                                                       const uint16_t *__restrict__ scales,
                                                       const uint32_t *__restrict__ zeros, int64_t O, int wpr, int lg,
@@ -201,34 +204,38 @@ __global__ void __launch_bounds__(256) dequant_kernel(const uint32_t *__restrict
     const int nzw = (nG + 7) / 8;
     const int64_t o0 = static_cast<int64_t>(blockIdx.x) * DQ_ROWS;
     const int rows = static_cast<int>(O - o0 < DQ_ROWS ? O - o0 : DQ_ROWS);
+    q += o0 * wpr;
+    scales += o0 * nG;
+    if (zeros) zeros += o0 * nzw;
+    uint4 *dst = reinterpret_cast<uint4 *>(out) + o0 * wpr;
     for (int w = threadIdx.x; w < wpr; w += blockDim.x) {
-        const int g = w >> (lg - 3);
+        const int g = w >> (lg - 3), zsh = 4 * (g & 7);
         uint32_t v[DQ_ROWS], zw[DQ_ROWS];
         uint16_t sv[DQ_ROWS];
 #pragma unroll
         for (int u = 0; u < DQ_ROWS; ++u) {
-            const int64_t o = o0 + (u < rows ? u : 0);
-            v[u] = __ldcs(q + o * wpr + w);           // read once
-            sv[u] = __ldg(scales + o * nG + g);
-            zw[u] = zeros ? __ldg(zeros + o * nzw + (g >> 3)) : 0x88888888u;
+            const int r = u < rows ? u : 0;           // (wpr <= 2^28: DQ_ROWS rows of words fit 32 bits)
+            v[u] = __ldcs(q + static_cast<uint32_t>(r * wpr + w));    // read once
+            sv[u] = __ldg(scales + static_cast<uint32_t>(r * nG + g));
+            zw[u] = zeros ? __ldg(zeros + static_cast<uint32_t>(r * nzw + (g >> 3))) : 0x88888888u;
         }
 #pragma unroll
         for (int u = 0; u < DQ_ROWS; ++u) {
             if (u >= rows) break;
-            const float d = __half2float(__ushort_as_half(sv[u])) * sw;
-            // nibbles (2e, 2e + 1) beside each other: 1024 + code as fp16 bits, minus (1024 + z) exactly
-            const uint32_t z = (0x6400u | ((zw[u] >> (4 * (g & 7))) & 15u)) * 0x00010001u;
-            uint32_t h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t b = v[u] >> (8 * e);
-                const uint32_t c = (b & 15u) | ((b << 12) & 0x000F0000u) | 0x64006400u;
-                const __half2 cz = __hsub2(*reinterpret_cast<const __half2 *>(&c), *reinterpret_cast<const __half2 *>(&z));
-                const float2 f = __half22float2(cz);
-                const __half2 hv = __floats2half2_rn(f.x * d, f.y * d);
-                h[e] = *reinterpret_cast<const uint32_t *>(&hv);
-            }
-            *reinterpret_cast<uint4 *>(out + ((o0 + u) * wpr + w) * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+            const float df = __half2float(__ushort_as_half(sv[u])) * sw;
+            const __half2 d = __floats2half2_rn(df, df);
+            // 1024 + code as fp16 bits minus (1024 + z); (1024 + 16 code) / 16 minus (64 + z): both exact
+            const __half2 z0 = dq_h2((0x6400u | ((zw[u] >> zsh) & 15u)) * 0x00010001u);
+            const __half2 z1 = __hsub2(dq_h2(0x63806380u), z0);
+            const __half2 r16 = dq_h2(0x2C002C00u);   // 1 / 16
+            const uint32_t v8 = v[u] >> 8, P = 0x64006400u;
+            const uint32_t e04 = dq_u32(__hmul2(__hsub2(dq_h2((v[u] & 0x000F000Fu) | P), z0), d));
+            const uint32_t e15 = dq_u32(__hmul2(__hfma2(dq_h2((v[u] & 0x00F000F0u) | P), r16, z1), d));
+            const uint32_t e26 = dq_u32(__hmul2(__hsub2(dq_h2((v8 & 0x000F000Fu) | P), z0), d));
+            const uint32_t e37 = dq_u32(__hmul2(__hfma2(dq_h2((v8 & 0x00F000F0u) | P), r16, z1), d));
+            dst[static_cast<uint32_t>(u * wpr + w)] =
+                make_uint4(__byte_perm(e04, e15, 0x5410), __byte_perm(e26, e37, 0x5410), __byte_perm(e04, e15, 0x7632),
+                           __byte_perm(e26, e37, 0x7632));
         }
     }
 }
@@ -258,7 +265,9 @@ cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t
 cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int64_t cols, int64_t ld,
                           const uint16_t *dh, int64_t F, const uint16_t *scales, int64_t n_scales, bool permute,
                           uint16_t *out, float *sx, int *grow, unsigned *dmax, cudaStream_t st) {
-    rows16_kernel<<<static_cast<unsigned>(M + DMAX_PARTS), 256, 0, st>>>(x, s16, M, cols, ld, dh, F, scales, n_scales,
+    // a row up to 8192 wide stays in the registers of 256 threads, twice that in 512's
+    const int threads = cols <= 8192 ? 256 : 512;
+    rows16_kernel<<<static_cast<unsigned>(M + DMAX_PARTS), threads, 0, st>>>(x, s16, M, cols, ld, dh, F, scales, n_scales,
                                                                         permute, out, sx, grow, dmax);
     return cudaGetLastError();
 }
