@@ -12,9 +12,9 @@ namespace awq {
 namespace {
 
 // Largest |Delta| of one of DMAX_PARTS parts of the layer's scales, as fp16 bits, into dmax[part]
-// (a block of 256 or 512 threads).
+// (a block of 128 or 256 threads).
 __device__ __forceinline__ void scales_max(const uint16_t *__restrict__ scales, int64_t n, int part, unsigned *dmax) {
-    __shared__ unsigned wm[16];
+    __shared__ unsigned wm[8];
     const int T = static_cast<int>(blockDim.x);
     const int64_t first = static_cast<int64_t>(part) * T + threadIdx.x, step = static_cast<int64_t>(DMAX_PARTS) * T;
     // 16 bytes at a time from the first 16-byte boundary on; the ragged ends one by one
@@ -55,7 +55,14 @@ __device__ __forceinline__ uint4 row_chunk(const uint16_t *__restrict__ r, int64
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// v[0..8) = the chunk's values, divided by s where given.
+// 1 / y of an fp16 value y, to 1 ulp: inside its range the plain instruction needs no scaling around it.
+__device__ __forceinline__ float rcp16(float y) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+    return r;
+}
+
+// v[0..8) = the chunk's values, divided by s where given (2 ulp: far below the fp16 rounding that follows).
 __device__ __forceinline__ void row_values(const uint4 &x, const uint16_t *__restrict__ s16, int64_t c, float (&v)[8]) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -69,9 +76,8 @@ __device__ __forceinline__ void row_values(const uint4 &x, const uint16_t *__res
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const __half2 h = *reinterpret_cast<const __half2 *>(&sw[e]);
-            // (2 ulp: far below the fp16 rounding that follows)
-            v[2 * e] = __fdividef(v[2 * e], __low2float(h));
-            v[2 * e + 1] = __fdividef(v[2 * e + 1], __high2float(h));
+            v[2 * e] *= rcp16(__low2float(h));
+            v[2 * e + 1] *= rcp16(__high2float(h));
         }
     }
 }
@@ -101,7 +107,8 @@ __device__ __forceinline__ float block_sum(float v, float *sm) {
 // Blocks from DMAX_PARTS on: one token each.  out[m] = fp16((row / s) * 2^-k), k from the row's largest
 // magnitude so that it lands in [2^14, 2^15); sx[m] = 2^k.  With dh: grow[m], an exponent
 // that bounds max |dh[m]| * ||row / s||.  The first blocks: the parts' largest |Delta|.
-__global__ void __launch_bounds__(512) rows16_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ s16,
+template <bool GROW>
+__global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ s16,
                                                      int64_t M, int64_t cols, int64_t ld,
                                                      const uint16_t *__restrict__ dh, int64_t F,
                                                      const uint16_t *__restrict__ scales, int64_t n_scales,
@@ -112,7 +119,7 @@ __global__ void __launch_bounds__(512) rows16_kernel(const uint16_t *__restrict_
         scales_max(scales, n_scales, static_cast<int>(blockIdx.x), dmax);
         return;
     }
-    __shared__ float sm[16];
+    __shared__ float sm[8];
     const int64_t m = blockIdx.x - DMAX_PARTS;
     const uint16_t *r = x + m * cols;
     const bool vec = cols % 8 == 0;
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(512) rows16_kernel(const uint16_t *__restrict_
 #pragma unroll
     for (int i = 0; i < KEEP; ++i) kept[i] = row_chunk(r, (i * T + threadIdx.x) * 8, cols, vec);
     float md = 0.0f;
-    if (grow) {                                       // the token's largest |dh|
+    if (GROW) {                                       // the token's largest |dh|
         const uint16_t *dr = dh + m * F;
         if (F % 8 == 0) {
             unsigned mb = 0u;                         // magnitudes of bf16 order as their bits
@@ -160,7 +167,7 @@ __global__ void __launch_bounds__(512) rows16_kernel(const uint16_t *__restrict_
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float lo = (permute ? v[e] : v[2 * e]) * sc, hi = (permute ? v[e + 4] : v[2 * e + 1]) * sc;
-            sq = fmaf(lo, lo, fmaf(hi, hi, sq));
+            if (GROW) sq = fmaf(lo, lo, fmaf(hi, hi, sq));
             const __half2 hv = __floats2half2_rn(lo, hi);
             h[e] = *reinterpret_cast<const uint32_t *>(&hv);
         }
@@ -174,7 +181,7 @@ __global__ void __launch_bounds__(512) rows16_kernel(const uint16_t *__restrict_
     }
     for (int64_t c = (KEEP * T + threadIdx.x) * 8; c < cols; c += T * 8) put(c, row_chunk(r, c, cols, vec));
     if (threadIdx.x == 0) sx[m] = ldexpf(1.0f, k);
-    if (grow) {
+    if (GROW) {
         sq = block_sum(sq, sm);
         md = block_max(md, sm);
         if (threadIdx.x == 0) {
@@ -265,10 +272,12 @@ cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t
 cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int64_t cols, int64_t ld,
                           const uint16_t *dh, int64_t F, const uint16_t *scales, int64_t n_scales, bool permute,
                           uint16_t *out, float *sx, int *grow, unsigned *dmax, cudaStream_t st) {
-    // a row up to 8192 wide stays in the registers of 256 threads, twice that in 512's
-    const int threads = cols <= 8192 ? 256 : 512;
-    rows16_kernel<<<static_cast<unsigned>(M + DMAX_PARTS), threads, 0, st>>>(x, s16, M, cols, ld, dh, F, scales, n_scales,
-                                                                        permute, out, sx, grow, dmax);
+    // Threads per row: few tokens are a matter of latency (77 rows of 4096: 3.1 us with 256 threads, 3.4 with
+    // 128), many of the instructions that each warp spends whatever its share (2048 rows of 4096: 14.9
+    // with 256, 12.6 with 128; of 13824: 25.5 with 256, 27.4 with 512).
+    const int threads = M > 512 && cols <= 4096 ? 128 : 256;
+    (grow ? rows16_kernel<true> : rows16_kernel<false>)<<<static_cast<unsigned>(M + DMAX_PARTS), threads, 0, st>>>(
+        x, s16, M, cols, ld, dh, F, scales, n_scales, permute, out, sx, grow, dmax);
     return cudaGetLastError();
 }
 
