@@ -135,6 +135,9 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 
 // ------------------------------------------------- programmatic dependent launch
+// What a kernel reads of the preceding one's results it reads after griddep_wait() and by __ldcg or a plain
+// load, not by __ldg, which tells the compiler that the memory holds the same throughout the kernel.
+//
 // Wait until the preceding kernel of the stream has completed and its memory is
 // visible (returns at once when the launch has no programmatic dependency).
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -142,6 +145,21 @@ __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wa
 // serialisation) to start its pre-wait part.
 __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launch a kernel that waits for the preceding one itself.
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t st, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 // Hint: bring [p, p + bytes) into L2 (bulk, asynchronous, no completion).  The

@@ -119,7 +119,7 @@ __device__ __forceinline__ void store_bf16_16(uint16_t *p, const float (&v)[16],
 
 __device__ __forceinline__ void epi_gated(const GemmArgs &a, uint32_t acc, int64_t row, int64_t f0, int par) {
     const int half = a.bn / 2;
-    const float sc = row < a.M ? __ldg(a.sx + row) : 0.0f;
+    const float sc = row < a.M ? __ldcg(a.sx + row) : 0.0f;
     const float sw = dq_scale(a.dmax);
     const bool vec = a.F % 8 == 0;
 #pragma unroll 1
@@ -142,11 +142,11 @@ __device__ __forceinline__ void epi_gated(const GemmArgs &a, uint32_t acc, int64
 __device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t f0, int par) {
     const int half = a.bn / 2;
     const bool ok = row < a.M;
-    const float sc = ok ? __ldg(a.sx + row) : 0.0f;
+    const float sc = ok ? __ldcg(a.sx + row) : 0.0f;
     const int kw = dq_exp(a.dmax);
     const float sw = ldexpf(1.0f, kw);
     // 2^-e of this token's gradients
-    const float sd = ok ? ldexpf(1.0f, -dgu_exp(__ldg(a.grow + row), a.inner, kw)) : 0.0f;
+    const float sd = ok ? ldexpf(1.0f, -dgu_exp(__ldcg(a.grow + row), a.inner, kw)) : 0.0f;
     const uint16_t *dh = a.dh + (ok ? row : 0) * a.F;
     const bool vec = a.F % 8 == 0;
 #pragma unroll 1
@@ -159,7 +159,7 @@ __device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, i
         float dv[16];
         if (vec && f0 + c + 16 <= a.F) {
             const uint4 *p = reinterpret_cast<const uint4 *>(dh + f0 + c);
-            const uint4 p0 = __ldg(p), p1 = __ldg(p + 1);
+            const uint4 p0 = __ldcg(p), p1 = __ldcg(p + 1);
             const uint32_t w[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -168,7 +168,7 @@ __device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, i
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) dv[k] = f0 + c + k < a.F ? bf16f(__ldg(dh + f0 + c + k)) : 0.0f;
+            for (int k = 0; k < 16; ++k) dv[k] = f0 + c + k < a.F ? bf16f(__ldcg(dh + f0 + c + k)) : 0.0f;
         }
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
@@ -219,10 +219,10 @@ __device__ __forceinline__ void out_scales(const GemmArgs &a, bool ok, int64_t r
     sc = sw = 1.0f;
     if (a.grow) {                                     // gated gradient: 2^e of the token
         const int kw = dq_exp(a.dmax);
-        sc = ok ? ldexpf(1.0f, dgu_exp(__ldg(a.grow + row), a.inner, kw)) : 0.0f;
+        sc = ok ? ldexpf(1.0f, dgu_exp(__ldcg(a.grow + row), a.inner, kw)) : 0.0f;
         sw = ldexpf(1.0f, kw);
     } else if (a.sx) {
-        sc = ok ? __ldg(a.sx + row) : 0.0f;
+        sc = ok ? __ldcg(a.sx + row) : 0.0f;
         sw = dq_scale(a.dmax);
     }
 }
@@ -233,7 +233,7 @@ __device__ __forceinline__ void out_columns(const GemmArgs &a, int64_t row, int6
     if (a.s16) {
 #pragma unroll
         for (int k = 0; k < C; k += 4) {
-            const uint2 sv = __ldg(reinterpret_cast<const uint2 *>(a.s16 + n + k));
+            const uint2 sv = __ldcg(reinterpret_cast<const uint2 *>(a.s16 + n + k));
             const __half2 s0 = *reinterpret_cast<const __half2 *>(&sv.x), s1 = *reinterpret_cast<const __half2 *>(&sv.y);
             v[k] = __fdividef(v[k], __low2float(s0));
             v[k + 1] = __fdividef(v[k + 1], __high2float(s0));
@@ -288,6 +288,8 @@ __device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t
 
 // Split tiles: block (tile, four columns), thread = row; the splits in order.
 __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant__ GemmArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
     const Tile tl = decode_tile(static_cast<int>(blockIdx.x), a.mt, a.nt);
     const int64_t row = static_cast<int64_t>(tl.m) * 256 + threadIdx.x;
     const int64_t n = static_cast<int64_t>(tl.n) * a.bn + blockIdx.y * 4;
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
     for (int i = 0; i < a.splits; ++i) {
-        const float4 w = __ldg(p + static_cast<int64_t>(i) * (a.bn / 4) * 256);
+        const float4 w = __ldcg(p + static_cast<int64_t>(i) * (a.bn / 4) * 256);
         v[0] += w.x;
         v[1] += w.y;
         v[2] += w.z;
@@ -332,7 +334,7 @@ __device__ __forceinline__ void ce_gather(uint32_t acc, int bn, int sub, float (
 __device__ __forceinline__ void epi_ce(const GemmArgs &a, float (&v)[CE_CHUNKS][16], int64_t row, int64_t n0, int slot,
                                        int sub) {
     if (row >= a.M) return;
-    const int64_t lab = __ldg(a.labels + row);
+    const int64_t lab = __ldcg(a.labels + row);
     float mx = -INFINITY, sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < CE_CHUNKS; ++i) {
@@ -391,7 +393,7 @@ __device__ __forceinline__ void epi_ce_t(const GemmArgs &a, float (&v)[CE_CHUNKS
         const int c = 16 * (sub + 2 * i);
         if (c < a.bn) {
             const int64_t m = c + (lane >> 1);        // the token this lane ends up with
-            const int64_t mine = m < a.N ? __ldg(a.labels + m) : -1;
+            const int64_t mine = m < a.N ? __ldcg(a.labels + m) : -1;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const int64_t lab = __shfl_sync(0xffffffffu, mine, 2 * k);
@@ -416,14 +418,14 @@ __device__ __forceinline__ void epi_ce_t(const GemmArgs &a, float (&v)[CE_CHUNKS
 __device__ __forceinline__ void ce_labels(const GemmArgs &a, int64_t tokens, int first, int step) {
     const int lane = threadIdx.x & 31;
     for (int64_t m = first; m < tokens; m += step) {
-        const int64_t lab = __ldg(a.labels + m);
+        const int64_t lab = __ldcg(a.labels + m);
         if (lab < 0 || lab >= a.V) continue;
         const uint4 *x = reinterpret_cast<const uint4 *>(a.x + m * a.inner);
         const uint4 *w = reinterpret_cast<const uint4 *>(a.w + lab * a.inner);
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll 4
         for (int i = lane; i < a.inner / 8; i += 32) {
-            const uint4 p = __ldg(x + i), q = __ldg(w + i);
+            const uint4 p = __ldcg(x + i), q = __ldcg(w + i);
             const uint32_t pv[4] = {p.x, p.y, p.z, p.w}, qv[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -440,10 +442,10 @@ __device__ __forceinline__ void ce_labels(const GemmArgs &a, int64_t tokens, int
 
 __device__ __forceinline__ void epi_ce_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int par) {
     const bool ok = row < a.M;
-    const int64_t lab = ok ? __ldg(a.labels + row) : -1;
+    const int64_t lab = ok ? __ldcg(a.labels + row) : -1;
     const bool scored = lab >= 0 && lab < a.V;
-    const float lse = ok ? __ldg(a.lse + row) : 0.0f;
-    const float w = ok ? __ldg(a.dloss + row) : 0.0f;
+    const float lse = ok ? __ldcg(a.lse + row) : 0.0f;
+    const float w = ok ? __ldcg(a.dloss + row) : 0.0f;
 #pragma unroll 1
     for (int c = 16 * par; c < a.bn; c += 32) {
         uint32_t r[16];
@@ -475,8 +477,8 @@ __device__ __forceinline__ void epi_ce_bwd_t(const GemmArgs &a, uint32_t acc, in
         // lane k holds token c + k's label, log-sum and weight
         const int64_t m = c + (lane & 15);
         const bool in = m < a.N;
-        const int64_t lab = in ? __ldg(a.labels + m) : -1;
-        const float lse = in ? __ldg(a.lse + m) : 0.0f, w = in ? __ldg(a.dloss + m) : 0.0f;
+        const int64_t lab = in ? __ldcg(a.labels + m) : -1;
+        const float lse = in ? __ldcg(a.lse + m) : 0.0f, w = in ? __ldcg(a.dloss + m) : 0.0f;
         const int rel = lab >= 0 && lab < a.V ? static_cast<int>(lab) : -1;   // V <= 2^24
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
@@ -504,6 +506,7 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
+    griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -538,6 +541,7 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
+    griddep_wait();                                   // the operands, scales and buffers of the kernels before
     // All 512 columns: the allocation starts at column 0, and a constant base keeps the MMAs' operands
     // in uniform registers.
     constexpr uint32_t tmem_base = 0;
@@ -700,11 +704,13 @@ cudaError_t launch_t(const GemmMaps &maps, const GemmArgs &a, int num_sms, cudaS
     cfg.blockDim = dim3(GM_THREADS<EPI>);
     cfg.dynamicSmemBytes = GM_SMEM;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     // Persistent: as many pairs as can be resident at once (one CTA per SM).
@@ -724,6 +730,7 @@ cudaError_t launch_t(const GemmMaps &maps, const GemmArgs &a, int num_sms, cudaS
     }
     const int tiles = a.mt * a.nt * a.splits;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, maps, a);
 }
 
@@ -779,8 +786,7 @@ cudaError_t launch_gemm16(int epi, bool bf16, bool a_mn, const GemmMaps &maps, c
                               : bf16 ? launch_t<EPI_OUT, true, false, true>(maps, a, num_sms, st)
                                      : launch_t<EPI_OUT, false, false, true>(maps, a, num_sms, st);
         if (e != cudaSuccess) return e;
-        gemm_finish_kernel<<<dim3(static_cast<unsigned>(a.mt * a.nt), static_cast<unsigned>(a.bn / 4)), 256, 0, st>>>(a);
-        return cudaGetLastError();
+        return launch_after(gemm_finish_kernel, dim3(static_cast<unsigned>(a.mt * a.nt), static_cast<unsigned>(a.bn / 4)), 256, st, a);
     }
     switch (epi) {
         case EPI_GATED: return launch_t<EPI_GATED, false, false, false>(maps, a, num_sms, st);
@@ -814,6 +820,7 @@ __global__ void __launch_bounds__(256) ce_final_kernel(const float2 *__restrict_
                                                        const int64_t *__restrict__ labels, int64_t V,
                                                        const float *__restrict__ tgt, float *__restrict__ loss,
                                                        float *__restrict__ lse) {
+    griddep_wait();
     __shared__ float2 sm[8][8];
     constexpr int T = ROWS ? 1 : 8;                   // tokens of the block
     const int tok = threadIdx.x % T, at = threadIdx.x / T;
@@ -822,7 +829,7 @@ __global__ void __launch_bounds__(256) ce_final_kernel(const float2 *__restrict_
     if (m < M) {
 #pragma unroll 4
         for (int t = at; t < n; t += 256 / T) {
-            const float2 p = __ldg(ROWS ? part + m * n + t : part + static_cast<int64_t>(t) * M + m);
+            const float2 p = __ldcg(ROWS ? part + m * n + t : part + static_cast<int64_t>(t) * M + m);
             join(mx, sum, p.x, p.y);
         }
     }
@@ -838,7 +845,7 @@ __global__ void __launch_bounds__(256) ce_final_kernel(const float2 *__restrict_
     sum = sm[0][tok].y;
 #pragma unroll
     for (int w = 1; w < 8; ++w) join(mx, sum, sm[w][tok].x, sm[w][tok].y);
-    const int64_t lab = __ldg(labels + m);
+    const int64_t lab = __ldcg(labels + m);
     if (lab < 0 || lab >= V) {
         lse[m] = mx + logf(sum);
         loss[m] = 0.0f;
@@ -846,7 +853,7 @@ __global__ void __launch_bounds__(256) ce_final_kernel(const float2 *__restrict_
     }
     // with the label's term t, which `part` leaves out: loss = log(1 + sum e^(mx - t)), written so
     // that neither a label far above the others nor one far below loses digits
-    const float t = __ldg(tgt + m), d = mx - t;
+    const float t = __ldcg(tgt + m), d = mx - t;
     const float l = d > 0.0f ? d + logf(sum + expf(-d)) : log1pf(sum * expf(d));
     loss[m] = l;
     lse[m] = t + l;
@@ -856,11 +863,9 @@ __global__ void __launch_bounds__(256) ce_final_kernel(const float2 *__restrict_
 
 cudaError_t launch_ce_final(const float2 *part, int n, bool rows, int64_t M, const int64_t *labels, int64_t V,
                             const float *tgt, float *loss, float *lse, cudaStream_t st) {
-    if (rows)
-        ce_final_kernel<true><<<static_cast<unsigned>(M), 256, 0, st>>>(part, n, M, labels, V, tgt, loss, lse);
-    else
-        ce_final_kernel<false><<<static_cast<unsigned>((M + 7) / 8), 256, 0, st>>>(part, n, M, labels, V, tgt, loss, lse);
-    return cudaGetLastError();
+    return rows ? launch_after(ce_final_kernel<true>, dim3(static_cast<unsigned>(M)), 256, st, part, n, M, labels, V, tgt, loss, lse)
+                : launch_after(ce_final_kernel<false>, dim3(static_cast<unsigned>((M + 7) / 8)), 256, st, part, n, M, labels, V,
+                               tgt, loss, lse);
 }
 
 }  // namespace awq

@@ -205,8 +205,10 @@ constexpr int DQ_ROWS = 2;
 __global__ void __launch_bounds__(256) dequant_kernel(const uint32_t *__restrict__ q,
                                                       const uint16_t *__restrict__ scales,
                                                       const uint32_t *__restrict__ zeros, int64_t O, int wpr, int lg,
-                                                      int nG, const unsigned *__restrict__ dmax,
+                                                      int nG, const unsigned *dmax,
                                                       uint16_t *__restrict__ out) {
+    griddep_launch_dependents();
+    griddep_wait();
     const float sw = ldexpf(1.0f, -dq_exp(dmax));
     const int nzw = (nG + 7) / 8;
     const int64_t o0 = static_cast<int64_t>(blockIdx.x) * DQ_ROWS;
@@ -252,6 +254,7 @@ __global__ void __launch_bounds__(256) dequant_kernel(const uint32_t *__restrict
 __global__ void __launch_bounds__(256) scored_rows_kernel(const uint4 *__restrict__ x,
                                                           const int64_t *__restrict__ labels, int64_t V, int64_t n,
                                                           int cpr, uint4 *__restrict__ out) {
+    griddep_launch_dependents();
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
         const int64_t lab = __ldg(labels + i / cpr);
@@ -284,9 +287,8 @@ cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int
 cudaError_t launch_dequant(const uint32_t *q, const uint16_t *scales, const uint32_t *zeros, int64_t O, int64_t I,
                            int gs, const unsigned *dmax, uint16_t *out, cudaStream_t st) {
     const int wpr = static_cast<int>(I / 8), threads = wpr < 256 ? (wpr + 31) / 32 * 32 : 256;
-    dequant_kernel<<<static_cast<unsigned>((O + DQ_ROWS - 1) / DQ_ROWS), threads, 0, st>>>(
-        q, scales, zeros, O, wpr, gs == 32 ? 5 : (gs == 64 ? 6 : 7), static_cast<int>(I / gs), dmax, out);
-    return cudaGetLastError();
+    return launch_after(dequant_kernel, dim3(static_cast<unsigned>((O + DQ_ROWS - 1) / DQ_ROWS)), threads, st, q, scales, zeros, O,
+                        wpr, gs == 32 ? 5 : (gs == 64 ? 6 : 7), static_cast<int>(I / gs), dmax, out);
 }
 
 }  // namespace awq

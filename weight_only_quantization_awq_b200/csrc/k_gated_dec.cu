@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(GD_THREADS, 1) gated_dec_kernel(const GdArgs a
                 for (int mb = 0; mb < a.M; mb += tpw) {
                     const int m = mb + (tpw == 2 ? lane >> 4 : 0);
                     const bool real = inside && m < a.M;
-                    const uint4 xv = real ? __ldg(reinterpret_cast<const uint4 *>(a.x + static_cast<int64_t>(m) * a.I) + w)
+                    const uint4 xv = real ? __ldcg(reinterpret_cast<const uint4 *>(a.x + static_cast<int64_t>(m) * a.I) + w)
                                           : make_uint4(0u, 0u, 0u, 0u);
                     const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
                     float v[8];

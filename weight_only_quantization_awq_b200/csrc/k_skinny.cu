@@ -126,7 +126,7 @@ __device__ __forceinline__ void sk_finish(const SkinnyArgs &a, int t, int m0, in
                 } else {
                     float da;
                     const float av = act_both(gv, a.act, da);
-                    const float dv = sk_bf16(__ldg(a.dh + (m0 + m) * a.F + f)) * tsd[m];
+                    const float dv = sk_bf16(__ldcg(a.dh + (m0 + m) * a.F + f)) * tsd[m];
                     uint16_t *dst = a.d16 + (m0 + m) * a.ldd + f;
                     dst[0] = __half_as_ushort(__float2half_rn((dv * uv) * da));
                     dst[a.F] = __half_as_ushort(__float2half_rn(dv * av));
@@ -140,8 +140,8 @@ __device__ __forceinline__ void sk_finish(const SkinnyArgs &a, int t, int m0, in
 // that EPI_GATED_BWD writes.
 template <bool GRAD, int EPI>
 __device__ __forceinline__ void sk_token_scale(const SkinnyArgs &a, int m, int kw, float &sc, float &sd) {
-    const int ex = a.grow ? dgu_exp(__ldg(a.grow + m), a.inner, kw) : 0;
-    sc = GRAD && a.grow ? ldexpf(1.0f, ex) : __ldg(a.sx + m);
+    const int ex = a.grow ? dgu_exp(__ldcg(a.grow + m), a.inner, kw) : 0;
+    sc = GRAD && a.grow ? ldexpf(1.0f, ex) : __ldcg(a.sx + m);
     sd = EPI == EPI_GATED_BWD ? ldexpf(1.0f, -ex) : 0.0f;
 }
 
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(128) skinny_finish_kernel(const __grid_constan
 #pragma unroll 8
     for (int ct = c0; ct <= c1; ++ct) {
         const float4 w =
-            __ldg(a.part + (static_cast<int64_t>(2 * ct + (sk_first(a, ct) > b0 ? 0 : 1)) * (a.n / 4) + blockIdx.y) * 128 + e);
+            __ldcg(a.part + (static_cast<int64_t>(2 * ct + (sk_first(a, ct) > b0 ? 0 : 1)) * (a.n / 4) + blockIdx.y) * 128 + e);
         v[0] += w.x;
         v[1] += w.y;
         v[2] += w.z;
@@ -555,10 +555,8 @@ cudaError_t launch_sk(const CUtensorMap &bmap, const SkinnyArgs &a, bool split, 
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kernel, bmap, a);
     if (e != cudaSuccess || !split) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.units / a.ks), static_cast<unsigned>(a.n / 4));
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, skinny_finish_kernel<GRAD, EPI>, a);
+    return launch_after(skinny_finish_kernel<GRAD, EPI>,
+                        dim3(static_cast<unsigned>(a.units / a.ks), static_cast<unsigned>(a.n / 4)), 128, st, a);
 }
 
 }  // namespace
