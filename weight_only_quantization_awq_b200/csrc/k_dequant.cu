@@ -44,12 +44,12 @@ __device__ __forceinline__ void scales_max(const uint16_t *__restrict__ scales, 
 // Row elements [c, c + 8) as bf16 bits, zeros past the end.
 __device__ __forceinline__ uint4 row_chunk(const uint16_t *__restrict__ r, int64_t c, int64_t cols, bool vec) {
     if (c >= cols) return make_uint4(0u, 0u, 0u, 0u);
-    if (vec) return __ldg(reinterpret_cast<const uint4 *>(r + c));
+    if (vec) return __ldcg(reinterpret_cast<const uint4 *>(r + c));
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = c + 2 * e < cols ? __ldg(r + c + 2 * e) : 0u;
-        const uint32_t hi = c + 2 * e + 1 < cols ? __ldg(r + c + 2 * e + 1) : 0u;
+        const uint32_t lo = c + 2 * e < cols ? __ldcg(r + c + 2 * e) : 0u;
+        const uint32_t hi = c + 2 * e + 1 < cols ? __ldcg(r + c + 2 * e + 1) : 0u;
         w[e] = lo | hi << 16;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -114,7 +114,10 @@ __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict_
                                                      const uint16_t *__restrict__ scales, int64_t n_scales,
                                                      bool permute, uint16_t *__restrict__ out, float *__restrict__ sx,
                                                      int *__restrict__ grow, unsigned *__restrict__ dmax) {
-    griddep_launch_dependents();                      // the products that follow wait for this kernel themselves
+    griddep_wait();
+    // The products that follow wait for this kernel themselves, but read their weights before: by now the
+    // kernel before this one, which may have written them, is done.
+    griddep_launch_dependents();
     if (blockIdx.x < DMAX_PARTS) {
         scales_max(scales, n_scales, static_cast<int>(blockIdx.x), dmax);
         return;
@@ -136,14 +139,14 @@ __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict_
             unsigned mb = 0u;                         // magnitudes of bf16 order as their bits
 #pragma unroll 4
             for (int64_t f = threadIdx.x; f < F / 8; f += T) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(dr) + f);
+                const uint4 q = __ldcg(reinterpret_cast<const uint4 *>(dr) + f);
                 mb = __vmaxu2(mb, __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu),
                                            __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
             }
             md = __uint_as_float(max(mb >> 16, mb & 0xFFFFu) << 16);
         } else {
             for (int64_t f = threadIdx.x; f < F; f += T)
-                md = fmaxf(md, fabsf(__uint_as_float(static_cast<uint32_t>(__ldg(dr + f)) << 16)));
+                md = fmaxf(md, fabsf(__uint_as_float(static_cast<uint32_t>(__ldcg(dr + f)) << 16)));
         }
     }
     auto largest = [&](int64_t c, const uint4 &x8) {
@@ -254,11 +257,12 @@ __global__ void __launch_bounds__(256) dequant_kernel(const uint32_t *__restrict
 __global__ void __launch_bounds__(256) scored_rows_kernel(const uint4 *__restrict__ x,
                                                           const int64_t *__restrict__ labels, int64_t V, int64_t n,
                                                           int cpr, uint4 *__restrict__ out) {
+    griddep_wait();
     griddep_launch_dependents();
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
-        const int64_t lab = __ldg(labels + i / cpr);
-        out[i] = lab >= 0 && lab < V ? __ldg(x + i) : make_uint4(0u, 0u, 0u, 0u);
+        const int64_t lab = __ldcg(labels + i / cpr);
+        out[i] = lab >= 0 && lab < V ? __ldcg(x + i) : make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
@@ -267,9 +271,8 @@ __global__ void __launch_bounds__(256) scored_rows_kernel(const uint4 *__restric
 cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t V, int64_t M, int64_t I,
                                uint16_t *out, int num_sms, cudaStream_t st) {
     const int64_t n = M * (I / 8), blocks = (n + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
-    scored_rows_kernel<<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, st>>>(
-        reinterpret_cast<const uint4 *>(x), labels, V, n, static_cast<int>(I / 8), reinterpret_cast<uint4 *>(out));
-    return cudaGetLastError();
+    return launch_after(scored_rows_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, st,
+                        reinterpret_cast<const uint4 *>(x), labels, V, n, static_cast<int>(I / 8), reinterpret_cast<uint4 *>(out));
 }
 
 cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int64_t cols, int64_t ld,
@@ -279,9 +282,8 @@ cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int
     // 128), many of the instructions that each warp spends whatever its share (2048 rows of 4096: 14.9
     // with 256, 12.6 with 128; of 13824: 25.5 with 256, 27.4 with 512).
     const int threads = M > 512 && cols <= 4096 ? 128 : 256;
-    (grow ? rows16_kernel<true> : rows16_kernel<false>)<<<static_cast<unsigned>(M + DMAX_PARTS), threads, 0, st>>>(
-        x, s16, M, cols, ld, dh, F, scales, n_scales, permute, out, sx, grow, dmax);
-    return cudaGetLastError();
+    return launch_after(grow ? rows16_kernel<true> : rows16_kernel<false>, dim3(static_cast<unsigned>(M + DMAX_PARTS)), threads,
+                        st, x, s16, M, cols, ld, dh, F, scales, n_scales, permute, out, sx, grow, dmax);
 }
 
 cudaError_t launch_dequant(const uint32_t *q, const uint16_t *scales, const uint32_t *zeros, int64_t O, int64_t I,

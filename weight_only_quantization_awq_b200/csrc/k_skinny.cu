@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
         place();
 #pragma unroll
         for (int u = 0; u < SK_PF; ++u) fetch(raw[u]);
-        // The packed weights are the caller's, complete before the kernel in front of this one began
-        // (it is launched in plain stream order); the exponent comes from that kernel.
+        // The packed weights are the caller's, complete before the kernel in front of this one let it
+        // start (rows16_kernel waits first); the exponent comes from that kernel.
         griddep_wait();
         const float dscale = ldexpf(1.0f, -dq_exp(a.dmax));
         const uint32_t P = 0x64006400u;
