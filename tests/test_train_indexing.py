@@ -52,22 +52,17 @@ def test_skinny_ranges_cover_every_stage_once(M, tiles, k):
                 assert slot not in slots.values() and slot < 2 * grid
                 slots[(T, c)] = slot
             u = end
-    assert seen == list(range(units))
+    assert seen == list(range(units)) and units * (grid + 1) < 2 ** 31
     # the second kernel finds exactly the CTAs that left partial sums
     for T in range(tiles * tt):
         b0, b1 = T * ks, (T + 1) * ks
-        c0 = b0 * grid // units
-        while c0 > 0 and first(units, grid, c0) > b0:
-            c0 -= 1
-        while first(units, grid, c0 + 1) <= b0:
-            c0 += 1
-        c1 = c0
-        while first(units, grid, c1 + 1) < b1:
-            c1 += 1
+        c0, c1 = (((u + 1) * grid - 1) // units for u in (b0, b1 - 1))
+        assert first(units, grid, c0) <= b0 < first(units, grid, c0 + 1)
+        assert first(units, grid, c1) <= b1 - 1 < first(units, grid, c1 + 1)
         own = [c for t, c in slots if t == T]
         assert own == ([] if c0 == c1 else list(range(c0, c1 + 1)))
         for c in own:
-            assert slots[(T, c)] == 2 * c + (0 if first(units, grid, c) > b0 else 1)
+            assert slots[(T, c)] == 2 * c + (1 if c == c0 else 0)
 
 
 @pytest.mark.parametrize("stages", [3, 4, 5])

@@ -87,9 +87,14 @@ __device__ __forceinline__ uint32_t sk_mul(uint32_t a, uint32_t b) {
 
 __device__ __forceinline__ float sk_bf16(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
 
-// First unit of CTA c's range.
+// First unit of CTA c's range, and the CTA whose range holds unit u: the largest c with
+// units c < (u + 1) grid.  (units (grid + 1) < 2^31, checked at the launch: a 64-bit division takes
+// several times as long, and the finishing kernel waits for it.)
 __device__ __forceinline__ int sk_first(const SkinnyArgs &a, int c) {
-    return static_cast<int>(static_cast<int64_t>(a.units) * c / a.grid);
+    return static_cast<int>(static_cast<uint32_t>(a.units) * static_cast<uint32_t>(c) / static_cast<uint32_t>(a.grid));
+}
+__device__ __forceinline__ int sk_owner(const SkinnyArgs &a, int u) {
+    return static_cast<int>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(a.grid) - 1u) / static_cast<uint32_t>(a.units));
 }
 
 // The results of K tokens (the tile's tokens c .. c + K - 1) from the accumulator's 128 lanes, thread e
@@ -153,11 +158,7 @@ __global__ void __launch_bounds__(128) skinny_finish_kernel(const __grid_constan
     griddep_wait();
     const int T = blockIdx.x, b0 = T * a.ks, b1 = b0 + a.ks;
     // the CTAs that share the tile, [c0, c1]: ranges cover the units in order
-    int c0 = static_cast<int>(static_cast<int64_t>(b0) * a.grid / a.units);
-    while (c0 > 0 && sk_first(a, c0) > b0) --c0;
-    while (sk_first(a, c0 + 1) <= b0) ++c0;
-    int c1 = c0;
-    while (sk_first(a, c1 + 1) < b1) ++c1;
+    const int c0 = sk_owner(a, b0), c1 = sk_owner(a, b1 - 1);
     if (c0 == c1) return;                             // one CTA's own: done
     const int e = threadIdx.x, c = blockIdx.y * 4;
     const int tt = T / a.tiles, t = T - tt * a.tiles, m0 = tt * a.n;
@@ -172,10 +173,11 @@ __global__ void __launch_bounds__(128) skinny_finish_kernel(const __grid_constan
     }
     __syncthreads();
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    // their slots: the first CTA's range began with or before the tile, the others' inside it
+    const float4 *p = a.part + (static_cast<int64_t>(2 * c0 + 1) * (a.n / 4) + blockIdx.y) * 128 + e;
 #pragma unroll 8
     for (int ct = c0; ct <= c1; ++ct) {
-        const float4 w =
-            __ldcg(a.part + (static_cast<int64_t>(2 * ct + (sk_first(a, ct) > b0 ? 0 : 1)) * (a.n / 4) + blockIdx.y) * 128 + e);
+        const float4 w = __ldcg(p + static_cast<int64_t>(2 * (ct - c0) - (ct > c0 ? 1 : 0)) * (a.n / 4) * 128);
         v[0] += w.x;
         v[1] += w.y;
         v[2] += w.z;
@@ -598,7 +600,7 @@ cudaError_t launch_skinny(bool grad, int epi, const CUtensorMap &bmap, SkinnyArg
     a.acc_cols = p.n <= 32 ? 32 : p.n <= 64 ? 64 : p.n <= 128 ? 128 : 256;
     const int fit = (232448 - 1024 - SK_TAIL) / (SK_A_BYTES + p.n * 256);
     a.stages = fit < SK_MAX_STAGES ? fit : SK_MAX_STAGES;
-    if (a.stages < SK_GROUPS) return cudaErrorInvalidConfiguration;
+    if (a.stages < SK_GROUPS || static_cast<int64_t>(a.units) * (p.grid + 1) > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (grad) return launch_sk<true, EPI_OUT>(bmap, a, split, st);
     return epi == EPI_GATED ? launch_sk<false, EPI_GATED>(bmap, a, split, st)
                             : launch_sk<false, EPI_GATED_BWD>(bmap, a, split, st);
