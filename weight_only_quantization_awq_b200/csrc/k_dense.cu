@@ -293,18 +293,29 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
     const Tile tl = decode_tile(static_cast<int>(blockIdx.x), a.mt, a.nt);
     const int64_t row = static_cast<int64_t>(tl.m) * 256 + threadIdx.x;
     const int64_t n = static_cast<int64_t>(tl.n) * a.bn + blockIdx.y * 4;
+    const bool ok = row < a.M && n < a.N;
+    const float4 *p = a.part4 + (static_cast<int64_t>(blockIdx.x) * a.splits * (a.bn / 4) + blockIdx.y) * 256 + threadIdx.x;
+    // the first partial sums are asked for before the scales: the kernel is as long as its chain of reads
+    constexpr int AHEAD = 8;
+    float4 w[AHEAD];
+    auto slot = [&](int i) { return __ldcg(p + static_cast<int64_t>(i) * (a.bn / 4) * 256); };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) w[i] = ok && i < a.splits ? slot(i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float sc, sw;
     out_scales(a, row < a.M, row, sc, sw);
-    if (row >= a.M || n >= a.N) return;
-    const float4 *p = a.part4 + (static_cast<int64_t>(blockIdx.x) * a.splits * (a.bn / 4) + blockIdx.y) * 256 + threadIdx.x;
+    if (!ok) return;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-    for (int i = 0; i < a.splits; ++i) {
-        const float4 w = __ldcg(p + static_cast<int64_t>(i) * (a.bn / 4) * 256);
-        v[0] += w.x;
-        v[1] += w.y;
-        v[2] += w.z;
-        v[3] += w.w;
+    for (int i0 = 0; i0 < a.splits; i0 += AHEAD) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            v[0] += w[i].x;
+            v[1] += w[i].y;
+            v[2] += w[i].z;
+            v[3] += w[i].w;
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            w[i] = i0 + AHEAD + i < a.splits ? slot(i0 + AHEAD + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = (v[k] * sc) * sw;

@@ -97,16 +97,39 @@ __device__ __forceinline__ int sk_owner(const SkinnyArgs &a, int u) {
     return static_cast<int>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(a.grid) - 1u) / static_cast<uint32_t>(a.units));
 }
 
+// What thread e reads of the caller's tensors for K tokens' results: its column's s, or its tokens' dh.
+template <int EPI, int K>
+struct SkPre {
+    uint16_t s, dh[K / 2];
+};
+template <int EPI, int K>
+__device__ __forceinline__ SkPre<EPI, K> sk_pre(const SkinnyArgs &a, int t, int m0, int mcount, int c, int e) {
+    SkPre<EPI, K> p;
+    if (EPI == EPI_OUT) {
+        const int64_t col = static_cast<int64_t>(t) * 128 + (e & ~7) + frag_perm8(e & 7);
+        p.s = a.s16 && col < a.I ? __ldg(a.s16 + col) : 0x3C00;     // 1.0
+    }
+    if (EPI == EPI_GATED_BWD) {
+        const int64_t f = static_cast<int64_t>(t) * 64 + (e & 63);
+#pragma unroll
+        for (int k2 = 0; k2 < K / 2; ++k2) {
+            const int m = c + (e >> 6) * (K / 2) + k2;
+            p.dh[k2] = f < a.F && m < mcount ? __ldcg(a.dh + (m0 + m) * a.F + f) : 0;
+        }
+    }
+    return p;
+}
+
 // The results of K tokens (the tile's tokens c .. c + K - 1) from the accumulator's 128 lanes, thread e
 // holding lane e's values.  tsc, tsd: the tile's token scales.  bar: hardware barrier of the 128 threads.
 // x: [K][128] floats of shared memory (gated products: lanes 64-127 hold the up values of lanes 0-63).
 template <int EPI, int K>
 __device__ __forceinline__ void sk_finish(const SkinnyArgs &a, int t, int m0, int mcount, int c, const float (&v)[K],
-                                          int e, float sw, const float *tsc, const float *tsd, float *x, int bar) {
+                                          const SkPre<EPI, K> &pre, int e, float sw, const float *tsc, const float *tsd, float *x, int bar) {
     if (EPI == EPI_OUT) {
         const int64_t col = static_cast<int64_t>(t) * 128 + (e & ~7) + frag_perm8(e & 7);
         if (col < a.I) {
-            const float s = a.s16 ? __half2float(__ushort_as_half(__ldg(a.s16 + col))) : 1.0f;
+            const float s = __half2float(__ushort_as_half(pre.s));
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 if (c + k < mcount)
@@ -131,7 +154,7 @@ __device__ __forceinline__ void sk_finish(const SkinnyArgs &a, int t, int m0, in
                 } else {
                     float da;
                     const float av = act_both(gv, a.act, da);
-                    const float dv = sk_bf16(__ldcg(a.dh + (m0 + m) * a.F + f)) * tsd[m];
+                    const float dv = sk_bf16(pre.dh[k2]) * tsd[m];
                     uint16_t *dst = a.d16 + (m0 + m) * a.ldd + f;
                     dst[0] = __half_as_ushort(__float2half_rn((dv * uv) * da));
                     dst[a.F] = __half_as_ushort(__float2half_rn(dv * av));
@@ -164,6 +187,17 @@ __global__ void __launch_bounds__(128) skinny_finish_kernel(const __grid_constan
     const int tt = T / a.tiles, t = T - tt * a.tiles, m0 = tt * a.n;
     const int mcount = static_cast<int>(a.M - m0 < a.n ? a.M - m0 : a.n);
     if (c >= mcount) return;
+    // Everything is asked for before anything is used: the kernel is as long as its chain of reads.
+    const SkPre<EPI, 4> pre = sk_pre<EPI, 4>(a, t, m0, mcount, c, e);
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    // their slots: the first CTA's range began with or before the tile, the others' inside it
+    const float4 *p = a.part + (static_cast<int64_t>(2 * c0 + 1) * (a.n / 4) + blockIdx.y) * 128 + e;
+    constexpr int AHEAD = 4;
+    float4 w[AHEAD];
+    const int n = c1 - c0 + 1;
+    auto slot = [&](int i) { return __ldcg(p + static_cast<int64_t>(2 * i - (i > 0 ? 1 : 0)) * (a.n / 4) * 128); };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) w[i] = i < n ? slot(i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const int kw = dq_exp(a.dmax);
     if (e < 4) {
         float sc = 0.0f, sd = 0.0f;
@@ -171,19 +205,20 @@ __global__ void __launch_bounds__(128) skinny_finish_kernel(const __grid_constan
         tsc[e] = sc;
         tsd[e] = sd;
     }
-    __syncthreads();
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    // their slots: the first CTA's range began with or before the tile, the others' inside it
-    const float4 *p = a.part + (static_cast<int64_t>(2 * c0 + 1) * (a.n / 4) + blockIdx.y) * 128 + e;
-#pragma unroll 8
-    for (int ct = c0; ct <= c1; ++ct) {
-        const float4 w = __ldcg(p + static_cast<int64_t>(2 * (ct - c0) - (ct > c0 ? 1 : 0)) * (a.n / 4) * 128);
-        v[0] += w.x;
-        v[1] += w.y;
-        v[2] += w.z;
-        v[3] += w.w;
+    for (int i0 = 0; i0 < n; i0 += AHEAD) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            v[0] += w[i].x;
+            v[1] += w[i].y;
+            v[2] += w[i].z;
+            v[3] += w[i].w;
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            w[i] = i0 + AHEAD + i < n ? slot(i0 + AHEAD + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    sk_finish<EPI, 4>(a, t, m0, mcount, c, v, e, ldexpf(1.0f, kw), tsc - c, tsd - c, x, 0);
+    __syncthreads();
+    sk_finish<EPI, 4>(a, t, m0, mcount, c, v, pre, e, ldexpf(1.0f, kw), tsc - c, tsd - c, x, 0);
 }
 
 // WHOLE: no tile is shared, and the last tile's results are shared out among the sets of warps.
@@ -395,12 +430,13 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
                                      (static_cast<uint32_t>(T - u0 / a.ks) & 1u) * a.acc_cols;
                 uint32_t flip = 0;
                 for (int c = 16 * set; c < a.n; c += 16 * SK_SETS, flip ^= 1u) {
+                    const SkPre<EPI, 16> pre = sk_pre<EPI, 16>(a, t, m0, mcount, c, e);
                     uint32_t rv[16];
                     tmem_ld16_wait(acc + c, rv);
                     float v[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(rv[k]);
-                    sk_finish<EPI, 16>(a, t, m0, mcount, c, v, e, ldexpf(1.0f, kw), ss, ss + 256, xs + flip * (16 * 128), 1 + set);
+                    sk_finish<EPI, 16>(a, t, m0, mcount, c, v, pre, e, ldexpf(1.0f, kw), ss, ss + 256, xs + flip * (16 * 128), 1 + set);
                     __syncwarp();
                 }
             }
@@ -509,7 +545,7 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
 #pragma unroll
                 for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(rv[k]);
                 if (whole) {
-                    sk_finish<EPI, 16>(a, t, m0, mcount, c, v, e, sw, tsc, tsd, xbuf + flip * (16 * 128), 1);
+                    sk_finish<EPI, 16>(a, t, m0, mcount, c, v, sk_pre<EPI, 16>(a, t, m0, mcount, c, e), e, sw, tsc, tsd, xbuf + flip * (16 * 128), 1);
                     flip ^= 1u;
                 } else {
 #pragma unroll
