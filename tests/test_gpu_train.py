@@ -266,7 +266,7 @@ def every_call(awq, M, seed=7):
 
 
 # tokens of every path: decode, dequantised on the way (one and several token tiles), dense
-PATHS = [1, 11, 40, 200, 400]
+PATHS = [1, 11, 40, 130, 200, 400]
 
 
 @pytest.mark.parametrize("M", PATHS)

@@ -277,10 +277,11 @@ struct SkinnyPlan {
     int64_t part_vecs;          // workspace: fp32 partial sums, by four
 };
 // Up to how many tokens, and below 4 GB of codes; above, the weights are dequantised once for dense
-// products.  Measured (us a call, this way against dense): 22016 x 4096 gated 320 tokens 118 / 124, 384
-// 129 / 125; its gradient, whose two products share the dequantised weights, 256 tokens 183 / 185, 320
-// 244 / 210; 4096 x 11008 gradient 320 tokens 75 / 77, 448 89 / 78.
-constexpr int64_t SKINNY_MAX_M = 352, SKINNY_MAX_M_GATED_GRAD = 256;
+// products: two tiles of 144 tokens, one for the gradient of the gated product, whose two dense products share the
+// dequantised weights.  Measured (us a call, this way / dense): 22016 x 4096 gated 144 tokens 54 / 89, 288
+// 90 / 114, 304 127 / 125; its gradient 144 tokens 106 / 136, 208 158 / 142; 4096 x 11008 gradient 144 tokens 36 /
+// 52, 208 56 / 54, 288 65 / 75, 304 91 / 79; 5504 x 2048 gradient 250 tokens 22 / 28.
+constexpr int64_t SKINNY_MAX_M = 288, SKINNY_MAX_M_GATED_GRAD = 144;
 inline bool skinny_supported(int64_t M, int64_t most, int64_t O, int64_t I) { return M <= most && O * I <= int64_t(1) << 32; }
 SkinnyPlan skinny_plan(int64_t M, int64_t tiles, int64_t k, int num_sms);
 struct SkinnyArgs {
