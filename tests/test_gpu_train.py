@@ -242,6 +242,37 @@ def test_cross_entropy_grad(awq, M, V, I, want_dw):
         within(dW, dW_r, e + UBF * (dW_r.abs() + e) + 1e-38, "dW")
 
 
+@pytest.mark.parametrize("M", [1, 3, 64, 100, 130])
+def test_cross_entropy_grad_of_a_label_is_not_rounded(awq, M):
+    """The label's term makes up most of a row of dx (and, for few tokens, of dW).  With a gradient half way
+    between two bf16 numbers its rounding alone would be off by 2^-8 of it, as much as the result's own."""
+    V, I = 3000, 256
+    x, W, labels = ce_case(M, V, I, M)
+    labels[:] = torch.arange(M, device="cuda") * 7
+    x *= 2.0 ** -10
+    W[labels] *= 64
+    _, lse = awq.awq_cross_entropy(x, W, labels)
+    x8, W8, rows = x.to(F8), W.to(F8), torch.arange(M, device="cuda")
+    l = x8 @ W8.T
+    el = acc(I) * (x8.abs() @ W8.abs().T) + 2.0 ** -21 * (1 + l.abs() + lse.to(F8).abs()[:, None])
+    p = torch.exp(l - lse.to(F8)[:, None])
+    dloss = ((1 + 2.0 ** -8) / (1 - p[rows, labels])).float()
+    dx, dW = awq.awq_cross_entropy_grad(x, W, labels, lse, dloss)
+    wgt = dloss.to(F8)[:, None]
+    ep = p * el * 1.01
+    p[rows, labels] -= 1.0
+    d, ed = p * wgt, ep * wgt.abs() + 2.0 ** -23 * (p * wgt).abs()     # before any rounding to 16 bits
+    off = torch.ones_like(d)
+    off[rows, labels] = 0.0
+    dx_r = d @ W8
+    e = (ed + UBF * off * d.abs()) @ W8.abs() + acc(V + 4096) * (d.abs() @ W8.abs())
+    within(dx, dx_r, e + UBF * (dx_r.abs() + e) + 1e-38, "dx")
+    dW_r = d.T @ x8
+    u = UBF * UBF if M <= 128 else UBF                 # two bf16 numbers, or one
+    e = (ed + u * d.abs()).T @ x8.abs() + acc(2 * M) * 2 * (d.abs().T @ x8.abs())
+    within(dW, dW_r, e + UBF * (dW_r.abs() + e) + 1e-38, "dW")
+
+
 # ------------------------------------------------------------------ what the formulas leave open
 def ffn(seed, M=40, I=256, F=320, gs=64):
     w, D, s = packed(2 * F, I, gs, True, True, seed)

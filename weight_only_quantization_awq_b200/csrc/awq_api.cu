@@ -1145,21 +1145,23 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
     vc = ((V + pieces - 1) / pieces + 255) / 256 * 256;
     const int64_t ldd = vc < round64(V) ? vc : round64(V);
     Workspace ws(st);
-    size_t bytes = Workspace::up(2 * M * ldd);
+    const int64_t dr = dW && M <= awq::CE_LO_MAX_M ? 2 * M : M;   // rows of d and of x in the head's gradient
+    size_t bytes = Workspace::up(2 * dr * ldd) + Workspace::up(4 * M);
     if (pieces > 1) bytes += Workspace::up(4 * M * in);
-    if (dW) bytes += Workspace::up(2 * M * in);
+    if (dW) bytes += Workspace::up(2 * dr * in);
     const awq::GemmPlan gp = awq::gemm_plan(M, in, vc < V ? vc : V, sms);   // dx: K is the piece's entries
     const int64_t parts = gp.part_vecs;
     const bool few = M <= awq::CE_BWD_T_MAX_M;            // the vocabulary on the rows, the tokens on the columns
     bytes += Workspace::up(16 * parts);
     if (awq_status_t s = ws.reserve(bytes)) return s;
-    uint16_t *d16 = ws.take<uint16_t>(M * ldd);
+    uint16_t *d16 = ws.take<uint16_t>(dr * ldd);
+    float *res = ws.take<float>(M);
     float4 *part4 = parts ? ws.take<float4>(parts) : nullptr;
     float *acc = pieces > 1 ? ws.take<float>(M * in) : nullptr;
     uint16_t *xz = nullptr;
     if (dW) {
-        xz = ws.take<uint16_t>(M * in);
-        AWQ_CUDA(awq::launch_scored_rows(x, labels, V, M, in, xz, sms, st));
+        xz = ws.take<uint16_t>(dr * in);
+        AWQ_CUDA(awq::launch_scored_rows(x, labels, V, M, in, static_cast<int>(dr / M), xz, sms, st));
     }
     kt_reset(4);
     kt_begin(4, st);
@@ -1182,6 +1184,8 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
         a.dloss = dloss;
         a.d16 = d16;
         a.ldd = ldd;
+        a.res = res;
+        a.lo = dr - M;
         if (awq_status_t s = map_kmajor(&maps.a, true, few ? Wp : x, in, a.M, in, 128)) return s;
         if (awq_status_t s = map_kmajor(&maps.b, true, few ? x : Wp, in, a.N, in, a.bn / 2)) return s;
         AWQ_CUDA(awq::launch_gemm16(few ? awq::EPI_CE_BWD_T : awq::EPI_CE_BWD, true, false, maps, a, sms, st));
@@ -1200,6 +1204,10 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
         b.acc = acc;
         b.first = v0 == 0;
         b.last = v0 + vc >= V;
+        b.labels = labels;
+        b.V = V;
+        b.w = W;
+        b.res = res;
         if (awq_status_t s = map_kmajor(&maps.a, true, d16, n, M, ldd, 128)) return s;
         if (awq_status_t s = map_mnmajor(&maps.b, true, Wp, in, n, in)) return s;
         AWQ_CUDA(awq::launch_gemm16(awq::EPI_OUT, true, false, maps, b, sms, st));
@@ -1211,10 +1219,10 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
             c.bn = awq::gemm_tile_cols(n, in, sms);
             c.mt = ceil_div(n, 256);
             c.nt = ceil_div(in, c.bn);
-            c.nk[0] = ceil_div(M, 64);
+            c.nk[0] = ceil_div(dr, 64);
             c.out = dW + v0 * in;
-            if (awq_status_t s = map_mnmajor(&maps.a, true, d16, n, M, ldd)) return s;
-            if (awq_status_t s = map_mnmajor(&maps.b, true, xz, in, M, in)) return s;
+            if (awq_status_t s = map_mnmajor(&maps.a, true, d16, n, dr, ldd)) return s;
+            if (awq_status_t s = map_mnmajor(&maps.b, true, xz, in, dr, in)) return s;
             AWQ_CUDA(awq::launch_gemm16(awq::EPI_OUT, true, true, maps, c, sms, st));
         }
     }

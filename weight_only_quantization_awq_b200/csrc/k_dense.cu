@@ -227,9 +227,27 @@ __device__ __forceinline__ void out_scales(const GemmArgs &a, bool ok, int64_t r
     }
 }
 
+// A token's label row of the head and the remainder of its label's gradient, which is a row of dx's largest term: left
+// out, its rounding error would be common to the whole row.
+struct LabelTerm {
+    const uint16_t *w;                                // null: none
+    float r;
+};
+__device__ __forceinline__ LabelTerm label_term(const GemmArgs &a, bool ok, int64_t row) {
+    LabelTerm t = {nullptr, 0.0f};
+    if (a.res && a.last && ok) {
+        const int64_t lab = __ldcg(a.labels + row);
+        if (lab >= 0 && lab < a.V) {
+            t.w = a.w + lab * a.N;
+            t.r = __ldcg(a.res + row);
+        }
+    }
+    return t;
+}
+
 // C consecutive scaled columns n .. of a row: divided by s, added to the pieces before, stored.
 template <int C>
-__device__ __forceinline__ void out_columns(const GemmArgs &a, int64_t row, int64_t n, float (&v)[C]) {
+__device__ __forceinline__ void out_columns(const GemmArgs &a, int64_t row, int64_t n, const LabelTerm &t, float (&v)[C]) {
     if (a.s16) {
 #pragma unroll
         for (int k = 0; k < C; k += 4) {
@@ -256,6 +274,16 @@ __device__ __forceinline__ void out_columns(const GemmArgs &a, int64_t row, int6
             return;
         }
     }
+    if (t.w && t.r != 0.0f) {
+#pragma unroll
+        for (int k = 0; k < C; k += 4) {
+            const uint2 w = __ldcg(reinterpret_cast<const uint2 *>(t.w + n + k));
+            v[k] = fmaf(t.r, __uint_as_float(w.x << 16), v[k]);
+            v[k + 1] = fmaf(t.r, __uint_as_float(w.x & 0xFFFF0000u), v[k + 1]);
+            v[k + 2] = fmaf(t.r, __uint_as_float(w.y << 16), v[k + 2]);
+            v[k + 3] = fmaf(t.r, __uint_as_float(w.y & 0xFFFF0000u), v[k + 3]);
+        }
+    }
     uint2 *o = reinterpret_cast<uint2 *>(a.out + row * a.N + n);
     if constexpr (C % 8 == 0) {
 #pragma unroll
@@ -272,6 +300,7 @@ __device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t
     const bool ok = row < a.M;
     float sc, sw;
     out_scales(a, ok, row, sc, sw);
+    const LabelTerm t = label_term(a, ok, row);
 #pragma unroll 1
     for (int c = 16 * par; c < a.bn; c += 32) {
         uint32_t r[16];
@@ -280,7 +309,7 @@ __device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t
             float v[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = (__uint_as_float(r[k]) * sc) * sw;
-            out_columns<16>(a, row, n0 + c, v);
+            out_columns<16>(a, row, n0 + c, t, v);
         }
         __syncwarp();
     }
@@ -304,6 +333,7 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
     float sc, sw;
     out_scales(a, row < a.M, row, sc, sw);
     if (!ok) return;
+    const LabelTerm t = label_term(a, true, row);
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int i0 = 0; i0 < a.splits; i0 += AHEAD) {
 #pragma unroll
@@ -319,7 +349,7 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = (v[k] * sc) * sw;
-    out_columns<4>(a, row, n, v);
+    out_columns<4>(a, row, n, t, v);
 }
 
 constexpr float LOG2E = 1.4426950408889634f;
@@ -451,6 +481,9 @@ __device__ __forceinline__ void ce_labels(const GemmArgs &a, int64_t tokens, int
     }
 }
 
+// What rounding to bf16 takes off v (exact).
+__device__ __forceinline__ float bf16_rest(float v) { return v - __bfloat162float(__float2bfloat16_rn(v)); }
+
 __device__ __forceinline__ void epi_ce_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int par) {
     const bool ok = row < a.M;
     const int64_t lab = ok ? __ldcg(a.labels + row) : -1;
@@ -469,9 +502,15 @@ __device__ __forceinline__ void epi_ce_bwd(const GemmArgs &a, uint32_t acc, int6
             float p = exp2f((__uint_as_float(r[k]) - lse) * LOG2E);
             if (j == k) p -= 1.0f;
             v[k] = scored ? p * w : 0.0f;
+            if (scored && j == k) a.res[row] = bf16_rest(v[k]);
         }
         // the row stride is a multiple of 64: the store may run into the row's own padding
         store_bf16_16(a.d16 + row * a.ldd + n0 + c, v, true, 16);
+        if (a.lo) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = bf16_rest(v[k]);
+            store_bf16_16(a.d16 + (a.lo + row) * a.ldd + n0 + c, v, true, 16);
+        }
         }
         __syncwarp();
     }
@@ -496,9 +535,14 @@ __device__ __forceinline__ void epi_ce_bwd_t(const GemmArgs &a, uint32_t acc, in
             const int lk = __shfl_sync(0xffffffffu, rel, k);
             const float sk = __shfl_sync(0xffffffffu, lse, k), wk = __shfl_sync(0xffffffffu, w, k);
             float p = exp2f((__uint_as_float(r[k]) - sk) * LOG2E);
-            if (lk == a.v0 + row) p -= 1.0f;
-            if (row < a.M && c + k < a.N)
-                a.d16[(c + k) * a.ldd + row] = __bfloat16_as_ushort(__float2bfloat16_rn(lk >= 0 ? p * wk : 0.0f));
+            const bool label = lk == a.v0 + row;      // (lk = -1: not a row)
+            if (label) p -= 1.0f;
+            if (row < a.M && c + k < a.N) {
+                const float d = lk >= 0 ? p * wk : 0.0f;
+                a.d16[(c + k) * a.ldd + row] = __bfloat16_as_ushort(__float2bfloat16_rn(d));
+                if (label) a.res[c + k] = bf16_rest(d);
+                if (a.lo) a.d16[(a.lo + c + k) * a.ldd + row] = __bfloat16_as_ushort(__float2bfloat16_rn(bf16_rest(d)));
+            }
         }
     }
 }

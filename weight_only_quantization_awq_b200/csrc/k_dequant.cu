@@ -252,27 +252,29 @@ __global__ void __launch_bounds__(256) dequant_kernel(const uint32_t *__restrict
     }
 }
 
-// out[m] = x[m] where the label is scored, zeros elsewhere: an unscored row adds nothing to the
+// out[m] = x[m] where the label is scored, zeros elsewhere, `copies` times over: an unscored row adds nothing to the
 // head's gradient, whatever (NaN, inf) its activations hold.
 __global__ void __launch_bounds__(256) scored_rows_kernel(const uint4 *__restrict__ x,
                                                           const int64_t *__restrict__ labels, int64_t V, int64_t n,
-                                                          int cpr, uint4 *__restrict__ out) {
+                                                          int cpr, int copies, uint4 *__restrict__ out) {
     griddep_wait();
     griddep_launch_dependents();
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
         const int64_t lab = __ldcg(labels + i / cpr);
-        out[i] = lab >= 0 && lab < V ? __ldcg(x + i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = lab >= 0 && lab < V ? __ldcg(x + i) : make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < copies; ++k) out[k * n + i] = v;
     }
 }
 
 }  // namespace
 
 cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t V, int64_t M, int64_t I,
-                               uint16_t *out, int num_sms, cudaStream_t st) {
+                               int copies, uint16_t *out, int num_sms, cudaStream_t st) {
     const int64_t n = M * (I / 8), blocks = (n + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
     return launch_after(scored_rows_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, st,
-                        reinterpret_cast<const uint4 *>(x), labels, V, n, static_cast<int>(I / 8), reinterpret_cast<uint4 *>(out));
+                        reinterpret_cast<const uint4 *>(x), labels, V, n, static_cast<int>(I / 8), copies,
+                        reinterpret_cast<uint4 *>(out));
 }
 
 cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int64_t cols, int64_t ld,
