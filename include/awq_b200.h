@@ -275,7 +275,17 @@ awq_status_t awq_linear_w4a16_batch(const awq_linear_desc_t *descs, int n, int64
  * Storage arguments as awq_linear_w4a16 with out = 2F; any F >= 1, M <= 2^20,
  * in <= 49152.  g and u are held in fp32 and rounded nowhere before h.
  * Precision of the operands: x / s16 is rounded to fp16 after a power-of-two
- * scale per token, (code - z) * scale once to fp16 after one per layer.
+ * scale (M <= 16: one per token and group; above: one per token).  M <= 16: the
+ * integer codes are exact, (code - z) * scale is applied in fp32 per group.
+ * M >= 17: (code - z) * scale is rounded once to fp16 after a power-of-two scale
+ * per layer.  Accumulation in fp32.
+ * M <= 16, while the staged activations and two tiles' scales fit one SM's shared
+ * memory: one launch streaming the codes.  Up to 288 tokens the weights are dequantised on their
+ * way into the tensor cores, above once into a temporary fp16 matrix of 4 F in bytes.
+ * Ordering, for this and the four calls below: their kernels are launched with
+ * programmatic stream serialisation.  Until the preceding kernel on `stream` has
+ * completed they read no argument and write nothing (M <= 16: they ask L2 to
+ * prefetch weights).
  * h must not overlap any input.  Asynchronous.
  */
 typedef enum { AWQ_ACT_SILU = 0, AWQ_ACT_GELU = 1, AWQ_ACT_GELU_TANH = 2 } awq_act_t;
@@ -290,8 +300,9 @@ awq_status_t awq_gated_w4a16(const uint16_t *x, int64_t M, int64_t in, int64_t F
  * packed weights frozen.  g and u are computed again from x, then
  *     dg = dh * u * act'(g),  du = dh * act(g),  dx = ([dg | du] * dequant(W)) / s16.
  * dh : [M, F] bf16 device;  dx : [M, in] bf16 device, written.  Other arguments as
- * awq_gated_w4a16.  dg and du are rounded to fp16 after a power-of-two scale per
- * token.  A token's gradient depends on that token's rows alone.
+ * awq_gated_w4a16 at M >= 17 (here for any M; the weights are dequantised on their
+ * way up to 144 tokens).  dg and du are rounded to fp16 after a power-of-two scale
+ * per token.  A token's gradient depends on that token's rows alone.
  * dx must not overlap any input.  Asynchronous.
  */
 awq_status_t awq_gated_w4a16_grad(const uint16_t *dh, const uint16_t *x, int64_t M, int64_t in,
@@ -321,7 +332,9 @@ awq_status_t awq_linear_w4a16_grad(const uint16_t *dy, int64_t M, int64_t in, in
  * A label outside [0, V) (e.g. -100) marks a token that is not scored: loss[m] = 0.
  * x : [M, in] bf16, W : [V, in] bf16, labels : [M] int64, loss and lse : [M] fp32
  * written; all device.  in % 64 == 0, in <= 49152, any V in [1, 2^24], M <= 2^20.
- * Products are exact, sums fp32.  Asynchronous.
+ * Products are exact; logits are accumulated in fp32, 1024 columns at a time on the
+ * tensor cores, the label's on the CUDA cores; maxima and sums of exponentials in
+ * fp32.  Asynchronous.
  */
 awq_status_t awq_cross_entropy(const uint16_t *x, int64_t M, int64_t in, const uint16_t *W,
                                int64_t V, const int64_t *labels, float *loss, float *lse,
@@ -334,7 +347,9 @@ awq_status_t awq_cross_entropy(const uint16_t *x, int64_t M, int64_t in, const u
  * lse : [M] fp32 from awq_cross_entropy on the same x and W;  dloss : [M] fp32, the
  * gradient of each token's loss (1 / scored tokens for a mean).  dx : [M, in] bf16,
  * written;  dW : [V, in] bf16, written, or NULL when the head is frozen.  d is computed
- * in pieces of the vocabulary and rounded to bf16; the pieces of dx meet in fp32.
+ * in pieces of the vocabulary and rounded to bf16; what that takes off the label's
+ * entry is added to dx, and for M <= 128 dW takes all of d's remainders, too (over more
+ * tokens they average out); the pieces of dx meet in fp32.
  * Rows of x that are not scored add nothing to dW whatever they hold.  dx and dW must not
  * overlap any input or each other.  Asynchronous.
  */

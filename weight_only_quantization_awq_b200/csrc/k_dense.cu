@@ -28,7 +28,11 @@
 // The TMA and MMA warps run their loops warp-wide, one elected lane issuing, so that ring counters
 // and descriptors live in uniform registers.  With one lane running the loop alone, a slab took
 // at least 570 cycles whatever its width, and a 2048 x 32000 x 4096 product 359 us; so it is 326 us
-// (1645 TFLOP/s, 99% of the measured 1652).
+// (1645 TFLOP/s, 99% of the measured 1652), 341 us with the K chunks of EPI_CE.
+//
+// Bound: the tensor pipe (active 94% of the cycles of a 2048 x 22016 x 4096 gated product, 245 us, and of EPI_CE's;
+// in a loop the power limit sets its clock) wherever the tokens fill tiles of 256 rows; for few tokens the reading
+// of the operand from HBM (EPI_CE_T, 13 tokens, 32000 x 4096: 45 us of 49 a call, 5.8 TB/s).
 //
 // Every wait is bounded, as in the other kernels: a CTA that gives up raises its abort flag,
 // waits (bounded) for its MMAs and leaves without writing its remaining tiles.

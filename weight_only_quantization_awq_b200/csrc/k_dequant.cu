@@ -107,6 +107,8 @@ __device__ __forceinline__ float block_sum(float v, float *sm) {
 // Blocks from DMAX_PARTS on: one token each.  out[m] = fp16((row / s) * 2^-k), k from the row's largest
 // magnitude so that it lands in [2^14, 2^15); sx[m] = 2^k.  With dh: grow[m], an exponent
 // that bounds max |dh[m]| * ||row / s||.  The first blocks: the parts' largest |Delta|.
+// Bound: latency for few tokens (3 us), the reads and writes of the rows and each warp's share of scalar work for
+// many (2048 rows of 4096: 12.6 us; the row stays packed in registers between the two passes).
 template <bool GROW>
 __global__ void __launch_bounds__(256) rows16_kernel(const uint16_t *__restrict__ x, const uint16_t *__restrict__ s16,
                                                      int64_t M, int64_t cols, int64_t ld,
@@ -204,6 +206,8 @@ __device__ __forceinline__ uint32_t dq_u32(__half2 v) { return *reinterpret_cast
 // Delta 2^-kW itself only below 2^-14, that is below 2^-24 of the largest).  A
 // block takes DQ_ROWS rows, a thread the same packed word (8 columns, one 16-byte store) of each: their
 // loads are in flight together, and a warp's loads and stores are contiguous.
+// Bound: HBM, half a byte read and two written per weight: 22016 x 4096 in 41 us, 5.5 TB/s (four rows a block 43,
+// eight 49; tiles of the matrix taken as one long row of words, by 8 resident blocks an SM, 46 to 49).
 constexpr int DQ_ROWS = 2;
 __global__ void __launch_bounds__(256) dequant_kernel(const uint32_t *__restrict__ q,
                                                       const uint16_t *__restrict__ scales,

@@ -21,6 +21,13 @@
 //     sum_i (c_i - z) Delta x_i / s_i = Delta 2^k ((D - 1024 T1) - z T2),
 // T1 the sum of the staged values and T2 that of the activations they stand for: xs = fp16((x / s)
 // 2^-k), one power of two per (token, group), so staging needs no pass over the whole row first.
+//
+// Measured: 22016 x 4096, group 128, one token 15.5 us a call back to back (46.8 MB, 3.0 TB/s, 46% of HBM); 27648 x
+// 5120 with zero points, 8 tokens 31.9 us.  What holds it: the packed loop is about 17500 of the
+// kernel's cycles, of which the MMAs (16 cycles of a sub-core each) need 10200 and the unpacking the integer pipe, 52%
+// busy over the whole kernel; the staging of activations and scales in front of it is latency.  Sums of the
+// activations by an extra MMA instead of in the staging make 16 tokens faster (32.2 -> 27.2 us) and one token
+// slower (15.5 -> 16.8); not kept.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
