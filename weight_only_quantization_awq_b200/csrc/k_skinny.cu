@@ -51,7 +51,7 @@ constexpr int SK_GROUPS = 3;                           // groups of eight dequan
 constexpr int SK_DQ_WARPS = 8 * SK_GROUPS;
 constexpr int SK_WARP_EPI = SK_DQ_WARPS, SK_WARP_TMA = SK_DQ_WARPS + 4, SK_WARP_MMA = SK_DQ_WARPS + 5;   // four epilogue warps: TMEM lane quadrants 0-3
 constexpr int SK_THREADS = (SK_DQ_WARPS + 6) * 32;
-constexpr int SK_PF = 1;                              // units of packed codes in flight per thread (twice that per CTA)
+constexpr int SK_PF = 1;                              // units of packed codes in flight per thread (SK_GROUPS times that per CTA)
 constexpr int SK_A_BYTES = 32768;                     // 128 x 128 fp16
 constexpr int SK_MAX_STAGES = 5;
 constexpr int SK_MAX_N = 144;                         // tokens per tile: the most with three stages
