@@ -458,6 +458,9 @@ def _act_code(act) -> int:
 
 def _rows(t: torch.Tensor, name: str, like: torch.Tensor, M: int, cols: int):
     """An [M, cols] bf16 operand on `like`'s device."""
+    if (t.is_cuda and t.dtype == torch.bfloat16 and t.shape == (M, cols) and t.get_device() == like.get_device()
+            and t.is_contiguous()):
+        return t
     if t.dim() != 2 or t.dtype != torch.bfloat16 or tuple(t.shape) != (M, cols):
         raise ValueError(f"{name} must be a bfloat16 tensor of shape [{M}, {cols}]")
     _dev(t, name)
@@ -563,7 +566,7 @@ def awq_linear_w4a16_grad(dy: torch.Tensor, qweight: torch.Tensor, scales: torch
         raise ValueError("dy and qweight must be 2-D")
     M, inp, out_f = dy.shape[0], qweight.shape[1] * 8, qweight.shape[0]
     if out is None:
-        out = torch.empty((M, inp), dtype=torch.bfloat16, device=dy.device)
+        out = dy.new_empty((M, inp), dtype=torch.bfloat16)
     else:
         _out(out, "out", dy, torch.bfloat16, M * inp)
         _apart(out, "out", dy, qweight, scales, zeros, s16)
@@ -578,6 +581,12 @@ def awq_linear_w4a16_grad(dy: torch.Tensor, qweight: torch.Tensor, scales: torch
 
 def _ce_operands(x, W, labels):
     """x [M, in] bf16, W [V, in] bf16, labels [M] int64 on one device.  Returns (M, in, V)."""
+    if x.is_cuda and x.dim() == 2 and W.dim() == 2:   # all as it should be, in one expression (see _fits)
+        (M, inp), dev = x.shape, x.get_device()
+        if (x.dtype == W.dtype == torch.bfloat16 and W.shape[1] == inp and labels.dtype == torch.int64
+                and labels.shape == (M,) and W.get_device() == dev and labels.get_device() == dev
+                and x.is_contiguous() and W.is_contiguous() and labels.is_contiguous()):
+            return M, inp, W.shape[0]
     if x.dim() != 2 or x.dtype != torch.bfloat16 or W.dim() != 2 or W.dtype != torch.bfloat16:
         raise ValueError("x and W must be 2-D bfloat16 tensors")
     M, inp = x.shape
@@ -598,7 +607,7 @@ def awq_cross_entropy(x: torch.Tensor, W: torch.Tensor, labels: torch.Tensor):
     (e.g. -100) marks a token that is not scored: its loss is 0."""
     M, inp, V = _ce_operands(x, W, labels)
     loss = torch.empty(M, dtype=torch.float32, device=x.device)
-    lse = torch.empty(M, dtype=torch.float32, device=x.device)
+    lse = torch.empty_like(loss)
     _launch("awq_cross_entropy", lib.awq_cross_entropy, x.get_device(), x.data_ptr(), M, inp, W.data_ptr(), V,
             labels.data_ptr(), loss.data_ptr(), lse.data_ptr())
     return loss, lse
@@ -611,17 +620,19 @@ def awq_cross_entropy_grad(x: torch.Tensor, W: torch.Tensor, labels: torch.Tenso
     dloss [M] fp32, the gradient of each token's loss; dW is None with want_dw=False (a frozen head).
     Tokens that are not scored have no gradient and add nothing to dW."""
     M, inp, V = _ce_operands(x, W, labels)
+    dev = x.get_device()
     for t, n in ((lse, "lse"), (dloss, "dloss")):
-        _out(t, n, x, torch.float32, M)
+        if not (t.dtype == torch.float32 and t.shape == (M,) and t.get_device() == dev and t.is_contiguous()):
+            _out(t, n, x, torch.float32, M)
     if dW is not None and not want_dw:
         raise ValueError("dW given with want_dw=False")
     if dx is None:
-        dx = torch.empty((M, inp), dtype=torch.bfloat16, device=x.device)
+        dx = x.new_empty((M, inp))
     else:
         _out(dx, "dx", x, torch.bfloat16, M * inp)
         _apart(dx, "dx", x, W, labels, lse, dloss, dW)
     if want_dw and dW is None:
-        dW = torch.empty((V, inp), dtype=torch.bfloat16, device=x.device)
+        dW = x.new_empty((V, inp))
     elif want_dw:
         _out(dW, "dW", x, torch.bfloat16, V * inp)
         _apart(dW, "dW", x, W, labels, lse, dloss)
