@@ -361,6 +361,37 @@ def test_calls_on_two_streams_at_once(awq):
             assert torch.equal(t, w), n
 
 
+def test_calls_back_to_back(awq):
+    """Calls of every path in mixed order with nothing between them, each reading what the one before it
+    wrote where it can: kernels start while their predecessors end, and workspaces are used again at once."""
+    calls = {(n, M): c for M in PATHS for n, c in every_call(awq, M, seed=60 + M).items()}
+    chains = {}
+    for M in (1, 20, 130, 300):
+        w, _, _ = packed(2 * 2816, 1024, 128, True, True, 70 + M)
+        wd, _, _ = packed(2816, 1024, 128, False, True, 71 + M)
+        x = rand(M, 1024, 72 + M)
+
+        def chain(x=x, w=w, wd=wd):
+            h = awq.awq_gated_w4a16(x, *w)
+            y = awq.awq_linear_w4a16_grad(h, *wd)     # [M, 1024] again
+            z = awq.awq_gated_w4a16(y, *w)
+            return h, y, z, awq.awq_gated_w4a16_grad(z, y, *w)
+        chains[("chain", M)] = chain
+    calls.update(chains)
+    want = {}
+    for n, c in calls.items():
+        want[n] = [t.clone() for t in c()]
+        torch.cuda.synchronize()
+    order = np.random.default_rng(20261208).permutation(np.repeat(np.arange(len(calls)), 8))
+    names = list(calls)
+    for part in np.array_split(order, 4):
+        got = [(names[k], calls[names[k]]()) for k in part]
+        torch.cuda.synchronize()
+        for n, outs in got:
+            for a, b in zip(outs, want[n]):
+                assert torch.equal(a, b), n
+
+
 @pytest.mark.parametrize("M", PATHS[1:])
 def test_a_bad_token_stays_alone(awq, M):
     """NaN and infinities of one token reach that token's results only."""
