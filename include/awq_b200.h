@@ -274,14 +274,16 @@ awq_status_t awq_linear_w4a16_batch(const awq_linear_desc_t *descs, int n, int64
  * tanh form.  x : [M, in] bf16 device; h : [M, F] bf16 device, written.
  * Storage arguments as awq_linear_w4a16 with out = 2F; any F >= 1, M <= 2^20,
  * in <= 49152.  g and u are held in fp32 and rounded nowhere before h.
+ * M <= 16, while the staged activations and the scales of a few tiles of 16 columns
+ * fit one SM's shared memory (at in = 4096 and group 128 always; at group 32 up to 7
+ * tokens): one launch streaming the codes.  Up to 288 tokens the weights are
+ * dequantised on their way into the tensor cores, above once into a temporary fp16
+ * matrix of 4 F in bytes.
  * Precision of the operands: x / s16 is rounded to fp16 after a power-of-two
- * scale (M <= 16: one per token and group; above: one per token).  M <= 16: the
- * integer codes are exact, (code - z) * scale is applied in fp32 per group.
- * M >= 17: (code - z) * scale is rounded once to fp16 after a power-of-two scale
- * per layer.  Accumulation in fp32.
- * M <= 16, while the staged activations and two tiles' scales fit one SM's shared
- * memory: one launch streaming the codes.  Up to 288 tokens the weights are dequantised on their
- * way into the tensor cores, above once into a temporary fp16 matrix of 4 F in bytes.
+ * scale, one per token (streaming: per token and group); (code - z) * scale is
+ * rounded once to fp16 after a power-of-two scale per layer (streaming: the codes
+ * are exact, zero point and scale are applied in fp32 per group).  Accumulation in
+ * fp32.
  * Ordering, for this and the four calls below: their kernels are launched with
  * programmatic stream serialisation.  Until the preceding kernel on `stream` has
  * completed they read no argument and write nothing (M <= 16: they ask L2 to
@@ -300,8 +302,8 @@ awq_status_t awq_gated_w4a16(const uint16_t *x, int64_t M, int64_t in, int64_t F
  * packed weights frozen.  g and u are computed again from x, then
  *     dg = dh * u * act'(g),  du = dh * act(g),  dx = ([dg | du] * dequant(W)) / s16.
  * dh : [M, F] bf16 device;  dx : [M, in] bf16 device, written.  Other arguments as
- * awq_gated_w4a16 at M >= 17 (here for any M; the weights are dequantised on their
- * way up to 144 tokens).  dg and du are rounded to fp16 after a power-of-two scale
+ * awq_gated_w4a16, without the streaming (the weights are dequantised on their way
+ * up to 144 tokens).  dg and du are rounded to fp16 after a power-of-two scale
  * per token.  A token's gradient depends on that token's rows alone.
  * dx must not overlap any input.  Asynchronous.
  */

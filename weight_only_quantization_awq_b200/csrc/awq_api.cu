@@ -958,7 +958,7 @@ awq_status_t awq_gated_w4a16(const uint16_t *x, int64_t M, int64_t in, int64_t F
     if (!aligned16(x) || !aligned16(h)) return fail(AWQ_ERR_ALIGN, "misaligned pointer");
     int sms;
     if (awq_status_t s = device_info(&sms)) return s;
-    if (awq::gated_dec_supported(M, in, group_size)) {
+    if (awq::gated_dec_supported(M, in, F, group_size, sms)) {
         cudaStream_t st = static_cast<cudaStream_t>(stream);
         kt_reset(4);
         kt_begin(4, st);

@@ -314,10 +314,12 @@ struct SkinnyArgs {
 cudaError_t launch_skinny(bool grad, int epi, const CUtensorMap &bmap, SkinnyArgs a, const SkinnyPlan &p,
                           cudaStream_t st);
 
-// ---- gated feed-forward for decode-sized M (k_gated_dec.cu); supported: the staged activations
-// and two tiles' scales fit one SM's shared memory
+// ---- gated feed-forward for decode-sized M (k_gated_dec.cu); supported: the staged activations and the
+// scales of all of a CTA's tiles, or of four at a time, fit one SM's shared memory.  With fewer the
+// passes cost more than dequantising on the way into the tensor cores (22016 x 4096: group 32, 8 tokens, three
+// of five tiles a pass 39 / 36 us, 9 tokens, two 56 / 36; group 64, 12 tokens, four 36 / 35, 16 tokens, two 43 / 35).
 constexpr int64_t GATED_DEC_MAX_M = 16;
-bool gated_dec_supported(int64_t M, int64_t I, int gs);
+bool gated_dec_supported(int64_t M, int64_t I, int64_t F, int gs, int num_sms);
 cudaError_t launch_gated_dec(const uint16_t *x, int64_t M, int64_t I, int64_t F, const uint32_t *q,
                              const uint16_t *scales, const uint32_t *zeros, const uint16_t *s16, int gs, int act,
                              uint16_t *h, int num_sms, cudaStream_t st);

@@ -490,8 +490,13 @@ cudaError_t launch_gd(const GdArgs &a, int grid, cudaStream_t st) {
 
 }  // namespace
 
-bool gated_dec_supported(int64_t M, int64_t I, int gs) {
-    return M <= GATED_DEC_MAX_M && gd_pass_tiles(static_cast<int>(M), static_cast<int>(I), gs, M <= 8 ? 1 : 2, 2) >= 2;
+bool gated_dec_supported(int64_t M, int64_t I, int64_t F, int gs, int num_sms) {
+    if (M > GATED_DEC_MAX_M) return false;
+    const int64_t tiles = (F + GD_TILE - 1) / GD_TILE, grid = tiles < num_sms ? tiles : num_sms;
+    const int64_t own = (tiles + grid - 1) / grid;    // tiles of a CTA
+    const int want = own < 4 ? static_cast<int>(own) : 4;
+    const int fit = gd_pass_tiles(static_cast<int>(M), static_cast<int>(I), gs, M <= 8 ? 1 : 2, want);
+    return fit >= want || (fit >= 2 && !skinny_supported(M, GATED_DEC_MAX_M, 2 * F, I));
 }
 
 cudaError_t launch_gated_dec(const uint16_t *x, int64_t M, int64_t I, int64_t F, const uint32_t *q,
