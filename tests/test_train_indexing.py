@@ -18,10 +18,13 @@ def skinny_plan(M, tiles, k):
     n = -(-(-(-M // tt)) // 16) * 16
     tt = -(-M // n)
     ks = -(-k // 128)
-    cost = {c: -(-ks // c) * 600 + (c * 60 + 3000 if c > 1 else 0) for c in range(1, min(ks, 64) + 1)}
-    share = min(cost, key=cost.get)
-    units = tiles * ks * tt
-    return n, tt, ks, min(tiles * tt * share, SMS, units), units
+    T = tiles * tt
+    units = T * ks
+    cost = {SMS: -(-units // SMS) * 600 + 3000 + -(-SMS // T) * 60}
+    for c in range(1, min(ks, 64, SMS // T) + 1):
+        cost.setdefault(T * c, 10 ** 9)
+        cost[T * c] = min(cost[T * c], -(-ks // c) * 600 + (c * 60 + 1000 if c > 1 else 0) + (600 if ks % c else 0))
+    return n, tt, ks, min(min(cost, key=cost.get), units), units
 
 
 def first(units, grid, c):
@@ -30,7 +33,7 @@ def first(units, grid, c):
 
 @pytest.mark.parametrize("M,tiles,k", [
     (1, 1, 64), (17, 22, 512), (50, 4, 2742), (77, 172, 4096), (19, 86, 4096), (144, 3, 22016), (145, 7, 4096),
-    (256, 40, 27648), (352, 172, 4096), (300, 1, 128), (64, 500, 100)])
+    (256, 40, 27648), (352, 172, 4096), (300, 1, 128), (64, 500, 100), (50, 22, 512), (50, 44, 1024), (288, 3, 49152)])
 def test_skinny_ranges_cover_every_stage_once(M, tiles, k):
     n, tt, ks, grid, units = skinny_plan(M, tiles, k)
     assert n % 16 == 0 and n <= MAX_N and n * tt >= M and n * (tt - 1) < M

@@ -608,19 +608,22 @@ SkinnyPlan skinny_plan(int64_t M, int64_t tiles, int64_t k, int num_sms) {
     p.token_tiles = static_cast<int>((M + p.n - 1) / p.n);
     p.tiles = static_cast<int>(tiles);
     p.ks = static_cast<int>((k + 127) / 128);
-    // CTAs: one per SM, but no more of them to a tile than pays: a stage costs its CTA about 600 ns; the
-    // second kernel that shared tiles need takes 3 us, each CTA's partial sums about 60 ns of it.
-    const int64_t units = tiles * p.ks * p.token_tiles;
-    int64_t share = 1, best = INT64_MAX;
-    for (int64_t c = 1; c <= p.ks && c <= 64; ++c) {
-        const int64_t cost = (p.ks + c - 1) / c * 600 + (c > 1 ? c * 60 + 3000 : 0);
+    // CTAs.  Either as many to a tile as pay, c of them, all ranges inside one tile where c divides its
+    // stages; or one on every SM, whose ranges begin and end anywhere in a tile.  A stage costs its CTA about 600
+    // ns, the second kernel that shared tiles need 1 us (it starts while the first ends) and 60 ns per CTA of a
+    // tile, ranges that cross tiles 600 ns to 3 us.  Measured (us on the device, without the aligned choice /
+    // with it): 5632 x 1024 17 tokens 12.2 / 9.6, its gradient 25.8 / 20.2, 2816 x 1024 gradient 12.6 / 8.7; 11008 x
+    // 2048, where every SM has work either way, 16.8 / 16.8.
+    const int64_t T = tiles * p.token_tiles, units = T * p.ks;
+    p.grid = num_sms;
+    int64_t best = (units + num_sms - 1) / num_sms * 600 + 3000 + (num_sms + T - 1) / T * 60;
+    for (int64_t c = 1; c <= p.ks && c <= 64 && T * c <= num_sms; ++c) {
+        const int64_t cost = (p.ks + c - 1) / c * 600 + (c > 1 ? c * 60 + 1000 : 0) + (p.ks % c ? 600 : 0);
         if (cost < best) {
             best = cost;
-            share = c;
+            p.grid = static_cast<int>(T * c);
         }
     }
-    const int64_t most = tiles * p.token_tiles * share;
-    p.grid = static_cast<int>(most < num_sms ? most : num_sms);
     if (p.grid > units) p.grid = static_cast<int>(units);
     p.part_vecs = static_cast<int64_t>(2) * p.grid * p.n * 32;
     return p;
