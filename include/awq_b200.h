@@ -276,9 +276,9 @@ awq_status_t awq_linear_w4a16_batch(const awq_linear_desc_t *descs, int n, int64
  * in <= 49152.  g and u are held in fp32 and rounded nowhere before h.
  * M <= 16, while the staged activations and the scales of a few tiles of 16 columns
  * fit one SM's shared memory (at in = 4096 and group 128 always; at group 32 up to 7
- * tokens): one launch streaming the codes.  Up to 288 tokens the weights are
- * dequantised on their way into the tensor cores, above once into a temporary fp16
- * matrix (4 * F * in bytes).
+ * tokens): one launch streaming the codes.  Up to 144 or 288 tokens, by the size of
+ * the layer, the weights are dequantised on their way into the tensor cores, above
+ * once into a temporary fp16 matrix (4 * F * in bytes).
  * Precision of the operands: x / s16 is rounded to fp16 after a power-of-two
  * scale, one per token (streaming: per token and group); (code - z) * scale is
  * rounded once to fp16 after a power-of-two scale per layer (streaming: the codes

@@ -966,7 +966,7 @@ awq_status_t awq_gated_w4a16(const uint16_t *x, int64_t M, int64_t in, int64_t F
         kt_end(4, st);
         return AWQ_OK;
     }
-    if (awq::skinny_supported(M, awq::SKINNY_MAX_M, 2 * F, in))
+    if (awq::skinny_gated(M, 2 * F, in))
         return gated_skinny(nullptr, x, M, in, F, qweight, scales, zeros, s16, group_size, act, h, sms,
                             static_cast<cudaStream_t>(stream));
     return gated_dense(nullptr, x, M, in, F, qweight, scales, zeros, s16, group_size, act, h, sms,

@@ -290,6 +290,14 @@ struct SkinnyPlan {
 // 52, 208 56 / 54, 288 65 / 75, 304 91 / 79; 5504 x 2048 gradient 250 tokens 22 / 28.
 constexpr int64_t SKINNY_MAX_M = 288, SKINNY_MAX_M_GATED_GRAD = 144;
 inline bool skinny_supported(int64_t M, int64_t most, int64_t O, int64_t I) { return M <= most && O * I <= int64_t(1) << 32; }
+// The gated product: of more than one token tile only if the dequantised matrix does not stay in L2 from the pass
+// that writes it to the product, or is so small that the pass and its launch are what counts (us a call, this way /
+// dense: 11008 x 2048 150 tokens 30 / 29, 250 37 / 29; 13824 x 2560 200 tokens 42 / 39, 250 45 / 39; 22016 x 4096
+// 250 tokens 85 / 93; 8192 x 1536 150 tokens 17 / 22, 250 19 / 22; 5632 x 1024 250 tokens 15 / 17).
+inline bool skinny_gated(int64_t M, int64_t O, int64_t I) {
+    const bool in_l2 = O * I >= (int64_t(16) << 20) && O * I <= (int64_t(50) << 20);
+    return skinny_supported(M, M > 144 && in_l2 ? 144 : SKINNY_MAX_M, O, I);
+}
 SkinnyPlan skinny_plan(int64_t M, int64_t tiles, int64_t k, int num_sms);
 struct SkinnyArgs {
     const uint32_t *q;
