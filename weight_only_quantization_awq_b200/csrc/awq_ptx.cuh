@@ -136,7 +136,10 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 
 // ------------------------------------------------- programmatic dependent launch
 // What a kernel reads of the preceding one's results it reads after griddep_wait() and by __ldcg or a plain
-// load, not by __ldg, which tells the compiler that the memory holds the same throughout the kernel.
+// load, not by __ldg or through a const __restrict__ pointer, which tell the compiler that the memory holds the
+// same throughout the kernel.  This holds for activations, gradients and workspaces, which kernels
+// that let their dependents start early write; weights are written by kernels that do not (packing), so they
+// are complete before any kernel behind those starts.
 //
 // Wait until the preceding kernel of the stream has completed and its memory is
 // visible (returns at once when the launch has no programmatic dependency).

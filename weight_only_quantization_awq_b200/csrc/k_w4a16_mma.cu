@@ -48,11 +48,12 @@ constexpr int MMA_AHEAD = 4;          // groups of codes in flight per warp
 
 // One warp per (token, group) when gs = 128 (4 columns per lane); 2 or 4
 // (token, group) pairs per warp for gs = 64 or 32, reduced over lane segments.
+// x, which the preceding kernel may have written while this one started, is read by plain loads of a
+// pointer without __restrict__.
 template <int GS>
-__global__ void __launch_bounds__(256) xs_prep_kernel(const uint16_t *__restrict__ x,
+__global__ void __launch_bounds__(256) xs_prep_kernel(const uint16_t *x,
                                                       const uint16_t *__restrict__ s16, int64_t M,
-                                                      int64_t I, uint16_t *__restrict__ xsp,
-                                                      float2 *__restrict__ xsm) {
+                                                      int64_t I, uint16_t *xsp, float2 *xsm) {
     constexpr int LPG = GS / 4;                     // lanes per group: 32, 16 or 8
     // The main kernel may start (and read the packed codes) once every block here
     // has passed this wait, i.e. once whatever preceded this kernel on the stream
@@ -143,11 +144,13 @@ __device__ __forceinline__ void load_codes(Codes<GS> &c, const uint32_t *__restr
     }
 }
 
+// xsp and xsm, written by the kernel before, are read by plain loads of pointers without
+// __restrict__ (through L1: the warps of a block share them).
 template <int NT, int GS, bool ZEROS>
 __global__ void __launch_bounds__(MMA_THREADS) w4a16_mma_kernel(
     const uint32_t *__restrict__ qweight, const uint16_t *__restrict__ scales,
-    const uint32_t *__restrict__ zeros, const uint16_t *__restrict__ xsp,
-    const float2 *__restrict__ xsm, int64_t M, int64_t I, int64_t O, uint16_t *__restrict__ y) {
+    const uint32_t *__restrict__ zeros, const uint16_t *xsp, const float2 *xsm, int64_t M, int64_t I,
+    int64_t O, uint16_t *__restrict__ y) {
     constexpr int NW = GS / 32;                  // words per lane per row per group
     __shared__ float red[MMA_WARPS][16][8 * NT];
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(MMA_THREADS) w4a16_mma_kernel(
                 const uint32_t *src = reinterpret_cast<const uint32_t *>(xsp + mb * I + grp * GS + j * (GS / 4));
 #pragma unroll
                 for (int k = 0; k < GS / 8; k += 4) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + k));
+                    const uint4 v = *reinterpret_cast<const uint4 *>(src + k);
                     b[k] = v.x; b[k + 1] = v.y; b[k + 2] = v.z; b[k + 3] = v.w;
                 }
             } else {
@@ -222,8 +225,8 @@ __global__ void __launch_bounds__(MMA_THREADS) w4a16_mma_kernel(
             // tokens 2j, 2j + 1 of this n8 tile: scale 2^k and the sum of xs
             float2 f0 = make_float2(0.0f, 0.0f), f1 = make_float2(0.0f, 0.0f);
             const int m0 = 8 * t + 2 * j;
-            if (m0 < M) f0 = __ldg(xsm + m0 * nG + grp);
-            if (m0 + 1 < M) f1 = __ldg(xsm + (m0 + 1) * nG + grp);
+            if (m0 < M) f0 = xsm[m0 * nG + grp];
+            if (m0 + 1 < M) f1 = xsm[(m0 + 1) * nG + grp];
             acc[t][0] = __fmaf_rn(d0 * f0.x, __fmaf_rn(-zb0, f0.y, dacc[0]), acc[t][0]);
             acc[t][1] = __fmaf_rn(d0 * f1.x, __fmaf_rn(-zb0, f1.y, dacc[1]), acc[t][1]);
             acc[t][2] = __fmaf_rn(d1 * f0.x, __fmaf_rn(-zb1, f0.y, dacc[2]), acc[t][2]);

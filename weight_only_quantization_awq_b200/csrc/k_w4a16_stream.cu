@@ -144,7 +144,8 @@ __global__ void __launch_bounds__(GvShape<MT>::NW * 32, 1) w4a16_gemv_kernel(con
         const int wd = task & 3, ch = task >> 2, t = ch / MT, m = ch % MT;
         xv = sv = make_uint4(0u, 0u, 0u, 0u);
         if (task < ntask && m < a.M && t < nch) {
-            xv = __ldg(reinterpret_cast<const uint4 *>(a.x + static_cast<int64_t>(m) * I + t * 32 + wd * 8));
+            // (__ldcg: the preceding kernel, which may end while this one runs, may have written x)
+            xv = __ldcg(reinterpret_cast<const uint4 *>(a.x + static_cast<int64_t>(m) * I + t * 32 + wd * 8));
             // no s16: x arrives already divided by s (fp16 ones leave it unchanged)
             sv = a.s16 ? __ldg(reinterpret_cast<const uint4 *>(a.s16 + t * 32 + wd * 8))
                        : make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u);
