@@ -34,8 +34,9 @@
 // in a loop the power limit sets its clock) wherever the tokens fill tiles of 256 rows; for few tokens the reading
 // of the operand from HBM (EPI_CE_T, 13 tokens, 32000 x 4096: 45 us of 49 a call, 5.8 TB/s).
 //
-// Every wait is bounded, as in the other kernels: a CTA that gives up raises its abort flag,
-// waits (bounded) for its MMAs and leaves without writing its remaining tiles.
+// Every wait is bounded, as in the other kernels: a CTA that gives up raises its abort flag and
+// leaves without writing its remaining tiles, once the MMAs and the copies of both CTAs of the pair that
+// are in flight have finished (bounded, too).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -63,8 +64,8 @@ template <int EPI>
 constexpr int GM_KCHUNK = EPI == EPI_CE || EPI == EPI_CE_T ? 16 : 1 << 30;
 constexpr int GM_BAND = 8;                            // row tiles walked together
 constexpr uint32_t GM_TMEM = 512;
-constexpr int GM_BARS = 2 * GM_MAX_STAGES + 4 + 1;
-constexpr int GM_SMEM = 1024 + GM_RING + GM_BARS * 8 + 16;
+constexpr int GM_BARS = 2 * GM_MAX_STAGES + 4 + 2;
+constexpr int GM_SMEM = 1024 + GM_RING + GM_BARS * 8 + 16;   // ... and four words behind the barriers
 static_assert(GM_SMEM <= 232448, "shared memory plan");
 
 // Shared-memory descriptor of an MN-major operand in the 128-byte swizzle: blocks of 64
@@ -562,8 +563,10 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
     uint64_t *acc_full = empty + GM_MAX_STAGES;            // [2]: accumulator halves
     uint64_t *acc_empty = acc_full + 2;                // [2]
     uint64_t *drain = acc_empty + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *stopped = drain + 1;                     // the leader's: neither CTA issues any more copies
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(stopped + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile uint32_t *issued = reinterpret_cast<volatile uint32_t *>(tmem_slot + 2);   // [2] the leader's: their numbers
 
     griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -586,6 +589,7 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
             mbar_init(&acc_empty[h], 2 * 4 * GM_EPI_Q<EPI>);   // epilogue warps of both CTAs
         }
         mbar_init(drain, 1);
+        mbar_init(stopped, 2);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -606,7 +610,7 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
     constexpr uint32_t tmem_base = 0;
 
     if (warp == 0) {
-        uint32_t st = 0, ph = 1;
+        uint32_t st = 0, ph = 1, n_issued = 0;
         bool ok = true;
         const uint32_t bytes = GM_A_BYTES + (B_MN ? nb * 8192 : bh * 128);
         for (int t = pair; t < tiles && ok; t += pairs) {
@@ -640,12 +644,19 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
                     }
                 }
                 __syncwarp();
+                ++n_issued;
                 if (++st == static_cast<uint32_t>(stages)) {
                     st = 0;
                     ph ^= 1u;
                 }
             }
         }
+        // Where this CTA's copies ended, for the leader (below).
+        if (lane == 0) {
+            st_cluster_u32(cluster_addr(const_cast<uint32_t *>(issued) + rank, 0), n_issued);
+            mbar_arrive_release_cluster(cluster_addr(stopped, 0));
+        }
+        __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
             const uint32_t idesc = idesc_f16_f32(256, a.bn, BF16) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
@@ -682,6 +693,22 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
                 }
             }
             if (elect_one()) umma_commit_pair(drain, 0x3);
+            __syncwarp();
+            // Every slab multiplied: every copy has landed.  Else a wait ran out, and copies may be in flight,
+            // counted on this CTA's barriers: wait (bounded) for the last of every stage before either
+            // CTA leaves.  A stage that only one of the CTAs asked for gets the other's part of its barrier here,
+            // when no MMA waits for it any more.  (The copying warps may only now begin to wait for their last stage.)
+            if (!ok && lane == 0 && mbar_wait_drain(drain, 0, 2 * AWQ_WAIT_CYCLES) &&
+                mbar_wait_drain(stopped, 0, 2 * AWQ_WAIT_CYCLES)) {
+                fence_cluster();
+                const uint32_t i0 = issued[0], i1 = issued[1], most = i0 > i1 ? i0 : i1, n_st = static_cast<uint32_t>(stages);
+                const uint32_t bytes = GM_A_BYTES + (B_MN ? nb * 8192 : bh * 128);
+                for (uint32_t n = most > n_st ? most - n_st : 0; n < most; ++n) {
+                    if (n >= i1) mbar_complete_tx(&full[n % n_st], bytes);
+                    if (n >= i0) mbar_arrive_expect_tx(&full[n % n_st], bytes);
+                    mbar_wait_drain(&full[n % n_st], (n / n_st) & 1u);
+                }
+            }
             __syncwarp();
         }
     } else if (warp < GM_EPI_WARP0) {
