@@ -288,6 +288,9 @@ awq_status_t awq_linear_w4a16_batch(const awq_linear_desc_t *descs, int n, int64
  * programmatic stream serialisation.  Until the preceding kernel on `stream` has
  * completed they read no argument and write nothing (M <= 16: they ask L2 to
  * prefetch weights).
+ * Waits inside these kernels are bounded, at about 2 s of SM clock.  Should one run out
+ * (the device does not make progress), the call has returned AWQ_OK long since; the
+ * results that were not completed are NaN.
  * h must not overlap any input.  Asynchronous.
  */
 typedef enum { AWQ_ACT_SILU = 0, AWQ_ACT_GELU = 1, AWQ_ACT_GELU_TANH = 2 } awq_act_t;

@@ -10,13 +10,14 @@ the same ring indices, phases and barrier counts:
   `empty` and, at the end, to both `acc_full`; at last, or when a wait ran out, to both `drain`.  In the second case
   it waits for `drain`, `stopped` and then the last phase of every stage, supplying what one of the two CTAs never
   asked for.
-* epilogue, in each CTA: waits `acc_full`, reads, arrives on the leader's `acc_empty`.
+* epilogue, in each CTA: waits `acc_full`, reads, arrives on the leader's `acc_empty`; after a wait that ran out it
+  waits no more and writes NaN for this and every further accumulation.
 
 Copies land in any order, MMAs and commits complete in issue order, and a random scheduler interleaves the roles.  In
 half of the runs some waits run out: the role stops, its CTA's abort flag is set, and the CTA's other roles stop at
 their next wait that is not met.  The checks: without that, nothing deadlocks and every slab is multiplied
-once, from the stage that holds it; with it, every role ends, no wait of the last part runs out, and no copy
-is in flight when the CTAs leave.
+once, from the stage that holds it; with it, every role ends, no wait of the last part runs out, no copy
+is in flight when the CTAs leave, and every result is written: NaN, or made of all its slabs.
 """
 import random
 
@@ -53,7 +54,8 @@ class Bar:
 
 
 def run_pair(units, nk, stages, seed, expire, drained=True, epi=2):
-    """units: accumulations of nk slabs.  Returns (copies in flight at the end, slabs multiplied, aborted)."""
+    """units: accumulations of nk slabs.  Returns (copies in flight at the end, slabs multiplied, aborted, results:
+    whether the accumulation was complete, by (CTA, warp, accumulation))."""
     rnd = random.Random(seed)
     full = [Bar(1) for _ in range(stages)]            # the leader's
     empty = [[Bar(1) for _ in range(stages)] for _ in range(2)]
@@ -62,7 +64,7 @@ def run_pair(units, nk, stages, seed, expire, drained=True, epi=2):
     drain, stopped = [Bar(1), Bar(1)], Bar(2)
     abort, held = [False, False], [[None] * stages for _ in range(2)]
     copies, tensor, multiplied = [], [], []
-    sent = {}
+    sent, results = {}, {}
 
     def tma(rank):
         n = 0
@@ -105,16 +107,20 @@ def run_pair(units, nk, stages, seed, expire, drained=True, epi=2):
                 full[k % stages].arrive(expect_tx=1)
             assert (yield None, full[k % stages], k // stages)
 
-    def epilogue(rank):
+    def epilogue(rank, w):
+        ok = True
         for t in range(units):
-            if not (yield rank, acc_full[rank][t % 2], t // 2):
-                return
-            acc_empty[t % 2].arrive()
+            if ok:
+                ok = yield rank, acc_full[rank][t % 2], t // 2
+            if ok:
+                assert set(range(t * nk, (t + 1) * nk)) <= set(multiplied)
+                acc_empty[t % 2].arrive()
+            results[rank, w, t] = ok
 
     def leave(rank):                                  # one lane of the MMA warp, after its role
         assert (yield None, drain[rank], 0)
 
-    roles = [tma(0), tma(1), mma(), *(epilogue(r) for r in (0, 1) for _ in range(epi)), leave(0), leave(1)]
+    roles = [tma(0), tma(1), mma(), *(epilogue(r, w) for r in (0, 1) for w in range(epi)), leave(0), leave(1)]
     waits = {i: next(r, None) for i, r in enumerate(roles)}
     waits = {i: w for i, w in waits.items() if w is not None}
 
@@ -160,7 +166,7 @@ def run_pair(units, nk, stages, seed, expire, drained=True, epi=2):
             else:
                 for r in (0, 1):
                     {"empty": empty[r], "acc": acc_full[r], "drain": [drain[r]]}[what][v].arrive()
-    return len(copies), multiplied, any(abort)
+    return len(copies), multiplied, any(abort), results
 
 
 SHAPES = [(1, 1, 6), (1, 20, 6), (3, 7, 6), (5, 2, 12), (2, 40, 7), (9, 1, 6)]
@@ -169,15 +175,17 @@ SHAPES = [(1, 1, 6), (1, 20, 6), (3, 7, 6), (5, 2, 12), (2, 40, 7), (9, 1, 6)]
 @pytest.mark.parametrize("units,nk,stages", SHAPES)
 def test_every_slab_is_multiplied_once(units, nk, stages):
     for seed in range(30):
-        flying, done, aborted = run_pair(units, nk, stages, seed, 0.0)
+        flying, done, aborted, results = run_pair(units, nk, stages, seed, 0.0)
         assert flying == 0 and not aborted and done == list(range(units * nk))
+        assert len(results) == 4 * units and all(results.values())
 
 
 @pytest.mark.parametrize("units,nk,stages", SHAPES)
-def test_no_copy_is_in_flight_when_the_pair_leaves(units, nk, stages):
+def test_waits_that_run_out(units, nk, stages):
     for seed in range(200):
-        flying, done, _ = run_pair(units, nk, stages, 1000 + seed, (0.002, 0.02, 0.2)[seed % 3])
+        flying, done, _, results = run_pair(units, nk, stages, 1000 + seed, (0.002, 0.02, 0.2)[seed % 3])
         assert flying == 0 and done == list(range(len(done)))
+        assert len(results) == 4 * units             # nothing is left as it was
 
 
 def test_the_model_sees_copies_that_nobody_waits_for():

@@ -34,9 +34,10 @@
 // in a loop the power limit sets its clock) wherever the tokens fill tiles of 256 rows; for few tokens the reading
 // of the operand from HBM (EPI_CE_T, 13 tokens, 32000 x 4096: 45 us of 49 a call, 5.8 TB/s).
 //
-// Every wait is bounded, as in the other kernels: a CTA that gives up raises its abort flag and
-// leaves without writing its remaining tiles, once the MMAs and the copies of both CTAs of the pair that
-// are in flight have finished (bounded, too).
+// Every wait is bounded, as in the other kernels: a CTA that gives up raises its abort flag, writes NaN for
+// its remaining tiles (results, partial sums and gradients alike, so that no later step of the call adds
+// what was in the workspace before), and leaves once the MMAs and the copies of both CTAs of the pair
+// that are in flight have finished (bounded, too).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -120,11 +121,13 @@ __device__ __forceinline__ void store_bf16_16(uint16_t *p, const float (&v)[16],
 
 // ---- epilogues of one thread's row (its TMEM lane at `acc`), tile columns [0, bn).  The TMEM
 // loads are warp-wide: rows beyond M skip only the work between them, and every loop ends in a
-// warp barrier.
+// warp barrier.  `done` is false where the accumulator was never completed (a wait ran out): a scale
+// of NaN then makes every result NaN.
+constexpr float GM_NAN = __builtin_nanf("");
 
-__device__ __forceinline__ void epi_gated(const GemmArgs &a, uint32_t acc, int64_t row, int64_t f0, int par) {
+__device__ __forceinline__ void epi_gated(const GemmArgs &a, uint32_t acc, int64_t row, int64_t f0, int par, bool done) {
     const int half = a.bn / 2;
-    const float sc = row < a.M ? __ldcg(a.sx + row) : 0.0f;
+    const float sc = !done ? GM_NAN : row < a.M ? __ldcg(a.sx + row) : 0.0f;
     const float sw = dq_scale(a.dmax);
     const bool vec = a.F % 8 == 0;
 #pragma unroll 1
@@ -144,10 +147,11 @@ __device__ __forceinline__ void epi_gated(const GemmArgs &a, uint32_t acc, int64
     }
 }
 
-__device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t f0, int par) {
+__device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t f0, int par,
+                                              bool done) {
     const int half = a.bn / 2;
     const bool ok = row < a.M;
-    const float sc = ok ? __ldcg(a.sx + row) : 0.0f;
+    const float sc = !done ? GM_NAN : ok ? __ldcg(a.sx + row) : 0.0f;
     const int kw = dq_exp(a.dmax);
     const float sw = ldexpf(1.0f, kw);
     // 2^-e of this token's gradients
@@ -205,12 +209,15 @@ __device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, i
 }
 
 // A K split's partial sums: this unit's slot [bn / 4][256 rows] of four columns.
-__device__ __forceinline__ void epi_part(const GemmArgs &a, uint32_t acc, int unit, int r, int par) {
+__device__ __forceinline__ void epi_part(const GemmArgs &a, uint32_t acc, int unit, int r, int par, bool done) {
     float4 *p = a.part4 + static_cast<int64_t>(unit) * (a.bn / 4) * 256;
 #pragma unroll 1
     for (int c = 16 * par; c < a.bn; c += 32) {
         uint32_t v[16];
         tmem_ld16_wait(acc + c, v);
+        if (!done)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(GM_NAN);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             p[(c / 4 + k) * 256 + r] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
@@ -301,10 +308,11 @@ __device__ __forceinline__ void out_columns(const GemmArgs &a, int64_t row, int6
     }
 }
 
-__device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int par) {
+__device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int par, bool done) {
     const bool ok = row < a.M;
     float sc, sw;
     out_scales(a, ok, row, sc, sw);
+    if (!done) sc = GM_NAN;
     const LabelTerm t = label_term(a, ok, row);
 #pragma unroll 1
     for (int c = 16 * par; c < a.bn; c += 32) {
@@ -489,11 +497,11 @@ __device__ __forceinline__ void ce_labels(const GemmArgs &a, int64_t tokens, int
 // What rounding to bf16 takes off v (exact).
 __device__ __forceinline__ float bf16_rest(float v) { return v - __bfloat162float(__float2bfloat16_rn(v)); }
 
-__device__ __forceinline__ void epi_ce_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int par) {
+__device__ __forceinline__ void epi_ce_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int par, bool done) {
     const bool ok = row < a.M;
     const int64_t lab = ok ? __ldcg(a.labels + row) : -1;
     const bool scored = lab >= 0 && lab < a.V;
-    const float lse = ok ? __ldcg(a.lse + row) : 0.0f;
+    const float lse = !done ? GM_NAN : ok ? __ldcg(a.lse + row) : 0.0f;
     const float w = ok ? __ldcg(a.dloss + row) : 0.0f;
 #pragma unroll 1
     for (int c = 16 * par; c < a.bn; c += 32) {
@@ -523,7 +531,7 @@ __device__ __forceinline__ void epi_ce_bwd(const GemmArgs &a, uint32_t acc, int6
 
 // The gradients of few tokens, the vocabulary on the rows: the lanes of a warp are 32 neighbouring
 // entries of a token's row.
-__device__ __forceinline__ void epi_ce_bwd_t(const GemmArgs &a, uint32_t acc, int64_t row, int par) {
+__device__ __forceinline__ void epi_ce_bwd_t(const GemmArgs &a, uint32_t acc, int64_t row, int par, bool done) {
     const int lane = threadIdx.x & 31;
 #pragma unroll 1
     for (int c = 16 * par; c < a.bn; c += 32) {
@@ -533,7 +541,7 @@ __device__ __forceinline__ void epi_ce_bwd_t(const GemmArgs &a, uint32_t acc, in
         const int64_t m = c + (lane & 15);
         const bool in = m < a.N;
         const int64_t lab = in ? __ldcg(a.labels + m) : -1;
-        const float lse = in ? __ldcg(a.lse + m) : 0.0f, w = in ? __ldcg(a.dloss + m) : 0.0f;
+        const float lse = !done ? GM_NAN : in ? __ldcg(a.lse + m) : 0.0f, w = in ? __ldcg(a.dloss + m) : 0.0f;
         const int rel = lab >= 0 && lab < a.V ? static_cast<int>(lab) : -1;   // V <= 2^24
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
@@ -719,18 +727,18 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
         const uint32_t acc0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
         uint32_t ti = 0;
         bool ok = true;
-        auto await = [&]() {                          // the next accumulator half
-            ok = __all_sync(0xffffffffu, mbar_wait_sleep(&acc_full[ti & 1u], (ti >> 1) & 1u, abort_flag));
+        auto await = [&]() {                          // the next accumulator half (none after one that did not come)
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_sleep(&acc_full[ti & 1u], (ti >> 1) & 1u, abort_flag));
             tc_fence_after();
             return ok;
         };
         auto release = [&]() {                        // ... may be overwritten
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[ti & 1u], 0));
+            if (ok && lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[ti & 1u], 0));
             ++ti;
         };
-        for (int t = pair; t < tiles && ok; t += pairs) {
+        for (int t = pair; t < tiles; t += pairs) {
             const Tile tl = decode_tile(t / a.splits, a.mt, a.nt);
             const int64_t row = static_cast<int64_t>(tl.m) * 256 + rank * 128 + quad * 32 + lane;
             if constexpr (EPI == EPI_CE || EPI == EPI_CE_T) {
@@ -739,12 +747,15 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
                 for (int i = 0; i < CE_CHUNKS; ++i)
 #pragma unroll
                     for (int k = 0; k < 16; ++k) v[i][k] = 0.0f;
-                for (int kc = 0; kc < nk && ok; kc += GM_KCHUNK<EPI>) {
-                    if (!await()) break;
+                for (int kc = 0; kc < nk && await(); kc += GM_KCHUNK<EPI>) {
                     ce_gather<GM_EPI_Q<EPI>>(acc0 + (ti & 1u) * 256, a.bn, par, v);
                     release();
                 }
-                if (!ok) break;
+                if (!ok)
+#pragma unroll
+                    for (int i = 0; i < CE_CHUNKS; ++i)
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) v[i][k] = GM_NAN;
                 if constexpr (EPI == EPI_CE)
                     epi_ce(a, v, row, static_cast<int64_t>(tl.n) * a.bn, 4 * tl.n + par, par);
                 else
@@ -752,18 +763,18 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
                 __syncwarp();
                 continue;
             }
-            if (!await()) break;
+            await();
             const uint32_t acc = acc0 + (ti & 1u) * 256;
-            if constexpr (EPI == EPI_GATED) epi_gated(a, acc, row, static_cast<int64_t>(tl.n) * bh, par);
-            if constexpr (EPI == EPI_GATED_BWD) epi_gated_bwd(a, acc, row, static_cast<int64_t>(tl.n) * bh, par);
+            if constexpr (EPI == EPI_GATED) epi_gated(a, acc, row, static_cast<int64_t>(tl.n) * bh, par, ok);
+            if constexpr (EPI == EPI_GATED_BWD) epi_gated_bwd(a, acc, row, static_cast<int64_t>(tl.n) * bh, par, ok);
             if constexpr (EPI == EPI_OUT) {
                 if (a.splits > 1)
-                    epi_part(a, acc, t, static_cast<int>(rank) * 128 + quad * 32 + lane, par);
+                    epi_part(a, acc, t, static_cast<int>(rank) * 128 + quad * 32 + lane, par, ok);
                 else
-                    epi_out(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par);
+                    epi_out(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par, ok);
             }
-            if constexpr (EPI == EPI_CE_BWD_T) epi_ce_bwd_t(a, acc, row, par);
-            if constexpr (EPI == EPI_CE_BWD) epi_ce_bwd(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par);
+            if constexpr (EPI == EPI_CE_BWD_T) epi_ce_bwd_t(a, acc, row, par, ok);
+            if constexpr (EPI == EPI_CE_BWD) epi_ce_bwd(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par, ok);
             release();
         }
     }

@@ -33,8 +33,9 @@
 // in the gradient it is the order of the accumulator's lanes, and the epilogue writes lane p to
 // column frag_perm8(p) of its word.
 //
-// Every wait is bounded: a CTA that gives up raises its abort flag, waits (bounded) for its copies and
-// MMAs in flight, frees its TMEM and leaves without writing its remaining tiles.
+// Every wait is bounded: a CTA that gives up raises its abort flag, writes NaN for its remaining tiles
+// (partial sums and gradients, too: the steps that follow would add what was in the workspace before), waits
+// (bounded) for its copies and MMAs in flight, frees its TMEM and leaves.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -161,6 +162,24 @@ __device__ __forceinline__ void sk_finish(const SkinnyArgs &a, int t, int m0, in
                     dst[0] = __half_as_ushort(__float2half_rn((dv * uv) * da));
                     dst[a.F] = __half_as_ushort(__float2half_rn(dv * av));
                 }
+            }
+        }
+    }
+}
+
+// The same where the accumulator was never completed (a wait ran out): NaN for the tile's tokens c .. c + K - 1.
+template <int EPI, int K>
+__device__ __noinline__ void sk_give_up(const SkinnyArgs &a, int t, int m0, int mcount, int c, int e) {
+    const int64_t col = static_cast<int64_t>(t) * 128 + (e & ~7) + frag_perm8(e & 7), f = static_cast<int64_t>(t) * 64 + e;
+    for (int m = c; m < c + K && m < mcount; ++m) {
+        if (EPI == EPI_OUT) {
+            if (col < a.I) a.out[(m0 + m) * a.I + col] = 0x7FFF;
+        } else if (e < 64 && f < a.F) {
+            if (EPI == EPI_GATED) {
+                a.out[(m0 + m) * a.F + f] = 0x7FFF;
+            } else {
+                uint16_t *dst = a.d16 + (m0 + m) * a.ldd + f;
+                dst[0] = dst[a.F] = 0x7FFF;
             }
         }
     }
@@ -441,6 +460,8 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
                     sk_finish<EPI, 16>(a, t, m0, mcount, c, v, pre, e, ldexpf(1.0f, kw), ss, ss + 256, xs + flip * (16 * 128), 1 + set);
                     __syncwarp();
                 }
+            } else {
+                for (int c = 16 * set; c < a.n; c += 16 * SK_SETS) sk_give_up<EPI, 16>(a, t, m0, mcount, c, e);
             }
         }
     } else if (warp == SK_WARP_TMA) {
@@ -523,6 +544,7 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
         const float sw = ldexpf(1.0f, kw);
         uint32_t seg = 0, flip = 0;
         int have = -1;                                // token tile whose scales are in tsc
+        bool ok = true;
         for (int u = u0; u < u1; ++seg) {
             const int T = u / a.ks, tt = T / a.tiles, t = T - tt * a.tiles;
             const int b0 = T * a.ks, b1 = b0 + a.ks, end = b1 < u1 ? b1 : u1;
@@ -535,12 +557,21 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
                 named_bar_sync(1, 128);
                 have = tt;
             }
-            // (one outcome for the four warps: they meet at barriers below)
-            if (!named_bar_and(1, 128, mbar_wait_sleep(&acc_full[h], (seg >> 1) & 1u, abort_flag))) break;
+            // (one outcome for the four warps: they meet at barriers below; no wait after one that ran out)
+            if (ok) ok = named_bar_and(1, 128, mbar_wait_sleep(&acc_full[h], (seg >> 1) & 1u, abort_flag));
             tc_fence_after();
             // a shared tile's partial sums: this CTA's slot [n / 4][128] of four tokens
             float4 *mine = a.part + static_cast<int64_t>(2 * blockIdx.x + (u0 > b0 ? 0 : 1)) * a.n * 32;
             for (int c = 0; c < a.n; c += WHOLE && end == u1 ? 16 * SK_SETS : 16) {
+                if (!ok) {
+                    if (whole) {
+                        sk_give_up<EPI, 16>(a, t, m0, mcount, c, e);
+                    } else {
+                        const float nan = __uint_as_float(0x7FFFFFFFu);
+                        for (int k = 0; k < 4; ++k) mine[(c / 4 + k) * 128 + e] = make_float4(nan, nan, nan, nan);
+                    }
+                    continue;
+                }
                 uint32_t rv[16];
                 tmem_ld16_wait(acc + c, rv);
                 float v[16];
@@ -558,7 +589,7 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[h]);
+            if (ok && lane == 0) mbar_arrive(&acc_empty[h]);
             u = end;
         }
     }
