@@ -352,9 +352,10 @@ awq_status_t awq_cross_entropy(const uint16_t *x, int64_t M, int64_t in, const u
  * lse : [M] fp32 from awq_cross_entropy on the same x and W;  dloss : [M] fp32, the
  * gradient of each token's loss (1 / scored tokens for a mean).  dx : [M, in] bf16,
  * written;  dW : [V, in] bf16, written, or NULL when the head is frozen.  d is computed
- * in pieces of the vocabulary and rounded to bf16; what that takes off the label's
- * entry is added to dx, and for M <= 128 dW takes all of d's remainders, too (over more
- * tokens they average out); the pieces of dx meet in fp32.
+ * in pieces of the vocabulary and rounded to bf16, except for the label's entry in dx:
+ * that is exp(t - lse) - 1 of the label's logit t in fp32, and stays fp32.  dW takes it
+ * rounded to bf16; for M <= 128 it takes the remainders of all of d, too.  The pieces of
+ * dx meet in fp32.
  * Rows of x that are not scored add nothing to dW whatever they hold.  dx and dW must not
  * overlap any input or each other.  Asynchronous.
  */

@@ -1,0 +1,48 @@
+"""GPU checks of the digits that the gated, gradient and cross-entropy calls keep: the label's gradient of
+confident tokens.  Tolerances as in test_gpu_train."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_train import F8, UBF, awq, within  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("want_dw", [False, True])
+@pytest.mark.parametrize("M", [1, 13, 64, 65, 130, 300])
+def test_label_gradient_of_confident_tokens(awq, M, want_dw):  # noqa: F811
+    """d[label] = exp(t - lse) - 1 where t is nearly lse: what is left is as exact as t and lse are.
+
+    Dense positive rows of 4096 columns, t from 13 to 21, 1 - p from 1e-2 to 1e-4.  Column 0 is 1 in the label's row
+    of W and 0 elsewhere, so dx[:, 0] is d[label] itself, rounded to bf16.  t in fp32 is 64 chains (32 lanes of two)
+    of 64 FMAs and a tree: each rounding of a chain is at most 2^-24 of at most t / 64, those of a level of the tree
+    2^-24 t in all; as independent and uniform errors their standard deviations are sqrt(64 x 64 / 3) / 64 = 0.6 and
+    below sqrt(2 / 3) = 0.8 of 2^-24 t, together one: the bound is eight of those, 2^-21 t.  (lse is an input.)"""
+    I, V, L = 4096, 301, 77
+    rng = np.random.default_rng([20261209, 41, M])
+    x = np.abs(rng.standard_normal((M, I))) + 0.2
+    x[:, 0] = 0.0
+    W = np.abs(rng.standard_normal((V, I))) * 0.3 + 1.0
+    W *= 0.29 / W.mean()
+    W[L] *= 1.0 / 0.29
+    gap = np.log((V - 1) / 10.0 ** -(2 + 2 * rng.random(M)))   # t minus the other logits
+    x *= (gap / (0.71 * I * x.mean(1)))[:, None] * 64           # rows of W carry 1 / 64
+    W /= 64
+    W[:, 0] = 0.0
+    W[L, 0] = 1.0
+    dev = lambda a: torch.from_numpy(a.astype(np.float32)).cuda().to(torch.bfloat16)  # noqa: E731
+    x, W = dev(x), dev(W)
+    labels = torch.full((M,), L, device="cuda")
+    _, lse = awq.awq_cross_entropy(x, W, labels)
+    t = (x.to(F8) * W[L].to(F8)).sum(1)
+    d = torch.expm1(t - lse.to(F8))
+    assert ((-d > 3e-5) & (-d < 5e-2)).all() and (t > 10).all()
+    dx, dW = awq.awq_cross_entropy_grad(x, W, labels, lse, torch.ones(M, device="cuda"), want_dw=want_dw)
+    et = 2.0 ** -21 * t + 2.0 ** -22 * d.abs()       # and the rounding of expm1
+    within(dx[:, 0], d, et + UBF * (d.abs() + et), "d[label]")
+    if want_dw:
+        ref = (d[:, None] * x.to(F8)).sum(0)
+        u = UBF * UBF if M <= 128 else UBF
+        e = ((et + u * d.abs())[:, None] * x.to(F8)).sum(0) + 2.0 ** -16 * ref.abs()
+        within(dW[L], ref, e + UBF * (ref.abs() + e) + 1e-30, "dW[label]")

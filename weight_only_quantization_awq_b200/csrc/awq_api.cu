@@ -1158,11 +1158,7 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
     float *res = ws.take<float>(M);
     float4 *part4 = parts ? ws.take<float4>(parts) : nullptr;
     float *acc = pieces > 1 ? ws.take<float>(M * in) : nullptr;
-    uint16_t *xz = nullptr;
-    if (dW) {
-        xz = ws.take<uint16_t>(dr * in);
-        AWQ_CUDA(awq::launch_scored_rows(x, labels, V, M, in, static_cast<int>(dr / M), xz, sms, st));
-    }
+    uint16_t *xz = dW ? ws.take<uint16_t>(dr * in) : nullptr;
     kt_reset(4);
     kt_begin(4, st);
     for (int64_t v0 = 0; v0 < V; v0 += vc) {
@@ -1185,6 +1181,9 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
         a.d16 = d16;
         a.ldd = ldd;
         a.res = res;
+        a.x = x;
+        a.w = W;
+        a.inner = static_cast<int>(in);
         a.lo = dr - M;
         if (awq_status_t s = map_kmajor(&maps.a, true, few ? Wp : x, in, a.M, in, 128)) return s;
         if (awq_status_t s = map_kmajor(&maps.b, true, few ? x : Wp, in, a.N, in, a.bn / 2)) return s;
@@ -1212,6 +1211,9 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
         if (awq_status_t s = map_mnmajor(&maps.b, true, Wp, in, n, in)) return s;
         AWQ_CUDA(awq::launch_gemm16(awq::EPI_OUT, true, false, maps, b, sms, st));
         if (dW) {
+            // (behind the product with the head: its label terms are added in fp32)
+            AWQ_CUDA(awq::launch_scored_rows(x, labels, V, M, in, v0 == 0 ? static_cast<int>(dr / M) : 0, xz, res, d16, ldd,
+                                             v0, n, dr - M, sms, st));
             awq::GemmArgs c{};
             c.splits = 1;
             c.M = n;

@@ -11,7 +11,7 @@
 //   EPI_CE         logits = x W^T of one vocabulary tile: each row's maximum and sum of
 //                  exponentials over the tile, and the label's logit; the logits stay on chip;
 //   EPI_CE_T, EPI_CE_BWD_T   the same and the next for few tokens, the vocabulary on D's rows;
-//   EPI_CE_BWD     (exp(logit - lse) - [n = label]) * dloss as bf16, one piece of the vocabulary.
+//   EPI_CE_BWD     exp(logit - lse) * dloss as bf16, one piece of the vocabulary, the label's entry apart.
 //
 // CTA pairs (clusters of two, one CTA per SM, persistent over output tiles): a tile is 256 rows
 // x bn columns (bn <= 256, a multiple of 32) on tcgen05.mma.cta_group::2, M = 256, N = bn,
@@ -60,7 +60,11 @@ template <int EPI>
 constexpr int GM_THREADS = (GM_EPI_WARP0 + 4 * GM_EPI_Q<EPI>) * 32;
 // The cross entropy's logits are accumulated GM_KCHUNK slabs (1024 columns) at a time on the tensor cores
 // and added up in registers: the tensor cores truncate each 16-column step towards zero, and over
-// a whole row the losses came out 1e-6 of themselves too low.
+// a whole row the losses came out 1e-6 of themselves too low.  The gradients take K in one go: the same 1e-6 to
+// 2.5e-6 of a logit (4096 columns; in proportion to the columns, 3e-5 at the most that are allowed) is a relative
+// error of exp(logit - lse) of 5e-5 at a logit of 20, 6e-4 at the most columns, below the 2^-8 of the
+// rounding to bf16 that follows.  It is not below it in the label's entry, a difference of nearly equal
+// numbers: that one is formed from an fp32 logit (ce_labels).
 template <int EPI>
 constexpr int GM_KCHUNK = EPI == EPI_CE || EPI == EPI_CE_T ? 16 : 1 << 30;
 constexpr int GM_BAND = 8;                            // row tiles walked together
@@ -239,8 +243,8 @@ __device__ __forceinline__ void out_scales(const GemmArgs &a, bool ok, int64_t r
     }
 }
 
-// A token's label row of the head and the remainder of its label's gradient, which is a row of dx's largest term: left
-// out, its rounding error would be common to the whole row.
+// The gradient of a token's label, which is in fp32 and no part of the 16-bit ones: it adds its multiple of the
+// label's row of the head to dx.
 struct LabelTerm {
     const uint16_t *w;                                // null: none
     float r;
@@ -468,12 +472,15 @@ __device__ __forceinline__ void epi_ce_t(const GemmArgs &a, float (&v)[CE_CHUNKS
 // The labels' logits in fp32 by the two warps that have no other work, a warp per token: products of
 // bf16 values are exact, so this is the fp32 rounding of a few additions per lane.  The tensor
 // cores' truncation shows most where the label dominates its row (2.5e-6 of the loss at 4096
-// columns without this); the other terms of the sum average it out.
-__device__ __forceinline__ void ce_labels(const GemmArgs &a, int64_t tokens, int first, int step) {
+// columns without this); the other terms of the sum average it out.  GRAD: the gradients of the labels' logits,
+// (exp(t - lse) - 1) * dloss, of the labels in this piece of n entries: for a confident token t is nearly lse, and
+// with a logit from the tensor cores 1 - p = 1e-4 came out 30% off.
+template <bool GRAD>
+__device__ __forceinline__ void ce_labels(const GemmArgs &a, int64_t tokens, int64_t n, int first, int step) {
     const int lane = threadIdx.x & 31;
     for (int64_t m = first; m < tokens; m += step) {
         const int64_t lab = __ldcg(a.labels + m);
-        if (lab < 0 || lab >= a.V) continue;
+        if (GRAD ? lab < a.v0 || lab >= a.v0 + n : lab < 0 || lab >= a.V) continue;
         const uint4 *x = reinterpret_cast<const uint4 *>(a.x + m * a.inner);
         const uint4 *w = reinterpret_cast<const uint4 *>(a.w + lab * a.inner);
         float s0 = 0.0f, s1 = 0.0f;
@@ -490,7 +497,12 @@ __device__ __forceinline__ void ce_labels(const GemmArgs &a, int64_t tokens, int
         float s = s0 + s1;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        if (lane == 0) a.tgt[m] = s;
+        if (lane == 0) {
+            if (GRAD)
+                a.res[m] = expm1f(s - __ldcg(a.lse + m)) * __ldcg(a.dloss + m);
+            else
+                a.tgt[m] = s;
+        }
     }
 }
 
@@ -512,10 +524,8 @@ __device__ __forceinline__ void epi_ce_bwd(const GemmArgs &a, uint32_t acc, int6
         const int64_t j = lab - a.v0 - n0 - c;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            float p = exp2f((__uint_as_float(r[k]) - lse) * LOG2E);
-            if (j == k) p -= 1.0f;
-            v[k] = scored ? p * w : 0.0f;
-            if (scored && j == k) a.res[row] = bf16_rest(v[k]);
+            const float p = exp2f((__uint_as_float(r[k]) - lse) * LOG2E);
+            v[k] = scored && j != k ? p * w : 0.0f;
         }
         // the row stride is a multiple of 64: the store may run into the row's own padding
         store_bf16_16(a.d16 + row * a.ldd + n0 + c, v, true, 16);
@@ -547,13 +557,10 @@ __device__ __forceinline__ void epi_ce_bwd_t(const GemmArgs &a, uint32_t acc, in
         for (int k = 0; k < 16; ++k) {
             const int lk = __shfl_sync(0xffffffffu, rel, k);
             const float sk = __shfl_sync(0xffffffffu, lse, k), wk = __shfl_sync(0xffffffffu, w, k);
-            float p = exp2f((__uint_as_float(r[k]) - sk) * LOG2E);
-            const bool label = lk == a.v0 + row;      // (lk = -1: not a row)
-            if (label) p -= 1.0f;
+            const float p = exp2f((__uint_as_float(r[k]) - sk) * LOG2E);
             if (row < a.M && c + k < a.N) {
-                const float d = lk >= 0 ? p * wk : 0.0f;
+                const float d = lk >= 0 && lk != a.v0 + row ? p * wk : 0.0f;
                 a.d16[(c + k) * a.ldd + row] = __bfloat16_as_ushort(__float2bfloat16_rn(d));
-                if (label) a.res[c + k] = bf16_rest(d);
                 if (a.lo) a.d16[(a.lo + c + k) * a.ldd + row] = __bfloat16_as_ushort(__float2bfloat16_rn(bf16_rest(d)));
             }
         }
@@ -721,7 +728,10 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
         }
     } else if (warp < GM_EPI_WARP0) {
         if constexpr (EPI == EPI_CE || EPI == EPI_CE_T)
-            ce_labels(a, EPI == EPI_CE ? a.M : a.N, static_cast<int>(blockIdx.x) * 2 + warp - 2, static_cast<int>(gridDim.x) * 2);
+            ce_labels<false>(a, EPI == EPI_CE ? a.M : a.N, 0, static_cast<int>(blockIdx.x) * 2 + warp - 2, static_cast<int>(gridDim.x) * 2);
+        if constexpr (EPI == EPI_CE_BWD || EPI == EPI_CE_BWD_T)
+            ce_labels<true>(a, EPI == EPI_CE_BWD ? a.M : a.N, EPI == EPI_CE_BWD ? a.N : a.M,
+                            static_cast<int>(blockIdx.x) * 2 + warp - 2, static_cast<int>(gridDim.x) * 2);
     } else {
         const int quad = warp & 3, par = (warp - GM_EPI_WARP0) >> 2;
         const uint32_t acc0 = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);

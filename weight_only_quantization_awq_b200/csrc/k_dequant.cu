@@ -256,15 +256,28 @@ __global__ void __launch_bounds__(256) dequant_kernel(const uint32_t *__restrict
     }
 }
 
-// out[m] = x[m] where the label is scored, zeros elsewhere, `copies` times over: an unscored row adds nothing to the
-// head's gradient, whatever (NaN, inf) its activations hold.
+// The operands of the head's gradient that the products before it do not need: out[m] = x[m] where the label is scored,
+// zeros elsewhere, `copies` times over (an unscored row adds nothing to the gradient, whatever (NaN, inf) its
+// activations hold); and the labels' own gradients res[m] as bf16 in their places in d, [token][ldd] of the
+// vocabulary's entries [v0, v0 + nv), with what the rounding takes off in row lo + m (lo: 0, none).
 __global__ void __launch_bounds__(256) scored_rows_kernel(const uint4 *__restrict__ x,
                                                           const int64_t *__restrict__ labels, int64_t V, int64_t n,
-                                                          int cpr, int copies, uint4 *__restrict__ out) {
+                                                          int cpr, int copies, uint4 *__restrict__ out, int64_t M,
+                                                          const float *res, uint16_t *d, int64_t ldd, int64_t v0,
+                                                          int64_t nv, int64_t lo) {
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x, i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    for (int64_t m = i0; m < M; m += step) {
+        const int64_t lab = __ldcg(labels + m);
+        if (lab < v0 || lab >= v0 + nv) continue;
+        const float g = __ldcg(res + m);
+        const __nv_bfloat16 h = __float2bfloat16_rn(g);
+        d[m * ldd + lab - v0] = __bfloat16_as_ushort(h);
+        if (lo) d[(lo + m) * ldd + lab - v0] = __bfloat16_as_ushort(__float2bfloat16_rn(g - __bfloat162float(h)));
+    }
+    if (copies == 0) return;
+    for (int64_t i = i0; i < n; i += step) {
         const int64_t lab = __ldcg(labels + i / cpr);
         const uint4 v = lab >= 0 && lab < V ? __ldcg(x + i) : make_uint4(0u, 0u, 0u, 0u);
         for (int k = 0; k < copies; ++k) out[k * n + i] = v;
@@ -274,11 +287,12 @@ __global__ void __launch_bounds__(256) scored_rows_kernel(const uint4 *__restric
 }  // namespace
 
 cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t V, int64_t M, int64_t I,
-                               int copies, uint16_t *out, int num_sms, cudaStream_t st) {
-    const int64_t n = M * (I / 8), blocks = (n + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
+                               int copies, uint16_t *out, const float *res, uint16_t *d, int64_t ldd, int64_t v0,
+                               int64_t nv, int64_t lo, int num_sms, cudaStream_t st) {
+    const int64_t n = M * (I / 8), blocks = ((copies ? n : M) + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
     return launch_after(scored_rows_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, st,
                         reinterpret_cast<const uint4 *>(x), labels, V, n, static_cast<int>(I / 8), copies,
-                        reinterpret_cast<uint4 *>(out));
+                        reinterpret_cast<uint4 *>(out), M, res, d, ldd, v0, nv, lo);
 }
 
 cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int64_t cols, int64_t ld,
