@@ -1,10 +1,12 @@
 """GPU checks of the digits that the gated, gradient and cross-entropy calls keep: the label's gradient of
-confident tokens.  Tolerances as in test_gpu_train."""
+confident tokens, and magnitudes at the ends of the formats.  Tolerances as in test_gpu_train and
+test_gpu_train_paths."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_train import F8, UBF, awq, within  # noqa: F401
+from test_gpu_train import F8, PATHS, UBF, awq, rand, within  # noqa: F401
+from test_gpu_train_paths import BF16_NORM, normwise
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +48,37 @@ def test_label_gradient_of_confident_tokens(awq, M, want_dw):  # noqa: F811
         u = UBF * UBF if M <= 128 else UBF
         e = ((et + u * d.abs())[:, None] * x.to(F8)).sum(0) + 2.0 ** -16 * ref.abs()
         within(dW[L], ref, e + UBF * (ref.abs() + e) + 1e-30, "dW[label]")
+
+
+def signed_gates(F, I, scale, seed):
+    """A packed layer (group 128) whose gate rows are positive (even f) or negative throughout."""
+    rng = np.random.default_rng([20261209, 42, seed])
+    code = rng.integers(0, 16, (2 * F, I))
+    code[:F] = np.where(np.arange(F)[:, None] % 2 == 0, 12, 4)
+    nib = np.zeros((2 * F, I // 8), np.uint32)
+    for k in range(8):
+        nib |= code[:, k::8].astype(np.uint32) << np.uint32(4 * k)
+    delta = (scale * np.exp(0.3 * rng.standard_normal((2 * F, I // 128)))).astype(np.float16)
+    D = (code - 8) * np.repeat(delta.astype(np.float64), 128, 1)
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    return (dev(nib.view(np.int32)), dev(delta), None, None), dev(D)
+
+
+@pytest.mark.parametrize("M", PATHS)
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_gates_far_from_zero(awq, M, act):  # noqa: F811
+    """Gates of +-2^70: the derivative is 1 or 0 (gelu_tanh's polynomial in g^2 leaves fp32's range on the way)."""
+    F, I = 72, 256
+    w, D = signed_gates(F, I, 0.01, M)
+    x = (rand(M, I, 43).float().abs() * 2.0 ** 68).to(torch.bfloat16)
+    dh = (rand(M, F, 44).float() * 2.0 ** -90).to(torch.bfloat16)
+    gu = x.to(F8) @ D.T
+    g, u, d = gu[:, :F], gu[:, F:], dh.to(F8)
+    assert (g.abs() > 2.0 ** 66).all()
+    on = (g > 0).to(F8)
+    dx = awq.awq_gated_w4a16_grad(dh, x, *w, act=act)
+    assert torch.isfinite(dx.float()).all()
+    normwise(dx, torch.cat((d * u * on, d * g * on), 1) @ D, BF16_NORM, "dx")
+    h = awq.awq_gated_w4a16(x, *w, act=act)
+    off = (g < 0)
+    assert (h[off] == 0).all()

@@ -67,7 +67,9 @@ __device__ __forceinline__ float act_both(float g, int act, float &d) {
     const float c = 0.7978845608028654f;
     // (1 + tanh v) / 2 = sig(2 v)
     const float s = act_sigmoid(2.0f * c * g * (1.0f + 0.044715f * g * g));
-    d = s + g * (2.0f * s * (1.0f - s)) * c * (1.0f + 3.0f * 0.044715f * g * g);
+    // s (1 - s) is 0 in fp32 from |g| = 16 on (exp(-300)), where g's powers, from 2^64 on infinite, would make it NaN
+    const float b = fminf(fmaxf(g, -16.0f), 16.0f);
+    d = s + b * (2.0f * s * (1.0f - s)) * c * (1.0f + 3.0f * 0.044715f * b * b);
     return g * s;
 }
 __device__ __forceinline__ float act_value(float g, int act) {
