@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_train import F8, PATHS, UBF, awq, rand, within  # noqa: F401
+from test_gpu_train import F8, PATHS, UBF, awq, dx_ref, packed, rand, within  # noqa: F401
 from test_gpu_train_paths import BF16_NORM, normwise
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +82,28 @@ def test_gates_far_from_zero(awq, M, act):  # noqa: F811
     h = awq.awq_gated_w4a16(x, *w, act=act)
     off = (g < 0)
     assert (h[off] == 0).all()
+
+
+@pytest.mark.parametrize("M", PATHS)
+def test_rows_near_the_end_of_the_range(awq, M):  # noqa: F811
+    """Rows of 2^112 through weights of 2^-12: results of 2^105, whatever the order of the power-of-two factors."""
+    O, I = 160, 256
+    w, D, s = packed(O, I, 128, True, True, 45, scale=2.0 ** -12)
+    dy = (rand(M, O, 46).float() * 2.0 ** 110).to(torch.bfloat16)
+    ref, tol = dx_ref(dy.to(F8), torch.zeros_like(dy, dtype=F8), D, s, O)
+    assert ref.abs().max() < 2.0 ** 126
+    dx = awq.awq_linear_w4a16_grad(dy, *w)
+    within(dx, ref, tol, "dx")
+    normwise(dx, ref, BF16_NORM, "dx")
+    F = 72
+    w, D = signed_gates(F, I, 2.0 ** -12, M)
+    x = (rand(M, I, 47).float().abs() * 2.0 ** 112).to(torch.bfloat16)
+    dh = (rand(M, F, 48).float() * 2.0 ** -100).to(torch.bfloat16)
+    gu = x.to(F8) @ D.T
+    g, u, d = gu[:, :F], gu[:, F:], dh.to(F8)
+    assert (g.abs() > 2.0 ** 100).all() and gu.abs().max() < 2.0 ** 126
+    on = (g > 0).to(F8)
+    dx = awq.awq_gated_w4a16_grad(dh, x, *w)
+    normwise(dx, torch.cat((d * u * on, d * g * on), 1) @ D, BF16_NORM, "gated dx")
+    h = awq.awq_gated_w4a16(x, *w)
+    assert (h[g < 0] == 0).all()

@@ -142,8 +142,9 @@ __device__ __forceinline__ void epi_gated(const GemmArgs &a, uint32_t acc, int64
         float h[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            // the two power-of-two factors one after the other: each is a normal float
-            const float gv = (__uint_as_float(g[k]) * sc) * sw, uv = (__uint_as_float(u[k]) * sc) * sw;
+            // the two power-of-two factors one after the other, each a normal float, the layer's first: it is
+            // between 2^-34 and 2^5 and takes no sum out of fp32's range, the token's may
+            const float gv = (__uint_as_float(g[k]) * sw) * sc, uv = (__uint_as_float(u[k]) * sw) * sc;
             h[k] = act_value(gv, a.act) * uv;
         }
         if (row < a.M && f0 + c < a.F) store_bf16_16(a.out + row * a.F + f0 + c, h, vec, a.F - f0 - c);
@@ -189,7 +190,7 @@ __device__ __forceinline__ void epi_gated_bwd(const GemmArgs &a, uint32_t acc, i
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int64_t f = f0 + c + k + j;
-                const float gv = (__uint_as_float(g[k + j]) * sc) * sw, uv = (__uint_as_float(u[k + j]) * sc) * sw;
+                const float gv = (__uint_as_float(g[k + j]) * sw) * sc, uv = (__uint_as_float(u[k + j]) * sw) * sc;
                 float da;
                 const float av = act_both(gv, a.act, da);
                 const float d = dv[k + j] * sd;
@@ -230,7 +231,7 @@ __device__ __forceinline__ void epi_part(const GemmArgs &a, uint32_t acc, int un
     }
 }
 
-// A row's scale, as two factors that are normal floats each.  (Warp-wide: the layer's exponent.)
+// A row's scale, as two factors that are normal floats each; sw, the layer's, is applied first (epi_gated).  (Warp-wide: the layer's exponent.)
 __device__ __forceinline__ void out_scales(const GemmArgs &a, bool ok, int64_t row, float &sc, float &sw) {
     sc = sw = 1.0f;
     if (a.grow) {                                     // gated gradient: 2^e of the token
@@ -325,7 +326,7 @@ __device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t
         if (ok && n0 + c < a.N) {                     // N is a multiple of 64: a 16-column chunk is in or out
             float v[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = (__uint_as_float(r[k]) * sc) * sw;
+            for (int k = 0; k < 16; ++k) v[k] = (__uint_as_float(r[k]) * sw) * sc;
             out_columns<16>(a, row, n0 + c, t, v);
         }
         __syncwarp();
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
             w[i] = i0 + AHEAD + i < a.splits ? slot(i0 + AHEAD + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = (v[k] * sc) * sw;
+    for (int k = 0; k < 4; ++k) v[k] = (v[k] * sw) * sc;
     out_columns<4>(a, row, n, t, v);
 }
 

@@ -137,7 +137,7 @@ __device__ __forceinline__ void sk_finish(const SkinnyArgs &a, int t, int m0, in
             for (int k = 0; k < K; ++k)
                 if (c + k < mcount)
                     a.out[(m0 + c + k) * a.I + col] =
-                        __bfloat16_as_ushort(__float2bfloat16_rn(__fdividef((v[k] * tsc[c + k]) * sw, s)));
+                        __bfloat16_as_ushort(__float2bfloat16_rn(__fdividef((v[k] * sw) * tsc[c + k], s)));
         }
         return;
     }
@@ -150,8 +150,9 @@ __device__ __forceinline__ void sk_finish(const SkinnyArgs &a, int t, int m0, in
         for (int k2 = 0; k2 < K / 2; ++k2) {
             const int k = (e >> 6) * (K / 2) + k2, m = c + k;
             if (m < mcount) {
-                const float gv = (x[k * 128 + (e & 63)] * tsc[m]) * sw;
-                const float uv = (x[k * 128 + 64 + (e & 63)] * tsc[m]) * sw;
+                // (the layer's factor first: it takes no sum out of fp32's range, the token's may)
+                const float gv = (x[k * 128 + (e & 63)] * sw) * tsc[m];
+                const float uv = (x[k * 128 + 64 + (e & 63)] * sw) * tsc[m];
                 if (EPI == EPI_GATED) {
                     a.out[(m0 + m) * a.F + f] = __bfloat16_as_ushort(__float2bfloat16_rn(act_value(gv, a.act) * uv));
                 } else {
