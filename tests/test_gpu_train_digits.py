@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_train import F8, PATHS, UBF, awq, dx_ref, packed, rand, within  # noqa: F401
+from test_gpu_train import F8, PATHS, UBF, awq, dx_ref, gated_ref, packed, rand, within  # noqa: F401
 from test_gpu_train_paths import BF16_NORM, normwise
 
 pytestmark = pytest.mark.gpu
@@ -107,3 +107,37 @@ def test_rows_near_the_end_of_the_range(awq, M):  # noqa: F811
     normwise(dx, torch.cat((d * u * on, d * g * on), 1) @ D, BF16_NORM, "gated dx")
     h = awq.awq_gated_w4a16(x, *w)
     assert (h[g < 0] == 0).all()
+
+
+@pytest.mark.parametrize("M", PATHS)
+@pytest.mark.parametrize("wscale,xscale,dscale", [(2.0 ** -12, 2.0 ** -40, 2.0 ** -60), (8.0, 2.0 ** 20, 2.0 ** 30),
+                                                  (0.01, 2.0 ** -100, 2.0 ** 60), (2.0 ** -12, 1.0, 2.0 ** -100)])
+def test_gated_grad_of_extreme_magnitudes(awq, M, wscale, xscale, dscale):  # noqa: F811
+    F, I = 160, 256
+    w, D, s = packed(2 * F, I, 128, True, True, 49, scale=wscale)
+    x = (rand(M, I, 50).float() * xscale).to(torch.bfloat16)
+    dh = (rand(M, F, 51).float() * dscale).to(torch.bfloat16)
+    _, _, (a, da, g, u, _, _, eg) = gated_ref(x, D, s, "silu")
+    d = dh.to(F8)
+    ref = (torch.cat((d * u * da, d * a), 1) @ D) / s
+    assert 2.0 ** -120 < float(ref.abs().amax()) < 2.0 ** 120
+    # g is off by at most eg and act' is between -0.1 and 1.1 with |act''| <= 1: act' is off by min(eg, 1.2), and only
+    # where |g| < eg + 40 (beyond, exp(-40) of a step).  Of large gates that is the whole step of the few near zero.
+    unsure = torch.where(g.abs() < eg + 40, eg.clamp(max=1.2), 0.0)
+    step = ((d * u).abs() * unsure) @ D[:F].abs() / s
+    normwise(awq.awq_gated_w4a16_grad(dh, x, *w), ref, BF16_NORM + float(step.norm() / ref.norm()), "dx")
+
+
+@pytest.mark.parametrize("M", PATHS)
+def test_gated_grad_beside_an_outlying_scale(awq, M):  # noqa: F811
+    """One group scale 2^12 above the others sets the exponents of the layer and of the token's gradients.  Its
+    row has no gradient here, so dx is made of the others alone, 2^12 further down in fp16's range."""
+    F, I = 160, 256
+    w, D, s = packed(2 * F, I, 128, True, True, 52)
+    w[1][7, 1] *= 2.0 ** 12
+    D[7, 128:] *= 2.0 ** 12
+    x, dh = rand(M, I, 53), rand(M, F, 54, 1e-3)
+    dh[:, 7] = 0
+    _, _, (a, da, _, u, _, _, _) = gated_ref(x, D, s, "silu")
+    d = dh.to(F8)
+    normwise(awq.awq_gated_w4a16_grad(dh, x, *w), (torch.cat((d * u * da, d * a), 1) @ D) / s, BF16_NORM, "dx")
