@@ -48,6 +48,7 @@ namespace awq {
 
 namespace {
 
+constexpr float SK_NAN = __builtin_nanf("");
 constexpr int SK_GROUPS = 3;                           // groups of eight dequantising warps
 constexpr int SK_DQ_WARPS = 8 * SK_GROUPS;
 constexpr int SK_WARP_EPI = SK_DQ_WARPS, SK_WARP_TMA = SK_DQ_WARPS + 4, SK_WARP_MMA = SK_DQ_WARPS + 5;   // four epilogue warps: TMEM lane quadrants 0-3
@@ -124,7 +125,8 @@ __device__ __forceinline__ SkPre<EPI, K> sk_pre(const SkinnyArgs &a, int t, int 
 }
 
 // The results of K tokens (the tile's tokens c .. c + K - 1) from the accumulator's 128 lanes, thread e
-// holding lane e's values.  tsc, tsd: the tile's token scales.  bar: hardware barrier of the 128 threads.
+// holding lane e's values.  sw: the layer's scale, NaN where the accumulator was never completed (a wait ran out), which
+// makes every result NaN.  tsc, tsd: the tile's token scales.  bar: hardware barrier of the 128 threads.
 // x: [K][128] floats of shared memory (gated products: lanes 64-127 hold the up values of lanes 0-63).
 template <int EPI, int K>
 __device__ __forceinline__ void sk_finish(const SkinnyArgs &a, int t, int m0, int mcount, int c, const float (&v)[K],
@@ -163,24 +165,6 @@ __device__ __forceinline__ void sk_finish(const SkinnyArgs &a, int t, int m0, in
                     dst[0] = __half_as_ushort(__float2half_rn((dv * uv) * da));
                     dst[a.F] = __half_as_ushort(__float2half_rn(dv * av));
                 }
-            }
-        }
-    }
-}
-
-// The same where the accumulator was never completed (a wait ran out): NaN for the tile's tokens c .. c + K - 1.
-template <int EPI, int K>
-__device__ __noinline__ void sk_give_up(const SkinnyArgs &a, int t, int m0, int mcount, int c, int e) {
-    const int64_t col = static_cast<int64_t>(t) * 128 + (e & ~7) + frag_perm8(e & 7), f = static_cast<int64_t>(t) * 64 + e;
-    for (int m = c; m < c + K && m < mcount; ++m) {
-        if (EPI == EPI_OUT) {
-            if (col < a.I) a.out[(m0 + m) * a.I + col] = 0x7FFF;
-        } else if (e < 64 && f < a.F) {
-            if (EPI == EPI_GATED) {
-                a.out[(m0 + m) * a.F + f] = 0x7FFF;
-            } else {
-                uint16_t *dst = a.d16 + (m0 + m) * a.ldd + f;
-                dst[0] = dst[a.F] = 0x7FFF;
             }
         }
     }
@@ -440,29 +424,27 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
             for (int i = 0; i < 2; ++i)
                 if (e + 128 * i < mcount) sk_token_scale<GRAD, EPI>(a, m0 + e + 128 * i, kw, sc[i], sd[i]);
             if (ok) ok = mbar_wait_warp(drain, 0, abort_flag);
-            if (named_bar_and(1 + set, 128, ok && !*abort_flag)) {
-                tc_fence_after();
-                float *xs = reinterpret_cast<float *>(ring + (set - 1) * SK_SET_BYTES), *ss = xs + 2 * 16 * 128;
-                for (int i = 0; i < 2; ++i) {
-                    ss[e + 128 * i] = sc[i];
-                    ss[256 + e + 128 * i] = sd[i];
-                }
-                named_bar_sync(1 + set, 128);
-                const uint32_t acc = tmem_base + (static_cast<uint32_t>(e & 96) << 16) +
-                                     (static_cast<uint32_t>(T - u0 / a.ks) & 1u) * a.acc_cols;
-                uint32_t flip = 0;
-                for (int c = 16 * set; c < a.n; c += 16 * SK_SETS, flip ^= 1u) {
-                    const SkPre<EPI, 16> pre = sk_pre<EPI, 16>(a, t, m0, mcount, c, e);
-                    uint32_t rv[16];
-                    tmem_ld16_wait(acc + c, rv);
-                    float v[16];
+            // (after a wait that ran out, NaN: whatever still lands in the ring, or is left in the accumulator)
+            const float sw = named_bar_and(1 + set, 128, ok && !*abort_flag) ? ldexpf(1.0f, kw) : SK_NAN;
+            tc_fence_after();
+            float *xs = reinterpret_cast<float *>(ring + (set - 1) * SK_SET_BYTES), *ss = xs + 2 * 16 * 128;
+            for (int i = 0; i < 2; ++i) {
+                ss[e + 128 * i] = sc[i];
+                ss[256 + e + 128 * i] = sd[i];
+            }
+            named_bar_sync(1 + set, 128);
+            const uint32_t acc = tmem_base + (static_cast<uint32_t>(e & 96) << 16) +
+                                 (static_cast<uint32_t>(T - u0 / a.ks) & 1u) * a.acc_cols;
+            uint32_t flip = 0;
+            for (int c = 16 * set; c < a.n; c += 16 * SK_SETS, flip ^= 1u) {
+                const SkPre<EPI, 16> pre = sk_pre<EPI, 16>(a, t, m0, mcount, c, e);
+                uint32_t rv[16];
+                tmem_ld16_wait(acc + c, rv);
+                float v[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(rv[k]);
-                    sk_finish<EPI, 16>(a, t, m0, mcount, c, v, pre, e, ldexpf(1.0f, kw), ss, ss + 256, xs + flip * (16 * 128), 1 + set);
-                    __syncwarp();
-                }
-            } else {
-                for (int c = 16 * set; c < a.n; c += 16 * SK_SETS) sk_give_up<EPI, 16>(a, t, m0, mcount, c, e);
+                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(rv[k]);
+                sk_finish<EPI, 16>(a, t, m0, mcount, c, v, pre, e, sw, ss, ss + 256, xs + flip * (16 * 128), 1 + set);
+                __syncwarp();
             }
         }
     } else if (warp == SK_WARP_TMA) {
@@ -542,7 +524,7 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
         const int e = threadIdx.x - SK_WARP_EPI * 32; // lane of the accumulator
         const uint32_t quad = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int kw = dq_exp(a.dmax);
-        const float sw = ldexpf(1.0f, kw);
+        float sw = ldexpf(1.0f, kw);
         uint32_t seg = 0, flip = 0;
         int have = -1;                                // token tile whose scales are in tsc
         bool ok = true;
@@ -560,19 +542,11 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
             }
             // (one outcome for the four warps: they meet at barriers below; no wait after one that ran out)
             if (ok) ok = named_bar_and(1, 128, mbar_wait_sleep(&acc_full[h], (seg >> 1) & 1u, abort_flag));
+            if (!ok) sw = SK_NAN;
             tc_fence_after();
             // a shared tile's partial sums: this CTA's slot [n / 4][128] of four tokens
             float4 *mine = a.part + static_cast<int64_t>(2 * blockIdx.x + (u0 > b0 ? 0 : 1)) * a.n * 32;
             for (int c = 0; c < a.n; c += WHOLE && end == u1 ? 16 * SK_SETS : 16) {
-                if (!ok) {
-                    if (whole) {
-                        sk_give_up<EPI, 16>(a, t, m0, mcount, c, e);
-                    } else {
-                        const float nan = __uint_as_float(0x7FFFFFFFu);
-                        for (int k = 0; k < 4; ++k) mine[(c / 4 + k) * 128 + e] = make_float4(nan, nan, nan, nan);
-                    }
-                    continue;
-                }
                 uint32_t rv[16];
                 tmem_ld16_wait(acc + c, rv);
                 float v[16];
@@ -584,7 +558,8 @@ __global__ void __launch_bounds__(SK_THREADS, 1)
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mine[(c / 4 + k) * 128 + e] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        mine[(c / 4 + k) * 128 + e] = ok ? make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3])
+                                                         : make_float4(SK_NAN, SK_NAN, SK_NAN, SK_NAN);
                 }
                 __syncwarp();
             }
