@@ -60,7 +60,13 @@ awq_status_t device_info(int *sms) {
         cudaMemPool_t pool;
         AWQ_CUDA(cudaDeviceGetDefaultMemPool(&pool, dev));
         uint64_t thr = UINT64_MAX;
-        AWQ_CUDA(cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &thr));
+        // The process's first call may be one that is captured into a graph: nothing here touches a stream, so
+        // the thread's capture mode is relaxed meanwhile.
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        AWQ_CUDA(cudaThreadExchangeStreamCaptureMode(&mode));
+        const cudaError_t e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &thr);
+        AWQ_CUDA(cudaThreadExchangeStreamCaptureMode(&mode));
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMemPoolSetAttribute");
         d.ready = true;
     }
     *sms = d.sms;
