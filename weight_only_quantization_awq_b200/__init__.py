@@ -20,6 +20,8 @@ names:
     awq_fold_scale(P, s16)                   -> P / s per row (1/s folded into the previous op)
     awq_wait_selftest(limit, arrive)         -> status of one bounded in-kernel wait
 
+Results carry no autograd graph: the gradients are calls of their own.
+
 Importing raises ImportError when the compiled library is missing; there is no
 fallback implementation.
 """

@@ -10,10 +10,11 @@
 // rows.  Read K-major, they are 128 rows of A and two 64-deep slabs of K; read MN-major, 128 columns
 // of A^T and eight 16-deep steps of K.  Nothing but the descriptors differs.
 //
-// Bound: the dequantising warps.  A 128 x 128 stage takes its CTA about 1300 cycles, in which they issue half
-// of the time (integer pipe 51%, shared-memory pipe 47%, tensor pipe 23% at 77 tokens); the packed weights need a third of
-// that from HBM.  Measured: 22016 x 4096, 77 tokens 41 us a call (33 this kernel, 4 the second one, 3 the tokens'
-// rows), 11008 -> 4096 gradient, 19 tokens 25 us.
+// Bound: the dequantising warps' stages, 13 instructions a packed word and about 1300 cycles for 128 x 128.  No pipe
+// is saturated (issue 54%, integer pipe 51%, shared-memory pipe 47%, tensor pipe 23% at 77 tokens): the warps wait for
+// their codes, first of all, and for one another.  The packed weights need a third of that time from HBM.
+// Measured: 22016 x 4096, 77 tokens 41 us a call (33 this kernel, 4 the second one, 3 the tokens' rows); 11008 <- 4096
+// gradient, 19 tokens 25 us, of which 19 stages a CTA are 13.
 //
 // Roles: 24 warps dequantise, in three groups that take the stages in turn, so that one group computes
 // while another stores (a thread: 32 columns of two rows, two 16-byte loads of codes fetched SK_PF
