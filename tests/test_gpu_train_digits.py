@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_train import F8, PATHS, UBF, awq, dx_ref, gated_ref, packed, rand, within  # noqa: F401
+from test_gpu_train import F8, PATHS, UBF, awq, ce_case, dx_ref, gated_ref, packed, rand, within  # noqa: F401
 from test_gpu_train_paths import BF16_NORM, normwise
 
 pytestmark = pytest.mark.gpu
@@ -141,3 +141,21 @@ def test_gated_grad_beside_an_outlying_scale(awq, M):  # noqa: F811
     _, _, (a, da, _, u, _, _, _) = gated_ref(x, D, s, "silu")
     d = dh.to(F8)
     normwise(awq.awq_gated_w4a16_grad(dh, x, *w), (torch.cat((d * u * da, d * a), 1) @ D) / s, BF16_NORM, "dx")
+
+
+@pytest.mark.parametrize("M", [5, 100, 300])
+def test_infinite_gradients_stay_infinite(awq, M):  # noqa: F811
+    """dloss of one token infinite: the row of its label is -inf as the formula's is, not NaN from the remainder of a
+    rounding, and no other token has a part in it."""
+    x, W, labels = ce_case(M, 500, 64, M)
+    labels[:] = torch.arange(M, device="cuda")
+    x[2], W[2] = 0.125, 0.125                        # a logit of 1
+    W[3:] = 0.0
+    W[:2] = 0.0
+    _, lse = awq.awq_cross_entropy(x, W, labels)
+    dloss = torch.zeros(M, device="cuda")
+    dloss[2] = float("inf")
+    dx, dW = awq.awq_cross_entropy_grad(x, W, labels, lse, dloss)
+    assert (dW[2].float() == float("-inf")).all()
+    keep = torch.arange(M, device="cuda") != 2
+    assert (dx[keep] == 0).all()

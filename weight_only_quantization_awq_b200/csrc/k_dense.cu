@@ -507,9 +507,6 @@ __device__ __forceinline__ void ce_labels(const GemmArgs &a, int64_t tokens, int
     }
 }
 
-// What rounding to bf16 takes off v (exact).
-__device__ __forceinline__ float bf16_rest(float v) { return v - __bfloat162float(__float2bfloat16_rn(v)); }
-
 __device__ __forceinline__ void epi_ce_bwd(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int par, bool done) {
     const bool ok = row < a.M;
     const int64_t lab = ok ? __ldcg(a.labels + row) : -1;

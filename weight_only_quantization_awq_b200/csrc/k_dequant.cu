@@ -272,9 +272,8 @@ __global__ void __launch_bounds__(256) scored_rows_kernel(const uint4 *__restric
         const int64_t lab = __ldcg(labels + m);
         if (lab < v0 || lab >= v0 + nv) continue;
         const float g = __ldcg(res + m);
-        const __nv_bfloat16 h = __float2bfloat16_rn(g);
-        d[m * ldd + lab - v0] = __bfloat16_as_ushort(h);
-        if (lo) d[(lo + m) * ldd + lab - v0] = __bfloat16_as_ushort(__float2bfloat16_rn(g - __bfloat162float(h)));
+        d[m * ldd + lab - v0] = __bfloat16_as_ushort(__float2bfloat16_rn(g));
+        if (lo) d[(lo + m) * ldd + lab - v0] = __bfloat16_as_ushort(__float2bfloat16_rn(bf16_rest(g)));
     }
     if (copies == 0) return;
     for (int64_t i = i0; i < n; i += step) {

@@ -2,6 +2,7 @@
 // share between their kernels.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "awq_internal.h"
@@ -42,6 +43,13 @@ __device__ __forceinline__ int dgu_exp(int grow, int inner, int kw) {
     frexpf(sqrtf(static_cast<float>(inner)) * 1.2f, &r);
     const int k = grow + r + (kw + 15) - 15;           // 15 max |Delta| < 2^(kW + 15)
     return k < -125 ? -125 : (k > 125 ? 125 : k);
+}
+
+// What rounding to bf16 takes off v (exact; 0 where v or its rounding is not finite, so that an infinite gradient stays
+// infinite).
+__device__ __forceinline__ float bf16_rest(float v) {
+    const float r = v - __bfloat162float(__float2bfloat16_rn(v));
+    return fabsf(r) < INFINITY ? r : 0.0f;
 }
 
 // (2 ulp; exp(-g) = inf below about -88 gives 0)
