@@ -354,8 +354,8 @@ awq_status_t awq_cross_entropy(const uint16_t *x, int64_t M, int64_t in, const u
  * written;  dW : [V, in] bf16, written, or NULL when the head is frozen.  d is computed
  * in pieces of the vocabulary and rounded to bf16, except for the label's entry in dx:
  * that is exp(t - lse) - 1 of the label's logit t in fp32, and stays fp32.  dW takes it
- * rounded to bf16; for M <= 128 it takes the remainders of all of d, too.  The pieces of
- * dx meet in fp32.
+ * rounded to bf16 with the remainder added in fp32 for the first token of each label; for
+ * M <= 128 it takes the remainders of all of d instead.  The pieces of dx meet in fp32.
  * Rows of x that are not scored add nothing to dW whatever they hold.  dx and dW must not
  * overlap any input or each other.  Asynchronous.
  */

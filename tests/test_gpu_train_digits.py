@@ -143,6 +143,32 @@ def test_gated_grad_beside_an_outlying_scale(awq, M):  # noqa: F811
     normwise(awq.awq_gated_w4a16_grad(dh, x, *w), (torch.cat((d * u * da, d * a), 1) @ D) / s, BF16_NORM, "dx")
 
 
+@pytest.mark.parametrize("M,V,I", [(129, 20001, 256), (700, 33000, 512), (2048, 40000, 128), (5000, 9001, 64)])
+def test_head_gradient_of_single_labels(awq, M, V, I):  # noqa: F811
+    """A row of dW that one token labels is that token's x times (p - 1) dloss, and little else: with the 16-bit rounding
+    of that factor beside its own it is off by sqrt(2) x 1.7e-3 in the root mean square, with the factor exact by
+    1.7e-3 (test_gpu_train_paths).  Half of the tokens are alone with their label here, the other half share 7 labels."""
+    x, W, labels = ce_case(M, V, I, M + I)
+    order = torch.from_numpy(np.random.default_rng([20261209, 55, M]).permutation(V)[:M]).cuda()
+    labels[:] = order
+    labels[1::2] = torch.arange(M // 2, device="cuda") % 7
+    single = order[::2][order[::2] >= 7]
+    labels[0] = -100
+    single = single[single != order[0]]
+    _, lse = awq.awq_cross_entropy(x, W, labels)
+    dloss = torch.from_numpy((np.random.default_rng([20261209, 56, M]).random(M) + 0.5).astype(np.float32)).cuda()
+    dx, dW = awq.awq_cross_entropy_grad(x, W, labels, lse, dloss)
+    x8 = x.to(F8)
+    d = torch.exp(x8 @ W.to(F8).T - lse.to(F8)[:, None])
+    scored = labels >= 0
+    d[scored, labels[scored]] -= 1.0
+    d *= torch.where(scored, dloss.to(F8), 0.0)[:, None]
+    dW_r = d.T @ x8
+    normwise(dW[single], dW_r[single], 2e-3, "rows of one token")
+    normwise(dW, dW_r, BF16_NORM, "dW")
+    normwise(dx, d @ W.to(F8), BF16_NORM, "dx")
+
+
 @pytest.mark.parametrize("M", [5, 100, 300])
 def test_infinite_gradients_stay_infinite(awq, M):  # noqa: F811
     """dloss of one token infinite: the row of its label is -inf as the formula's is, not NaN from the remainder of a

@@ -22,7 +22,7 @@ KERNELS = [
     ("k_dequant.cu", "rows16_kernel", ["x", "r", "dh", "dr"]),
     ("k_dequant.cu", "dequant_kernel", ["dmax"]),
     ("k_dequant.cu", "scored_rows_kernel", ["x", "labels", "res"]),
-    ("k_dense.cu", "gemm16_kernel", ["a.sx", "a.dmax", "a.grow", "a.dh", "a.labels", "a.lse", "a.dloss", "a.x", "a.res"]),
+    ("k_dense.cu", "gemm16_kernel", ["a.sx", "a.dmax", "a.grow", "a.dh", "a.labels", "a.lse", "a.dloss", "a.x", "a.res", "a.owner"]),
     ("k_dense.cu", "gemm_finish_kernel", ["a.part4", "a.sx", "a.dmax", "a.grow", "a.res", "p"]),
     ("k_dense.cu", "ce_final_kernel", ["part", "labels", "tgt"]),
     ("k_skinny.cu", "skinny_kernel", ["a.sx", "a.dmax", "a.grow", "a.dh"]),

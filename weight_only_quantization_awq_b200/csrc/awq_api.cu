@@ -1155,6 +1155,8 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
     size_t bytes = Workspace::up(2 * dr * ldd) + Workspace::up(4 * M);
     if (pieces > 1) bytes += Workspace::up(4 * M * in);
     if (dW) bytes += Workspace::up(2 * dr * in);
+    const bool owners = dW && M > awq::CE_LO_MAX_M;       // (then M is above CE_BWD_T_MAX_M, too)
+    if (owners) bytes += Workspace::up(4 * ldd);
     const awq::GemmPlan gp = awq::gemm_plan(M, in, vc < V ? vc : V, sms);   // dx: K is the piece's entries
     const int64_t parts = gp.part_vecs;
     const bool few = M <= awq::CE_BWD_T_MAX_M;            // the vocabulary on the rows, the tokens on the columns
@@ -1165,6 +1167,7 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
     float4 *part4 = parts ? ws.take<float4>(parts) : nullptr;
     float *acc = pieces > 1 ? ws.take<float>(M * in) : nullptr;
     uint16_t *xz = dW ? ws.take<uint16_t>(dr * in) : nullptr;
+    int *owner = owners ? ws.take<int>(ldd) : nullptr;
     kt_reset(4);
     kt_begin(4, st);
     for (int64_t v0 = 0; v0 < V; v0 += vc) {
@@ -1190,6 +1193,7 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
         a.x = x;
         a.w = W;
         a.inner = static_cast<int>(in);
+        a.owner = owner;
         a.lo = dr - M;
         if (awq_status_t s = map_kmajor(&maps.a, true, few ? Wp : x, in, a.M, in, 128)) return s;
         if (awq_status_t s = map_kmajor(&maps.b, true, few ? x : Wp, in, a.N, in, a.bn / 2)) return s;
@@ -1219,7 +1223,7 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
         if (dW) {
             // (behind the product with the head: its label terms are added in fp32)
             AWQ_CUDA(awq::launch_scored_rows(x, labels, V, M, in, v0 == 0 ? static_cast<int>(dr / M) : 0, xz, res, d16, ldd,
-                                             v0, n, dr - M, sms, st));
+                                             v0, n, dr - M, owner, sms, st));
             awq::GemmArgs c{};
             c.splits = 1;
             c.M = n;
@@ -1229,6 +1233,9 @@ awq_status_t awq_cross_entropy_grad(const uint16_t *x, int64_t M, int64_t in, co
             c.nt = ceil_div(in, c.bn);
             c.nk[0] = ceil_div(dr, 64);
             c.out = dW + v0 * in;
+            c.owner = owner;
+            c.res = res;
+            c.x = x;
             if (awq_status_t s = map_mnmajor(&maps.a, true, d16, n, dr, ldd)) return s;
             if (awq_status_t s = map_mnmajor(&maps.b, true, xz, in, dr, in)) return s;
             AWQ_CUDA(awq::launch_gemm16(awq::EPI_OUT, true, true, maps, c, sms, st));

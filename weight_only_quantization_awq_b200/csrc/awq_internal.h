@@ -213,9 +213,12 @@ constexpr int64_t CE_T_MAX_M = 128;
 constexpr int64_t CE_BWD_T_MAX_M = 64;
 // Tokens up to which the head's gradient takes the remainders of the rounded gradients, too (twice the K, which the
 // writing of dW hides).  A label's rounding error, up to 2^-8 of its gradient, is common to all elements of that token's
-// part of a head row.  Above, a row that one token labels carries it beside the rounding of the result: of 2048
-// tokens and 32000 entries most rows with a label have one, and dW is off by 2.4e-3 in the norm instead of 1.7e-3.
+// part of a head row.  Above, where twice the K would cost twice the time, the remainder of the first token of each label
+// is added in fp32 (GemmArgs::owner): of 2048 tokens and 32000 entries most rows with a label have one, and without
+// it dW was off by 2.35e-3 in the norm instead of 1.7e-3.  A row of many tokens keeps the roundings of the others.
 constexpr int64_t CE_LO_MAX_M = 128;
+constexpr int CE_NO_TOKEN = 0x7FFFFFFF;
+static_assert(CE_LO_MAX_M >= CE_BWD_T_MAX_M, "owners go with EPI_CE_BWD");
 struct GemmMaps {
     CUtensorMap a, b;           // K-major: box 64 k x 128 rows (b: bn / 2 rows); MN-major: box 64 x 64
 };
@@ -245,6 +248,8 @@ struct GemmArgs {
     const uint16_t *x, *w;      // the operands themselves, rows of `inner` columns (the labels' logits); EPI_OUT: w, rows of N
     float *res;                 // [M] the gradient of the label's logit, whose place in d16 EPI_CE_BWD* leave zero: they
                                 // write it, EPI_OUT adds res[m] w[labels[m]] to row m (null: does not)
+    int *owner;                 // [N of the piece] the first token of each label, CE_NO_TOKEN: none.  EPI_CE_BWD clears it;
+                                // EPI_OUT adds the remainder of res[owner[n]] times that token's row of x to row n
     int64_t lo;                 // EPI_CE_BWD*: rows of d16 from a token's to its row of rounding remainders (0: none)
     // outputs
     uint16_t *out;              // bf16
@@ -275,7 +280,7 @@ cudaError_t launch_dequant(const uint32_t *q, const uint16_t *scales, const uint
                            int gs, const unsigned *dmax, uint16_t *out, cudaStream_t st);
 cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t V, int64_t M, int64_t I,
                                int copies, uint16_t *out, const float *res, uint16_t *d, int64_t ldd, int64_t v0,
-                               int64_t nv, int64_t lo, int num_sms, cudaStream_t st);
+                               int64_t nv, int64_t lo, int *owner, int num_sms, cudaStream_t st);
 
 // ---- products with a packed matrix for up to a few hundred tokens, dequantised on the way into
 // the tensor cores (k_skinny.cu): forward EPI_GATED / EPI_GATED_BWD (64 gate and 64 up rows per tile, K

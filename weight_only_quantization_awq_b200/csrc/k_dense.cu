@@ -250,9 +250,17 @@ struct LabelTerm {
     const uint16_t *w;                                // null: none
     float r;
 };
+// (The head's gradient, a.owner: a row is an entry of the vocabulary, and what rounding took off the gradient of the
+// first token that it labels adds its multiple of the token's row of x.)
 __device__ __forceinline__ LabelTerm label_term(const GemmArgs &a, bool ok, int64_t row) {
     LabelTerm t = {nullptr, 0.0f};
-    if (a.res && a.last && ok) {
+    if (a.owner) {
+        const int m = ok ? __ldcg(a.owner + row) : CE_NO_TOKEN;
+        if (m != CE_NO_TOKEN) {
+            t.w = a.x + m * a.N;
+            t.r = bf16_rest(__ldcg(a.res + m));
+        }
+    } else if (a.res && a.last && ok) {
         const int64_t lab = __ldcg(a.labels + row);
         if (lab >= 0 && lab < a.V) {
             t.w = a.w + lab * a.N;
@@ -262,9 +270,19 @@ __device__ __forceinline__ LabelTerm label_term(const GemmArgs &a, bool ok, int6
     return t;
 }
 
-// C consecutive scaled columns n .. of a row: divided by s, added to the pieces before, stored.
+// C columns n .. of the row that a label term adds.
 template <int C>
-__device__ __forceinline__ void out_columns(const GemmArgs &a, int64_t row, int64_t n, const LabelTerm &t, float (&v)[C]) {
+__device__ __forceinline__ void label_columns(const LabelTerm &t, int64_t n, uint2 (&w)[C / 4]) {
+    const bool any = t.w && t.r != 0.0f;
+#pragma unroll
+    for (int k = 0; k < C / 4; ++k)
+        w[k] = any ? __ldcg(reinterpret_cast<const uint2 *>(t.w + n) + k) : make_uint2(0u, 0u);
+}
+
+// C consecutive scaled columns n .. of a row: divided by s, added to the pieces before, with the label's term, stored.
+template <int C>
+__device__ __forceinline__ void out_columns(const GemmArgs &a, int64_t row, int64_t n, const LabelTerm &t,
+                                            const uint2 (&lw)[C / 4], float (&v)[C]) {
     if (a.s16) {
 #pragma unroll
         for (int k = 0; k < C; k += 4) {
@@ -294,7 +312,7 @@ __device__ __forceinline__ void out_columns(const GemmArgs &a, int64_t row, int6
     if (t.w && t.r != 0.0f) {
 #pragma unroll
         for (int k = 0; k < C; k += 4) {
-            const uint2 w = __ldcg(reinterpret_cast<const uint2 *>(t.w + n + k));
+            const uint2 w = lw[k / 4];
             v[k] = fmaf(t.r, __uint_as_float(w.x << 16), v[k]);
             v[k + 1] = fmaf(t.r, __uint_as_float(w.x & 0xFFFF0000u), v[k + 1]);
             v[k + 2] = fmaf(t.r, __uint_as_float(w.y << 16), v[k + 2]);
@@ -313,21 +331,22 @@ __device__ __forceinline__ void out_columns(const GemmArgs &a, int64_t row, int6
     }
 }
 
-__device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int par, bool done) {
+// (sc, sw, t: the row's, read before the accumulator is waited for)
+__device__ __forceinline__ void epi_out(const GemmArgs &a, uint32_t acc, int64_t row, int64_t n0, int par, float sc,
+                                        float sw, const LabelTerm &t) {
     const bool ok = row < a.M;
-    float sc, sw;
-    out_scales(a, ok, row, sc, sw);
-    if (!done) sc = GM_NAN;
-    const LabelTerm t = label_term(a, ok, row);
 #pragma unroll 1
     for (int c = 16 * par; c < a.bn; c += 32) {
+        const bool in = ok && n0 + c < a.N;           // N is a multiple of 64: a 16-column chunk is in or out
+        uint2 lw[4];
+        label_columns<16>(in ? t : LabelTerm{nullptr, 0.0f}, n0 + c, lw);
         uint32_t r[16];
         tmem_ld16_wait(acc + c, r);
-        if (ok && n0 + c < a.N) {                     // N is a multiple of 64: a 16-column chunk is in or out
+        if (in) {
             float v[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = (__uint_as_float(r[k]) * sw) * sc;
-            out_columns<16>(a, row, n0 + c, t, v);
+            out_columns<16>(a, row, n0 + c, t, lw, v);
         }
         __syncwarp();
     }
@@ -367,7 +386,9 @@ __global__ void __launch_bounds__(256) gemm_finish_kernel(const __grid_constant_
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = (v[k] * sw) * sc;
-    out_columns<4>(a, row, n, t, v);
+    uint2 lw[1];
+    label_columns<4>(t, n, lw);
+    out_columns<4>(a, row, n, t, lw, v);
 }
 
 constexpr float LOG2E = 1.4426950408889634f;
@@ -727,6 +748,9 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
     } else if (warp < GM_EPI_WARP0) {
         if constexpr (EPI == EPI_CE || EPI == EPI_CE_T)
             ce_labels<false>(a, EPI == EPI_CE ? a.M : a.N, 0, static_cast<int>(blockIdx.x) * 2 + warp - 2, static_cast<int>(gridDim.x) * 2);
+        if (EPI == EPI_CE_BWD && a.owner)
+            for (int64_t v = (static_cast<int64_t>(blockIdx.x) * 2 + warp - 2) * 32 + lane; v < a.N; v += static_cast<int64_t>(gridDim.x) * 64)
+                a.owner[v] = CE_NO_TOKEN;
         if constexpr (EPI == EPI_CE_BWD || EPI == EPI_CE_BWD_T)
             ce_labels<true>(a, EPI == EPI_CE_BWD ? a.M : a.N, EPI == EPI_CE_BWD ? a.N : a.M,
                             static_cast<int>(blockIdx.x) * 2 + warp - 2, static_cast<int>(gridDim.x) * 2);
@@ -771,7 +795,14 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
                 __syncwarp();
                 continue;
             }
-            await();
+            float sc = 1.0f, sw = 1.0f;
+            LabelTerm lt = {nullptr, 0.0f};
+            if constexpr (EPI == EPI_OUT)
+                if (a.splits == 1) {
+                    out_scales(a, row < a.M, row, sc, sw);
+                    lt = label_term(a, row < a.M, row);
+                }
+            if (!await()) sc = GM_NAN;
             const uint32_t acc = acc0 + (ti & 1u) * 256;
             if constexpr (EPI == EPI_GATED) epi_gated(a, acc, row, static_cast<int64_t>(tl.n) * bh, par, ok);
             if constexpr (EPI == EPI_GATED_BWD) epi_gated_bwd(a, acc, row, static_cast<int64_t>(tl.n) * bh, par, ok);
@@ -779,7 +810,7 @@ __global__ void __launch_bounds__(GM_THREADS<EPI>, 1)
                 if (a.splits > 1)
                     epi_part(a, acc, t, static_cast<int>(rank) * 128 + quad * 32 + lane, par, ok);
                 else
-                    epi_out(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par, ok);
+                    epi_out(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par, sc, sw, lt);
             }
             if constexpr (EPI == EPI_CE_BWD_T) epi_ce_bwd_t(a, acc, row, par, ok);
             if constexpr (EPI == EPI_CE_BWD) epi_ce_bwd(a, acc, row, static_cast<int64_t>(tl.n) * a.bn, par, ok);

@@ -259,12 +259,13 @@ __global__ void __launch_bounds__(256) dequant_kernel(const uint32_t *__restrict
 // The operands of the head's gradient that the products before it do not need: out[m] = x[m] where the label is scored,
 // zeros elsewhere, `copies` times over (an unscored row adds nothing to the gradient, whatever (NaN, inf) its
 // activations hold); and the labels' own gradients res[m] as bf16 in their places in d, [token][ldd] of the
-// vocabulary's entries [v0, v0 + nv), with what the rounding takes off in row lo + m (lo: 0, none).
+// vocabulary's entries [v0, v0 + nv), with what the rounding takes off in row lo + m (lo: 0, none), and with the first
+// token of each label in owner (null: not), all CE_NO_TOKEN before.
 __global__ void __launch_bounds__(256) scored_rows_kernel(const uint4 *__restrict__ x,
                                                           const int64_t *__restrict__ labels, int64_t V, int64_t n,
                                                           int cpr, int copies, uint4 *__restrict__ out, int64_t M,
                                                           const float *res, uint16_t *d, int64_t ldd, int64_t v0,
-                                                          int64_t nv, int64_t lo) {
+                                                          int64_t nv, int64_t lo, int *owner) {
     griddep_wait();
     griddep_launch_dependents();
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x, i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -273,6 +274,7 @@ __global__ void __launch_bounds__(256) scored_rows_kernel(const uint4 *__restric
         if (lab < v0 || lab >= v0 + nv) continue;
         const float g = __ldcg(res + m);
         d[m * ldd + lab - v0] = __bfloat16_as_ushort(__float2bfloat16_rn(g));
+        if (owner) atomicMin(owner + lab - v0, static_cast<int>(m));     // (the same whatever the order)
         if (lo) d[(lo + m) * ldd + lab - v0] = __bfloat16_as_ushort(__float2bfloat16_rn(bf16_rest(g)));
     }
     if (copies == 0) return;
@@ -287,11 +289,11 @@ __global__ void __launch_bounds__(256) scored_rows_kernel(const uint4 *__restric
 
 cudaError_t launch_scored_rows(const uint16_t *x, const int64_t *labels, int64_t V, int64_t M, int64_t I,
                                int copies, uint16_t *out, const float *res, uint16_t *d, int64_t ldd, int64_t v0,
-                               int64_t nv, int64_t lo, int num_sms, cudaStream_t st) {
+                               int64_t nv, int64_t lo, int *owner, int num_sms, cudaStream_t st) {
     const int64_t n = M * (I / 8), blocks = ((copies ? n : M) + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
     return launch_after(scored_rows_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), 256, st,
                         reinterpret_cast<const uint4 *>(x), labels, V, n, static_cast<int>(I / 8), copies,
-                        reinterpret_cast<uint4 *>(out), M, res, d, ldd, v0, nv, lo);
+                        reinterpret_cast<uint4 *>(out), M, res, d, ldd, v0, nv, lo, owner);
 }
 
 cudaError_t launch_rows16(const uint16_t *x, const uint16_t *s16, int64_t M, int64_t cols, int64_t ld,
